@@ -407,6 +407,103 @@ vscan_status vscan_backward(const vscan_route* route, const vscan_args* args, co
  */
 vscan_status vscan_status_from_device_word(int32_t word);
 
+/*
+ * ---- Gated delta rule -------------------------------------------------------
+ *
+ * A token mixer with a matrix state S [dim_k][dim_v] per value head, run in the
+ * order of one direction of a route (or over plain or packed sequences) next to
+ * the diagonal scan above (an addition of this library; the pages have no
+ * counterpart):
+ *
+ *   g_t    = A_h * softplus(a_t + bias_h)                 log decay
+ *   beta_t = beta_scale / (1 + exp(-b_t))                 write strength
+ *   S_t    = e^{g_t} S_{t-1} + beta_t k_t (v_t - e^{g_t} S_{t-1}^T k_t)^T
+ *   y_t    = scale * S_t^T q_t
+ *
+ * q and k have heads_k heads, each shared by heads_v / heads_k consecutive value
+ * heads. Keys of length at most 1 (vscan_qknorm_forward with VSCAN_NORM_L2) and
+ * beta <= 1 keep the update contractive. States are float32; the products run on
+ * bf16 tensor cores with every float32 operand split into three bf16 terms, so
+ * states and float32 results keep float32 accuracy. Values must be finite: a
+ * non-finite value in one token can reach other tokens of its chunk of 64 steps.
+ */
+typedef struct vscan_delta_args {
+    int32_t batch;       /* images, >= 0; with seq_offsets: packed sequences         */
+    int32_t tokens;      /* rows per image (the route's count when one is given),
+                            >= 0; with seq_offsets: rows of the packed arrays; 1 for
+                            vscan_delta_step                                         */
+    int32_t heads_k;     /* heads of q and k                                         */
+    int32_t heads_v;     /* heads of v, y, a, b and the state: a multiple of heads_k */
+    int32_t dim_k;       /* width of a q or k head: <= 128, a multiple of 4 (f32) or
+                            8 (bf16)                                                 */
+    int32_t dim_v;       /* width of a v or y head: <= 256, the same multiple        */
+    int32_t dtype;       /* vscan_dtype of q, k, v, a, b and y                       */
+    int32_t direction;   /* direction of the route, 0 .. K - 1; 0 without a route    */
+    const void* q;       /* device, [batch][tokens][heads_k][dim_k], 16-byte aligned */
+    const void* k;       /* device, [batch][tokens][heads_k][dim_k], 16-byte aligned */
+    const void* v;       /* device, [batch][tokens][heads_v][dim_v], 16-byte aligned */
+    const void* a;       /* device, [batch][tokens][heads_v], raw decay step         */
+    const void* b;       /* device, [batch][tokens][heads_v], raw write strength     */
+    void* y;             /* device, [batch][tokens][heads_v][dim_v], 16-byte aligned;
+                            written (not accumulated); no overlap with the inputs    */
+    const float* A;      /* device, [heads_v] (negative for decay)                   */
+    const float* bias;   /* device, [heads_v], or NULL for no bias                   */
+    const float* initial_state; /* device, [batch][heads_v][dim_k][dim_v], 16-byte
+                            aligned, or NULL for zero                                */
+    float* final_state;  /* device, the same shape, or NULL; may be initial_state    */
+    const int32_t* seq_offsets; /* device, [batch + 1], non-decreasing, or NULL. The
+                            token arrays then hold the packed rows of `batch`
+                            sequences ([tokens][..], batch strides unused) and
+                            sequence i is rows seq_offsets[i] .. seq_offsets[i+1]-1,
+                            possibly none. Values are clamped into 0 .. tokens; rows
+                            outside every sequence are neither read nor written. Not
+                            together with a route.                                   */
+    float scale;         /* output scale                                             */
+    float beta_scale;    /* write-strength scale (1 for beta in 0 .. 1)              */
+    /* Strides in elements (0 = dense): token t of image b at b * batch stride +
+     * t * token stride; the heads of one token are contiguous. Of q, k, v and y
+     * multiples of 4 (f32) or 8 (bf16), and token strides at least one token's
+     * width; a and b may have any positive ones.                                 */
+    int64_t q_tok_stride, q_batch_stride;
+    int64_t k_tok_stride, k_batch_stride;
+    int64_t v_tok_stride, v_batch_stride;
+    int64_t a_tok_stride, a_batch_stride;
+    int64_t b_tok_stride, b_batch_stride;
+    int64_t y_tok_stride, y_batch_stride;
+    void* workspace;     /* device scratch, 16-byte aligned                          */
+    uint64_t workspace_bytes;
+} vscan_delta_args;
+
+/*
+ * Device scratch bytes vscan_delta_forward needs (host only): for every chunk of
+ * 64 steps and value head the triangular inverse, the masked q k^T product and
+ * the decays (about 41 KiB in bf16, 49 KiB in float32). Packed sequences count
+ * tokens / 64 + batch + 1 chunks whatever their lengths.
+ */
+vscan_status vscan_delta_workspace_size(const vscan_route* route, const vscan_delta_args* args, uint64_t* bytes);
+
+/*
+ * Chunked forward pass over one direction of `route` (BIDIR, CROSS4 or ATROUS2;
+ * NULL for plain or packed sequences). An ATROUS2 direction visits its own
+ * group's tokens only: the other rows of y are left as they are, and a padding
+ * slot is a step of zero q, k, v, a and b, whose state still decays. Enqueued on
+ * stream (two launches); allocates nothing; never synchronizes; overlapping
+ * calls need workspaces of their own.
+ * Errors: INVALID_ARGUMENT, SHAPE (heads or direction that do not fit, a token
+ * count that is not the route's), ALIGNMENT, UNSUPPORTED (pooled routes, head
+ * widths above the limits, heads_v or batch above 65535, seq_offsets with a
+ * route), WORKSPACE, CUDA.
+ */
+vscan_status vscan_delta_forward(const vscan_route* route, const vscan_delta_args* args, void* stream);
+
+/*
+ * One token of each of `batch` sequences (tokens must be 1; no route, no
+ * seq_offsets): reads initial_state, which must be given, writes the updated
+ * state to final_state (which may be the same memory) and y. One launch; no
+ * workspace. Errors as vscan_delta_forward.
+ */
+vscan_status vscan_delta_step(const vscan_delta_args* args, void* stream);
+
 /* Message for the last non-OK status on this thread ("" if none). */
 const char* vscan_last_error(void);
 

@@ -412,3 +412,9 @@ class BackwardPlan:
 
 
 __all__.append("BackwardPlan")
+
+
+# the matrix-state mixer and the query/key norm that feeds it
+from .delta import delta_forward, delta_step  # noqa: E402
+
+__all__ += ["delta_forward", "delta_step"]

@@ -74,6 +74,20 @@ class VscanGrads(ctypes.Structure):
         ("workspace_bytes", ctypes.c_uint64)]
 
 
+class VscanDeltaArgs(ctypes.Structure):
+    """Mirror of struct vscan_delta_args (include/vscan.h)."""
+
+    _fields_ = (
+        [(name, ctypes.c_int32) for name in
+         ("batch", "tokens", "heads_k", "heads_v", "dim_k", "dim_v", "dtype", "direction")]
+        + [(name, ctypes.c_void_p) for name in
+           ("q", "k", "v", "a", "b", "y", "A", "bias", "initial_state", "final_state", "seq_offsets")]
+        + [("scale", ctypes.c_float), ("beta_scale", ctypes.c_float)]
+        + [(f"{name}_{axis}_stride", ctypes.c_int64) for name in "qkvaby" for axis in ("tok", "batch")]
+        + [("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_uint64)]
+    )
+
+
 class VscanError(RuntimeError):
     def __init__(self, status, message):
         self.status = status
@@ -88,6 +102,7 @@ def _load():
     lib = ctypes.CDLL(LIB_PATH)
     i32, p, u64 = ctypes.c_int32, ctypes.c_void_p, ctypes.c_uint64
     pa = ctypes.POINTER(VscanArgs)
+    pd = ctypes.POINTER(VscanDeltaArgs)
     sigs = {
         "vscan_create_route": ([ctypes.POINTER(p), i32, i32, i32, i32], i32),
         "vscan_destroy": ([p], i32),
@@ -103,6 +118,9 @@ def _load():
         "vscan_backward_workspace_size": ([p, pa, ctypes.POINTER(u64)], i32),
         "vscan_backward_plan_kernel": ([p, pa, ctypes.POINTER(ctypes.c_char_p)], i32),
         "vscan_backward": ([p, pa, p, ctypes.POINTER(VscanGrads), p], i32),
+        "vscan_delta_workspace_size": ([p, pd, ctypes.POINTER(u64)], i32),
+        "vscan_delta_forward": ([p, pd, p], i32),
+        "vscan_delta_step": ([pd, p], i32),
         "vscan_last_error": ([], ctypes.c_char_p),
         "vscan_status_string": ([i32], ctypes.c_char_p),
         "vscan_status_from_device_word": ([i32], i32),

@@ -8,7 +8,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libvscan.so")
-SOURCES = [os.path.join(CSRC, "vscan_api.cu")]
+SOURCES = [os.path.join(CSRC, name) for name in ("vscan_api.cu", "vscan_delta.cu")]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -24,7 +24,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         newest = max(os.path.getmtime(f) for f in _inputs())
         if os.path.getmtime(LIB) >= newest:
             return LIB
-    cmd = ["nvcc", "-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC,-O2",
+    cmd = ["nvcc", "-t", "0", "-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC,-O2",
            "-shared", "-cudart", "static", "-I", INCLUDE, "-I", CSRC, "-o", LIB, *SOURCES]
     if verbose_ptxas:
         cmd.insert(1, "-Xptxas=-v")

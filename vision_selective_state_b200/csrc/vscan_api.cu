@@ -15,7 +15,7 @@
 
 #include "vscan.h"
 #include "vscan_backward.cuh"
-#include <nvtx3/nvToolsExt.h>
+#include "vscan_host.h"
 
 #include "vscan_check.cuh"
 #include "vscan_layout.cuh"
@@ -25,26 +25,13 @@
 #include "vscan_route.cuh"
 #include "vscan_stream.cuh"
 
-struct vscan_route {
-    vscan::RouteGeom g;
-};
-
 namespace {
 
-constexpr int32_t kAbiVersion = 5;
-
-// A named NVTX range for the duration of a public call, so a profiler's
-// timeline groups each call's copies and kernels (a no-op unless a tool is
-// attached; NVTX v3 is header-only).
-struct NvtxRange {
-    explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-    ~NvtxRange() { nvtxRangePop(); }
-    NvtxRange(const NvtxRange&) = delete;
-    NvtxRange& operator=(const NvtxRange&) = delete;
-};
-constexpr int32_t kKnownFlags = VSCAN_FLAG_ZOH | VSCAN_FLAG_CHECK_VALUES;
-constexpr size_t kMaxSmem = 200 * 1024;  // dynamic shared memory the kernels may ask for
 thread_local std::string g_last_error;
+
+}  // namespace
+
+namespace vscan_host {
 
 vscan_status fail(vscan_status s, const char* fmt, ...)
 {
@@ -62,11 +49,21 @@ vscan_status cuda_fail(cudaError_t e, const char* what)
     return fail(VSCAN_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorString(e), cudaGetErrorName(e));
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace vscan_host
 
-size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
+namespace {
 
-size_t elem_bytes(int32_t dtype) { return dtype == VSCAN_BF16 ? 2 : 4; }
+using vscan_host::aligned16;
+using vscan_host::cuda_fail;
+using vscan_host::elem_bytes;
+using vscan_host::fail;
+using vscan_host::NvtxRange;
+using vscan_host::round256;
+using vscan_host::set_smem_once;
+
+constexpr int32_t kAbiVersion = 5;
+constexpr int32_t kKnownFlags = VSCAN_FLAG_ZOH | VSCAN_FLAG_CHECK_VALUES;
+constexpr size_t kMaxSmem = 200 * 1024;  // dynamic shared memory the kernels may ask for
 
 bool is_pool(int kind) { return kind == vscan::RK_POOL_W || kind == vscan::RK_POOL_H; }
 
@@ -231,23 +228,6 @@ uint64_t workspace_need(const vscan_route* r, const vscan_args* a)
 
 // BIDIR sequences at least this long run 32-step chunks (bf16 I/O, no options).
 constexpr int kLongChunkMinL = 2048;
-
-// Raise a kernel's dynamic shared-memory limit once per device (the attribute
-// stays set for the process), not on every launch: one flag per instantiation
-// of the calling template and device ordinal.
-template <typename Kernel>
-cudaError_t set_smem_once(Kernel* fn, int bytes, int* done_by_device, int max_devices)
-{
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < max_devices && __atomic_load_n(&done_by_device[dev], __ATOMIC_ACQUIRE) >= bytes)
-        return cudaSuccess;
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && dev >= 0 && dev < max_devices)
-        __atomic_store_n(&done_by_device[dev], bytes, __ATOMIC_RELEASE);
-    return e;
-}
 
 constexpr int kAttrDevices = 64;
 

@@ -1,0 +1,280 @@
+// C ABI of the gated delta rule (declared in include/vscan.h): argument checks,
+// workspace layout, kernel selection and launch. Every check runs before the
+// first CUDA call, so a rejected call launches nothing.
+#include <cmath>
+
+#include "vscan.h"
+#include "vscan_delta.cuh"
+#include "vscan_host.h"
+
+namespace {
+
+using vscan_host::aligned16;
+using vscan_host::cuda_fail;
+using vscan_host::fail;
+using vscan_host::NvtxRange;
+using vscan_host::round256;
+using vscan_host::set_smem_once;
+using vscan::DeltaParams;
+using vscan::DL_C;
+
+constexpr int kAttrDevices = 64;
+constexpr int kMaxDimK = 128, kMaxDimV = 256, kMaxGrid = 65535;
+
+// Widths the kernels are built for: dim_k is rounded up to one of them.
+int padded_dim_k(int dk) { return (dk + 31) / 32 * 32; }
+
+struct Stride { int64_t tok, img; };
+
+Stride resolve(int64_t tok, int64_t img, int64_t width, int64_t tokens)
+{
+    Stride s;
+    s.tok = tok ? tok : width;
+    s.img = img ? img : s.tok * tokens;
+    return s;
+}
+
+vscan_status check_stride(const char* name, int64_t tok, int64_t img, int64_t width, int64_t tokens, int vec)
+{
+    if (tok < 0 || img < 0) return fail(VSCAN_ERR_INVALID_ARGUMENT, "%s strides must be >= 0 (0 = dense)", name);
+    const Stride s = resolve(tok, img, width, tokens);
+    if (s.tok < width || s.tok % vec != 0)
+        return fail(VSCAN_ERR_ALIGNMENT, "%s token stride %lld must be >= %lld and a multiple of %d", name, (long long)s.tok,
+                    (long long)width, vec);
+    if (s.img % vec != 0)
+        return fail(VSCAN_ERR_ALIGNMENT, "%s batch stride %lld is not a multiple of %d", name, (long long)s.img, vec);
+    return VSCAN_OK;
+}
+
+// Checks that do not depend on where the tensors live.
+vscan_status check_shape(const vscan_route* r, const vscan_delta_args* a)
+{
+    if (!a) return fail(VSCAN_ERR_INVALID_ARGUMENT, "args is NULL");
+    if (a->dtype != VSCAN_F32 && a->dtype != VSCAN_BF16)
+        return fail(VSCAN_ERR_INVALID_ARGUMENT, "unknown dtype %d", a->dtype);
+    if (a->batch < 0) return fail(VSCAN_ERR_INVALID_ARGUMENT, "batch %d < 0", a->batch);
+    if (a->tokens < 0) return fail(VSCAN_ERR_INVALID_ARGUMENT, "tokens %d < 0", a->tokens);
+    if (a->heads_k < 1 || a->heads_v < 1)
+        return fail(VSCAN_ERR_INVALID_ARGUMENT, "heads_k %d and heads_v %d must be >= 1", a->heads_k, a->heads_v);
+    if (a->heads_v % a->heads_k != 0)
+        return fail(VSCAN_ERR_SHAPE, "heads_v %d is not a multiple of heads_k %d", a->heads_v, a->heads_k);
+    if (a->dim_k < 1 || a->dim_v < 1)
+        return fail(VSCAN_ERR_INVALID_ARGUMENT, "dim_k %d and dim_v %d must be >= 1", a->dim_k, a->dim_v);
+    const int vec = a->dtype == VSCAN_F32 ? 4 : 8;
+    if (a->dim_k % vec != 0 || a->dim_v % vec != 0)
+        return fail(VSCAN_ERR_ALIGNMENT, "dim_k %d and dim_v %d must be multiples of %d (16-byte rows)", a->dim_k, a->dim_v, vec);
+    if (a->dim_k > kMaxDimK || a->dim_v > kMaxDimV)
+        return fail(VSCAN_ERR_UNSUPPORTED, "dim_k %d > %d or dim_v %d > %d", a->dim_k, kMaxDimK, a->dim_v, kMaxDimV);
+    if (a->batch > kMaxGrid || a->heads_v > kMaxGrid)
+        return fail(VSCAN_ERR_UNSUPPORTED, "batch %d or heads_v %d > %d", a->batch, a->heads_v, kMaxGrid);
+    if (!std::isfinite(a->scale) || !std::isfinite(a->beta_scale))
+        return fail(VSCAN_ERR_INVALID_ARGUMENT, "scale and beta_scale must be finite");
+    if (r) {
+        if (r->g.kind != vscan::RK_BIDIR && r->g.kind != vscan::RK_CROSS4 && r->g.kind != vscan::RK_ATROUS2)
+            return fail(VSCAN_ERR_UNSUPPORTED, "the delta rule runs over BIDIR, CROSS4 and ATROUS2 routes");
+        if (a->seq_offsets) return fail(VSCAN_ERR_UNSUPPORTED, "seq_offsets needs plain sequences, not a route");
+        if (a->direction < 0 || a->direction >= r->g.K)
+            return fail(VSCAN_ERR_SHAPE, "direction %d, the route has %d", a->direction, r->g.K);
+        if (a->tokens != r->g.tokens)
+            return fail(VSCAN_ERR_SHAPE, "tokens %d, the route has %d per image", a->tokens, r->g.tokens);
+    } else if (a->direction != 0) {
+        return fail(VSCAN_ERR_SHAPE, "direction %d without a route", a->direction);
+    }
+    const int64_t wk = (int64_t)a->heads_k * a->dim_k, wv = (int64_t)a->heads_v * a->dim_v;
+    vscan_status st;
+    if ((st = check_stride("q", a->q_tok_stride, a->q_batch_stride, wk, a->tokens, vec)) != VSCAN_OK) return st;
+    if ((st = check_stride("k", a->k_tok_stride, a->k_batch_stride, wk, a->tokens, vec)) != VSCAN_OK) return st;
+    if ((st = check_stride("v", a->v_tok_stride, a->v_batch_stride, wv, a->tokens, vec)) != VSCAN_OK) return st;
+    if ((st = check_stride("y", a->y_tok_stride, a->y_batch_stride, wv, a->tokens, vec)) != VSCAN_OK) return st;
+    if ((st = check_stride("a", a->a_tok_stride, a->a_batch_stride, 1, a->tokens, 1)) != VSCAN_OK) return st;
+    if ((st = check_stride("b", a->b_tok_stride, a->b_batch_stride, 1, a->tokens, 1)) != VSCAN_OK) return st;
+    return VSCAN_OK;
+}
+
+// y (or, for the gradients, dy) is the last tensor: the only one some calls lack.
+vscan_status check_pointers(const vscan_delta_args* a, const void* y)
+{
+    if (!a->q || !a->k || !a->v || !a->a || !a->b || !y || !a->A)
+        return fail(VSCAN_ERR_INVALID_ARGUMENT, "q, k, v, a, b, A and y (dy) must not be NULL");
+    if (!aligned16(a->q) || !aligned16(a->k) || !aligned16(a->v) || !aligned16(y) || !aligned16(a->initial_state) ||
+        !aligned16(a->final_state))
+        return fail(VSCAN_ERR_ALIGNMENT, "q, k, v, y (dy) and the states must be 16-byte aligned");
+    const uintptr_t el = a->dtype == VSCAN_F32 ? 3 : 1;
+    if (((uintptr_t)a->a & el) || ((uintptr_t)a->b & el) || ((uintptr_t)a->A & 3) || ((uintptr_t)a->bias & 3) ||
+        ((uintptr_t)a->seq_offsets & 3))
+        return fail(VSCAN_ERR_ALIGNMENT, "a, b, A, bias or seq_offsets is not aligned to its element");
+    return VSCAN_OK;
+}
+
+int chunks_of(const vscan_route* r, const vscan_delta_args* a)
+{
+    return ((r ? r->g.L : a->tokens) + DL_C - 1) / DL_C;
+}
+
+// Chunk slots of the workspace. A packed sequence's slots start at
+// floor(first row / 64) + its index: sequences never share one.
+long long slots_of(const vscan_route* r, const vscan_delta_args* a)
+{
+    if (a->seq_offsets) return (long long)a->tokens / DL_C + a->batch + 1;
+    return (long long)a->batch * chunks_of(r, a);
+}
+
+bool empty(const vscan_delta_args* a) { return a->batch == 0; }
+
+struct Layout {
+    size_t T, P, vec, total;
+};
+
+Layout forward_layout(const vscan_route* r, const vscan_delta_args* a, int pplanes)
+{
+    const size_t n = (size_t)slots_of(r, a) * a->heads_v;
+    Layout l;
+    l.T = 0;
+    l.P = l.T + round256(n * 3 * vscan::DL_PLANE * 2);
+    l.vec = l.P + round256(n * pplanes * vscan::DL_PLANE * 2);
+    l.total = l.vec + round256(n * vscan::DL_VECS * 4);
+    return l;
+}
+
+int forward_planes(const vscan_delta_args* a) { return a->dtype == VSCAN_F32 ? 3 : 2; }
+
+DeltaParams make_params(const vscan_route* r, const vscan_delta_args* a)
+{
+    DeltaParams p{};
+    if (r) { p.g = r->g; p.has_route = 1; }
+    p.dir = a->direction;
+    p.batch = a->batch;
+    p.tokens = a->tokens;
+    p.heads_k = a->heads_k;
+    p.heads_v = a->heads_v;
+    p.group = a->heads_v / a->heads_k;
+    p.dk = a->dim_k;
+    p.dv = a->dim_v;
+    p.offsets = a->seq_offsets;
+    p.chunks = chunks_of(r, a);
+    p.slots = slots_of(r, a);
+    p.q = a->q; p.k = a->k; p.v = a->v; p.a = a->a; p.b = a->b; p.y = a->y;
+    p.A = a->A; p.bias = a->bias;
+    p.s_in = a->initial_state;
+    p.s_out = a->final_state;
+    p.scale = a->scale;
+    p.beta_scale = a->beta_scale;
+    const int64_t wk = (int64_t)a->heads_k * a->dim_k, wv = (int64_t)a->heads_v * a->dim_v;
+    Stride s;
+    s = resolve(a->q_tok_stride, a->q_batch_stride, wk, a->tokens); p.q_tok = s.tok; p.q_img = s.img;
+    s = resolve(a->k_tok_stride, a->k_batch_stride, wk, a->tokens); p.k_tok = s.tok; p.k_img = s.img;
+    s = resolve(a->v_tok_stride, a->v_batch_stride, wv, a->tokens); p.v_tok = s.tok; p.v_img = s.img;
+    s = resolve(a->y_tok_stride, a->y_batch_stride, wv, a->tokens); p.y_tok = s.tok; p.y_img = s.img;
+    s = resolve(a->a_tok_stride, a->a_batch_stride, a->heads_v, a->tokens); p.a_tok = s.tok; p.a_img = s.img;
+    s = resolve(a->b_tok_stride, a->b_batch_stride, a->heads_v, a->tokens); p.b_tok = s.tok; p.b_img = s.img;
+    return p;
+}
+
+template <typename T, int DKP>
+cudaError_t launch_prep(const DeltaParams& p, cudaStream_t stream)
+{
+    if (p.slots == 0 || p.tokens == 0) return cudaSuccess;
+    static int done[kAttrDevices];
+    constexpr size_t smem = vscan::delta_prep_smem<T, DKP>();
+    cudaError_t e = set_smem_once(vscan::delta_prep_kernel<T, DKP>, (int)smem, done, kAttrDevices);
+    if (e != cudaSuccess) return e;
+    vscan::delta_prep_kernel<T, DKP><<<dim3((unsigned)p.slots, p.heads_v), 128, smem, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T, int DKP, bool SAVE>
+cudaError_t launch_scan(const DeltaParams& p, cudaStream_t stream)
+{
+    using Sh = vscan::ScanShape<T, DKP>;
+    static int done[kAttrDevices];
+    const int warps = p.dv >= 128 ? 8 : (p.dv + 15) / 16;
+    const size_t smem = Sh::STAGES * Sh::stage_bytes(warps);
+    cudaError_t e = set_smem_once(vscan::delta_scan_kernel<T, DKP, SAVE>, (int)smem, done, kAttrDevices);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((p.dv + 127) / 128, p.heads_v, p.batch);
+    vscan::delta_scan_kernel<T, DKP, SAVE><<<grid, warps * 32, smem, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T, int DKP>
+cudaError_t run_forward(const DeltaParams& p, cudaStream_t stream)
+{
+    cudaError_t e = launch_prep<T, DKP>(p, stream);
+    if (e != cudaSuccess) return e;
+    return launch_scan<T, DKP, false>(p, stream);
+}
+
+// f(width) with the I/O type and the padded key width as template arguments.
+#define DELTA_DISPATCH(FN, a, ...)                                                              \
+    (a->dtype == VSCAN_F32                                                                      \
+         ? (padded_dim_k(a->dim_k) == 32   ? FN<float, 32>(__VA_ARGS__)                         \
+            : padded_dim_k(a->dim_k) == 64 ? FN<float, 64>(__VA_ARGS__)                         \
+            : padded_dim_k(a->dim_k) == 96 ? FN<float, 96>(__VA_ARGS__)                         \
+                                           : FN<float, 128>(__VA_ARGS__))                       \
+         : (padded_dim_k(a->dim_k) == 32   ? FN<__nv_bfloat16, 32>(__VA_ARGS__)                 \
+            : padded_dim_k(a->dim_k) == 64 ? FN<__nv_bfloat16, 64>(__VA_ARGS__)                 \
+            : padded_dim_k(a->dim_k) == 96 ? FN<__nv_bfloat16, 96>(__VA_ARGS__)                 \
+                                           : FN<__nv_bfloat16, 128>(__VA_ARGS__)))
+
+}  // namespace
+
+extern "C" {
+
+vscan_status vscan_delta_workspace_size(const vscan_route* route, const vscan_delta_args* args, uint64_t* bytes)
+{
+    if (!bytes) return fail(VSCAN_ERR_INVALID_ARGUMENT, "bytes is NULL");
+    const vscan_status st = check_shape(route, args);
+    if (st != VSCAN_OK) return st;
+    *bytes = empty(args) ? 0 : forward_layout(route, args, forward_planes(args)).total;
+    return VSCAN_OK;
+}
+
+vscan_status vscan_delta_forward(const vscan_route* route, const vscan_delta_args* args, void* stream)
+{
+    vscan_status st = check_shape(route, args);
+    if (st != VSCAN_OK) return st;
+    if (empty(args) || (args->tokens == 0 && !args->final_state)) return VSCAN_OK;
+    if (args->tokens > 0 && (st = check_pointers(args, args->y)) != VSCAN_OK) return st;
+    if (!aligned16(args->initial_state) || !aligned16(args->final_state))
+        return fail(VSCAN_ERR_ALIGNMENT, "the states must be 16-byte aligned");
+    const Layout l = forward_layout(route, args, forward_planes(args));
+    if (l.total && (!args->workspace || args->workspace_bytes < l.total))
+        return fail(VSCAN_ERR_WORKSPACE, "workspace of %llu bytes, %llu needed", (unsigned long long)args->workspace_bytes,
+                    (unsigned long long)l.total);
+    if (!aligned16(args->workspace)) return fail(VSCAN_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
+    if (slots_of(route, args) > 0x7fffffffLL)
+        return fail(VSCAN_ERR_UNSUPPORTED, "more than 2^31 chunks of %d steps", DL_C);
+    NvtxRange range("vscan_delta_forward");
+    DeltaParams p = make_params(route, args);
+    char* ws = static_cast<char*>(args->workspace);
+    p.tplanes = forward_planes(args);
+    p.wT = reinterpret_cast<__nv_bfloat16*>(ws + l.T);
+    p.wP = reinterpret_cast<__nv_bfloat16*>(ws + l.P);
+    p.wvec = reinterpret_cast<float*>(ws + l.vec);
+    const cudaError_t e = DELTA_DISPATCH(run_forward, args, p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? VSCAN_OK : cuda_fail(e, "vscan_delta_forward");
+}
+
+vscan_status vscan_delta_step(const vscan_delta_args* args, void* stream)
+{
+    vscan_status st = check_shape(nullptr, args);
+    if (st != VSCAN_OK) return st;
+    if (args->tokens != 1) return fail(VSCAN_ERR_SHAPE, "vscan_delta_step takes one token a row, not %d", args->tokens);
+    if (args->seq_offsets) return fail(VSCAN_ERR_UNSUPPORTED, "vscan_delta_step takes no seq_offsets");
+    if (empty(args)) return VSCAN_OK;
+    if ((st = check_pointers(args, args->y)) != VSCAN_OK) return st;
+    if (!args->initial_state || !args->final_state)
+        return fail(VSCAN_ERR_INVALID_ARGUMENT, "initial_state and final_state must not be NULL");
+    NvtxRange range("vscan_delta_step");
+    const DeltaParams p = make_params(nullptr, args);
+    const dim3 grid((p.dv + vscan::DS_COLS - 1) / vscan::DS_COLS, p.heads_v, p.batch);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (args->dtype == VSCAN_F32)
+        vscan::delta_step_kernel<float><<<grid, 128, 0, s>>>(p);
+    else
+        vscan::delta_step_kernel<__nv_bfloat16><<<grid, 128, 0, s>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? VSCAN_OK : cuda_fail(e, "vscan_delta_step");
+}
+
+}  // extern "C"

@@ -1,0 +1,790 @@
+// Gated delta rule: device code of the chunked forward and backward passes and
+// of the single-token step.
+//
+// Per value head, with log decay g and write strength beta,
+//
+//   S_t = e^{g_t} S_{t-1} + beta_t k_t (v_t - e^{g_t} S_{t-1}^T k_t)^T,   y_t = scale S_t^T q_t.
+//
+// Inside a chunk of 64 steps with entering state S0 and G the running sum of g,
+// substituting the recurrence into itself gives
+//
+//   (I + L) W = X,   L_ij = beta_i e^{G_i - G_j} k_i.k_j (j < i),   X_i = beta_i (v_i - e^{G_i} S0^T k_i)
+//   y_i = scale e^{G_i} S0^T q_i + sum_{j<=i} P_ij w_j,             P_ij = scale e^{G_i - G_j} q_i.k_j
+//   S_C = e^{G_C} S0 + sum_j e^{G_C - G_j} k_j w_j^T
+//
+// so a chunk is matrix products plus the inverse T = (I + L)^-1 of a 64 x 64
+// unit lower triangle. delta_prep_kernel computes T, P and the decays of every
+// chunk in parallel; delta_scan_kernel walks the chunks of one head in order
+// and holds the state in registers; delta_rscan_kernel walks them backwards for
+// the gradients; delta_grad_kernel turns both walks into dq, dk, da, db chunk
+// by chunk in parallel.
+//
+// Precision. Products run on the bf16 tensor-core path with float32
+// accumulation. A bf16 input is exact there; every float32 operand (the state,
+// W, T, P) is split into three bf16 terms of 8 bits each (x = x0 + x1 + x2 to
+// 2^-24) and the products of total order up to 2 are summed, so that states and
+// gradients keep float32 accuracy: one term alone would leave 2^-9 and two 2^-17
+// in a carried state.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "vscan_common.cuh"
+#include "vscan_params.cuh"
+#include "vscan_route.cuh"
+
+namespace vscan {
+
+constexpr int DL_C = 64;          // steps per chunk
+constexpr int DL_TPITCH = 72;     // shared-memory row pitch of a 64-wide bf16 tile: 144 bytes, an odd
+                                  // multiple of 16, so ldmatrix rows fall into different banks
+constexpr int DL_VECS = 4 * DL_C;  // floats per chunk: e^{G_i}, e^{G_C - G_i}, beta_i, and {e^{G_C}}
+constexpr int DL_PLANE = DL_C * DL_C;
+
+struct DeltaParams {
+    RouteGeom g;
+    int has_route, dir;
+    int batch;        // images, or packed sequences
+    int tokens;       // rows per image, or rows of the packed arrays
+    int heads_k, heads_v, group;
+    int dk, dv;
+    const int* offsets;  // [batch + 1] or null
+    int chunks;          // chunks per image (no offsets)
+    long long slots;     // chunk slots in the workspace
+    int tplanes;         // bf16 planes of P in the workspace (T always has 3)
+    const void *q, *k, *v, *a, *b;
+    const float *A, *bias;
+    const float* s_in;
+    float* s_out;
+    void* y;
+    float scale, beta_scale;
+    long long q_tok, q_img, k_tok, k_img, v_tok, v_img, a_tok, a_img, b_tok, b_img, y_tok, y_img;
+    // workspace, indexed by slot * heads_v + head
+    __nv_bfloat16* wT;   // [..][3][64][64]
+    __nv_bfloat16* wP;   // [..][tplanes][64][64]
+    float* wvec;         // [..][DL_VECS]
+    float* wS;           // [..][dv][DKP]: state entering the chunk (backward)
+    float* wW;           // [..][64][dv]: W of the chunk (backward)
+    // backward
+    const void* dy;      // like y
+    const float* ds_in;  // gradient of the final state or null
+    float* ds_out;       // gradient of the initial state or null
+    float* wdS;          // [..][dv][DKP]: gradient of the state leaving the chunk
+    float* wdV;          // [..][64][dv]
+    float* wpart;        // [..][2]: per-chunk sums for dA and dbias
+    float *wdq, *wdk;    // [images][tokens][heads_v][dk]: with shared key heads, per value head
+    void *dq, *dkey, *dvalue, *da, *db;  // dense, in the I/O type
+    float *dA, *dbias;
+};
+
+// The steps of one image or packed sequence: its length, its first workspace
+// slot, and the token row of a step. Offsets come from device memory: they are
+// clamped into the arrays so that no value of theirs leads outside.
+struct DeltaSeq {
+    int len, first;
+    long long slot;
+};
+
+__device__ __forceinline__ DeltaSeq delta_seq(const DeltaParams& p, int b)
+{
+    DeltaSeq s;
+    if (p.offsets) {
+        const int o0 = min(max(p.offsets[b], 0), p.tokens);
+        const int o1 = min(max(p.offsets[b + 1], o0), p.tokens);
+        s.len = o1 - o0;
+        s.first = o0;
+        s.slot = o0 / DL_C + b;
+    } else {
+        s.len = p.has_route ? p.g.L : p.tokens;
+        s.first = 0;
+        s.slot = (long long)b * p.chunks;
+    }
+    return s;
+}
+
+// Row of step t in the token arrays of its image; -1 for a padding step of the
+// atrous route, whose token is zero, and behind the sequence's end.
+__device__ __forceinline__ int delta_row(const DeltaParams& p, const DeltaSeq& s, int t)
+{
+    if (t >= s.len) return -1;
+    if (!p.has_route) return s.first + t;
+    return route_token_any(p.g, p.dir, t);
+}
+
+__device__ __forceinline__ long long delta_img(const DeltaParams& p, int b) { return p.offsets ? 0 : b; }
+
+// ---- tensor-core fragments ------------------------------------------------------
+// m16n8k16: lane (g, t) = (lane / 4, lane % 4) holds of A the pairs of columns
+// 2t and 2t + 8 of rows g and g + 8; of B the pairs of rows 2t and 2t + 8 of
+// column g; of C columns 2t, 2t + 1 of rows g and g + 8. Two neighbouring C
+// tiles therefore are one A fragment once rounded, without any exchange.
+struct Frag4 { uint32_t x[4]; };
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const Frag4& a, uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a.x[0]), "r"(a.x[1]), "r"(a.x[2]), "r"(a.x[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ Frag4 ldsm4(const __nv_bfloat16* p)
+{
+    Frag4 f;
+    const unsigned s = static_cast<unsigned>(__cvta_generic_to_shared(p));
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(f.x[0]), "=r"(f.x[1]), "=r"(f.x[2]), "=r"(f.x[3]) : "r"(s));
+    return f;
+}
+
+__device__ __forceinline__ Frag4 ldsm4t(const __nv_bfloat16* p)
+{
+    Frag4 f;
+    const unsigned s = static_cast<unsigned>(__cvta_generic_to_shared(p));
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(f.x[0]), "=r"(f.x[1]), "=r"(f.x[2]), "=r"(f.x[3]) : "r"(s));
+    return f;
+}
+
+// A fragment of the 16 x 16 block at (m0, k0) of a row-major [m][k] tile, or of
+// the transpose of a [k][m] tile.
+__device__ __forceinline__ Frag4 load_a(const __nv_bfloat16* t, int pitch, int m0, int k0, int lane)
+{
+    return ldsm4(t + (m0 + (lane & 7) + ((lane >> 3) & 1) * 8) * pitch + k0 + (lane >> 4) * 8);
+}
+__device__ __forceinline__ Frag4 load_a_t(const __nv_bfloat16* t, int pitch, int m0, int k0, int lane)
+{
+    return ldsm4t(t + (k0 + (lane & 7) + (lane >> 4) * 8) * pitch + m0 + ((lane >> 3) & 1) * 8);
+}
+// B fragments of two neighbouring 8-wide column tiles (x[0..1] at n0, x[2..3] at
+// n0 + 8) of a [n][k] tile, or of a [k][n] tile.
+__device__ __forceinline__ Frag4 load_b(const __nv_bfloat16* t, int pitch, int n0, int k0, int lane)
+{
+    return ldsm4(t + (n0 + (lane & 7) + (lane >> 4) * 8) * pitch + k0 + ((lane >> 3) & 1) * 8);
+}
+__device__ __forceinline__ Frag4 load_b_t(const __nv_bfloat16* t, int pitch, int n0, int k0, int lane)
+{
+    return ldsm4t(t + (k0 + (lane & 7) + ((lane >> 3) & 1) * 8) * pitch + n0 + (lane >> 4) * 8);
+}
+
+// x = h + r for a pair: h rounded to bf16 (packed, x in the low half), r exact.
+__device__ __forceinline__ uint32_t split_bf16(float& x, float& y)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(&h);
+    x -= __uint_as_float(u << 16);
+    y -= __uint_as_float(u & 0xffff0000u);
+    return u;
+}
+
+// NT bf16 terms of a pair of C tiles as A fragments.
+template <int NT>
+__device__ __forceinline__ void split_tiles(const float (&lo)[4], const float (&hi)[4], Frag4 (&out)[NT])
+{
+    float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[n].x[i] = split_bf16(v[2 * i], v[2 * i + 1]);
+}
+
+// c += sum over terms a[x] b[y], x + y <= ORD, b from NB planes of one pair of column tiles.
+template <int NA, int NB, int ORD = 2>
+__device__ __forceinline__ void mma_terms(float (&c0)[4], float (&c1)[4], const Frag4 (&a)[NA], const Frag4 (&b)[NB])
+{
+    // small terms first: they add up before the large one hides their last bits
+#pragma unroll
+    for (int o = ORD; o >= 0; --o)
+#pragma unroll
+        for (int y = 0; y < NB; ++y) {
+            const int x = o - y;
+            if (x >= 0 && x < NA) {
+                mma_bf16(c0, a[x], b[y].x[0], b[y].x[1]);
+                mma_bf16(c1, a[x], b[y].x[2], b[y].x[3]);
+            }
+        }
+}
+
+// ---- tiles ------------------------------------------------------------------------
+template <typename T> struct DeltaIo;
+template <> struct DeltaIo<__nv_bfloat16> { static constexpr int planes = 1; };
+template <> struct DeltaIo<float> { static constexpr int planes = 3; };
+
+// Rows [0, 64) of one head's [64][cols] tile of a token array into `planes` bf16
+// planes of shared memory (pitch elements a row, plane elements apart): steps
+// without a token and columns from `have` on are zero. bf16 rows are copied
+// asynchronously (the caller commits and waits); float32 rows are split here.
+__device__ __forceinline__ void load_tile(__nv_bfloat16* dst, int pitch, int, const __nv_bfloat16* src, long long tok,
+                                          const DeltaParams& p, const DeltaSeq& s, int t0, int cols, int have, int tid,
+                                          int nthreads)
+{
+    const int vecs = cols / 8;
+    for (int i = tid; i < DL_C * vecs; i += nthreads) {
+        const int r = i / vecs, c = (i - r * vecs) * 8;
+        const int row = delta_row(p, s, t0 + r);
+        const bool ok = row >= 0 && c < have;
+        cp_async16(dst + r * pitch + c, ok ? src + row * tok + c : src, ok);
+    }
+}
+__device__ __forceinline__ void load_tile(__nv_bfloat16* dst, int pitch, int plane, const float* src, long long tok,
+                                          const DeltaParams& p, const DeltaSeq& s, int t0, int cols, int have, int tid,
+                                          int nthreads)
+{
+    const int vecs = cols / 4;
+    for (int i = tid; i < DL_C * vecs; i += nthreads) {
+        const int r = i / vecs, c = (i - r * vecs) * 4;
+        const int row = delta_row(p, s, t0 + r);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (row >= 0 && c < have) x = __ldg(reinterpret_cast<const float4*>(src + row * tok + c));
+#pragma unroll
+        for (int n = 0; n < 3; ++n) {
+            uint2 u;
+            u.x = split_bf16(x.x, x.y);
+            u.y = split_bf16(x.z, x.w);
+            *reinterpret_cast<uint2*>(dst + n * plane + r * pitch + c) = u;
+        }
+    }
+}
+
+// The same rows unsplit, in the I/O type.
+template <typename T>
+__device__ __forceinline__ void load_raw(T* dst, int pitch, const T* src, long long tok, const DeltaParams& p,
+                                         const DeltaSeq& s, int t0, int cols, int have, int tid, int nthreads)
+{
+    constexpr int V = 16 / sizeof(T);
+    const int vecs = cols / V;
+    for (int i = tid; i < DL_C * vecs; i += nthreads) {
+        const int r = i / vecs, c = (i - r * vecs) * V;
+        const int row = delta_row(p, s, t0 + r);
+        const bool ok = row >= 0 && c < have;
+        cp_async16(dst + r * pitch + c, ok ? src + row * tok + c : src, ok);
+    }
+}
+
+// `planes` 64 x 64 bf16 planes from the workspace, pitch DL_TPITCH in shared memory.
+__device__ __forceinline__ void load_planes(__nv_bfloat16* dst, const __nv_bfloat16* src, int planes, int tid, int nthreads)
+{
+    for (int i = tid; i < planes * (DL_C * 8); i += nthreads) {
+        const int r = i >> 3, c = (i & 7) * 8;
+        cp_async16(dst + r * DL_TPITCH + c, src + r * DL_C + c, true);
+    }
+}
+
+// Log decay of a step. It is clamped at -120 (e^-120 is 0 in float32 with or
+// without the clamp), which keeps differences of its sums free of inf - inf.
+__device__ __forceinline__ float delta_softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
+__device__ __forceinline__ float delta_decay(float A, float x)
+{
+    const float g = A * delta_softplus(x);
+    return g < -120.f ? -120.f : g;
+}
+__device__ __forceinline__ float delta_sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
+
+// e^x of a difference of running sums held in float64: the float32 rounding of a
+// far-away sum would be an error of the exponent.
+__device__ __forceinline__ float exp_diff(double d)
+{
+    const float h = (float)d;
+    const float e = expf(h);
+    return e + e * (float)(d - (double)h);
+}
+
+// ---- per-chunk triangle: T, P, decays -----------------------------------------------
+// One CTA of four warps per chunk and value head. Bound by latency: two
+// 64 x 64 x dk products, 4 x 16 dependent rows of forward substitution and three
+// rounds of 16 x 16 block products.
+template <int DKP>
+struct PrepShape {
+    static constexpr int pitch = DKP + 8;  // an odd multiple of 16 bytes
+    static constexpr int plane = DL_C * pitch;
+};
+
+constexpr int DL_LP = DL_C + 1;  // pitch of the float32 triangle
+
+template <typename T, int DKP>
+constexpr size_t delta_prep_smem()
+{
+    const size_t tiles = 2 * (size_t)DeltaIo<T>::planes * PrepShape<DKP>::plane * 2;
+    const size_t tri = 2 * (size_t)DL_C * DL_LP * 4 + 4 * 16 * 17 * 4;
+    return tiles + tri + DL_C * 8 + 4 * DL_C * 4;
+}
+
+template <typename T, int DKP>
+__global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaParams p)
+{
+    constexpr int NP = DeltaIo<T>::planes, PITCH = PrepShape<DKP>::pitch, PLANE = PrepShape<DKP>::plane;
+    extern __shared__ __align__(16) unsigned char smem[];
+    double* G = reinterpret_cast<double*>(smem);
+    float* beta = reinterpret_cast<float*>(G + DL_C);
+    float* L = beta + 4 * DL_C;                 // [64][65]
+    float* Ti = L + DL_C * DL_LP;               // [64][65]
+    float* tmp = Ti + DL_C * DL_LP;             // [4 warps][16][17]
+    __nv_bfloat16* K = reinterpret_cast<__nv_bfloat16*>(tmp + 4 * 16 * 17);
+    __nv_bfloat16* Q = K + NP * PLANE;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, head = blockIdx.y;
+
+    // the sequence of this slot
+    int b;
+    if (p.offsets) {
+        int lo = 0, hi = p.batch;  // last b whose first slot is <= blockIdx.x
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (delta_seq(p, mid).slot <= (long long)blockIdx.x) lo = mid; else hi = mid;
+        }
+        b = lo;
+    } else {
+        b = blockIdx.x / p.chunks;
+    }
+    const DeltaSeq s = delta_seq(p, b);
+    const long long c = (long long)blockIdx.x - s.slot;
+    if (c < 0 || c * DL_C >= s.len) return;
+    const int t0 = (int)c * DL_C;
+    const long long img = delta_img(p, b);
+    const int hk = head / p.group;
+    const size_t rec = (size_t)blockIdx.x * p.heads_v + head;
+
+    load_tile(K, PITCH, PLANE, reinterpret_cast<const T*>(p.k) + img * p.k_img + (long long)hk * p.dk, p.k_tok, p, s, t0,
+              DKP, p.dk, tid, 128);
+    load_tile(Q, PITCH, PLANE, reinterpret_cast<const T*>(p.q) + img * p.q_img + (long long)hk * p.dk, p.q_tok, p, s, t0,
+              DKP, p.dk, tid, 128);
+    cp_async_commit();
+
+    if (warp == 0) {  // running sum of the log decay: two steps a lane, then a scan over the lanes
+        double g[2];
+        const float A = p.A[head], bias = p.bias ? p.bias[head] : 0.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = t0 + 2 * lane + i;
+            const int row = delta_row(p, s, t);
+            const float a = row >= 0 ? to_float(reinterpret_cast<const T*>(p.a)[img * p.a_img + row * p.a_tok + head]) : 0.f;
+            const float bb = row >= 0 ? to_float(reinterpret_cast<const T*>(p.b)[img * p.b_img + row * p.b_tok + head]) : 0.f;
+            g[i] = t < s.len ? (double)delta_decay(A, a + bias) : 0.0;
+            beta[2 * lane + i] = t < s.len ? p.beta_scale * delta_sigmoid(bb) : 0.f;
+        }
+        double sum = g[0] + g[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double other = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += other;
+        }
+        G[2 * lane] = sum - g[1];
+        G[2 * lane + 1] = sum;
+        __syncwarp();
+        float* vec = p.wvec + rec * DL_VECS;
+        const double last = G[DL_C - 1];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = 2 * lane + i;
+            vec[r] = exp_diff(G[r]);
+            vec[DL_C + r] = exp_diff(last - G[r]);
+            vec[2 * DL_C + r] = beta[r];
+        }
+        if (lane == 0) vec[3 * DL_C] = exp_diff(last);
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+
+    // K K^T and Q K^T, rows 16 warp .. of the lower triangle
+    {
+        float kk[8][4] = {}, qk[8][4] = {};
+        const int m0 = warp * 16;
+        for (int k0 = 0; k0 < DKP; k0 += 16) {
+            Frag4 ak[NP], aq[NP];
+#pragma unroll
+            for (int n = 0; n < NP; ++n) {
+                ak[n] = load_a(K + n * PLANE, PITCH, m0, k0, lane);
+                aq[n] = load_a(Q + n * PLANE, PITCH, m0, k0, lane);
+            }
+#pragma unroll
+            for (int nt = 0; nt < 8; nt += 2) {
+                if (nt * 8 <= m0) {
+                    Frag4 bk[NP];
+#pragma unroll
+                    for (int n = 0; n < NP; ++n) bk[n] = load_b(K + n * PLANE, PITCH, nt * 8, k0, lane);
+                    mma_terms<NP, NP>(kk[nt], kk[nt + 1], ak, bk);
+                    mma_terms<NP, NP>(qk[nt], qk[nt + 1], aq, bk);
+                }
+            }
+        }
+        __nv_bfloat16* wP = p.wP + rec * p.tplanes * DL_PLANE;
+        const int gr = lane >> 2, tc = (lane & 3) * 2;
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int i = m0 + gr + half * 8, j = nt * 8 + tc;
+                float pv[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    // selected, not multiplied by zero: what lies above the diagonal is not looked at
+                    const float d = j + e <= i ? exp_diff(G[i] - G[j + e]) : 0.f;
+                    pv[e] = j + e <= i ? p.scale * (d * qk[nt][half * 2 + e]) : 0.f;
+                    L[i * DL_LP + j + e] = j + e < i ? beta[i] * (d * kk[nt][half * 2 + e]) : 0.f;
+                    Ti[i * DL_LP + j + e] = 0.f;
+                }
+                for (int n = 0; n < p.tplanes; ++n)
+                    *reinterpret_cast<uint32_t*>(wP + n * DL_PLANE + i * DL_C + j) = split_bf16(pv[0], pv[1]);
+            }
+    }
+    __syncthreads();
+
+    // T = (I + L)^-1. Diagonal 16 x 16 blocks by forward substitution, one
+    // column a lane, one block a warp.
+    if (lane < 16) {
+        float x[16];
+        const float* Lb = L + (warp * 16) * DL_LP + warp * 16;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float v = i == lane ? 1.f : 0.f;
+#pragma unroll
+            for (int j = 0; j < i; ++j) v -= Lb[i * DL_LP + j] * x[j];
+            x[i] = v;
+            Ti[(warp * 16 + i) * DL_LP + warp * 16 + lane] = v;
+        }
+    }
+    __syncthreads();
+    // Blocks at distance d below the diagonal: T_rs = -T_rr sum_m L_rm T_ms.
+    for (int d = 1; d < 4; ++d) {
+        const int r = warp + d;
+        if (r < 4) {
+            float* t = tmp + warp * 16 * 17;
+            const int col = lane & 15, half = (lane >> 4) * 8;
+            float m[8] = {};
+            for (int kk = warp * 16; kk < r * 16; ++kk) {
+                const float x = Ti[kk * DL_LP + warp * 16 + col];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m[i] += L[(r * 16 + half + i) * DL_LP + kk] * x;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[(half + i) * 17 + col] = m[i];
+            __syncwarp();
+            float o[8] = {};
+#pragma unroll 4
+            for (int kk = 0; kk < 16; ++kk) {
+                const float x = t[kk * 17 + col];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] -= Ti[(r * 16 + half + i) * DL_LP + r * 16 + kk] * x;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) Ti[(r * 16 + half + i) * DL_LP + warp * 16 + col] = o[i];
+        }
+        __syncthreads();
+    }
+    __nv_bfloat16* wT = p.wT + rec * 3 * DL_PLANE;
+    for (int i = tid; i < DL_PLANE / 2; i += 128) {
+        const int r = i >> 5, j = (i & 31) * 2;
+        float x = Ti[r * DL_LP + j], y = Ti[r * DL_LP + j + 1];
+#pragma unroll
+        for (int n = 0; n < 3; ++n) *reinterpret_cast<uint32_t*>(wT + n * DL_PLANE + r * DL_C + j) = split_bf16(x, y);
+    }
+}
+
+// ---- the walk over the chunks -----------------------------------------------------
+// One CTA per image (sequence), value head and slice of up to 128 value
+// channels; each warp owns 16 value channels and holds S^T[16][DKP] of them in
+// registers, so the walk needs no exchange between warps: S^T K^T, X^T, W^T and
+// y^T come out of one product in exactly the layout that the next one takes.
+// The next chunk's tiles are copied while this one computes (STAGES = 2).
+template <typename T, int DKP>
+struct ScanShape {
+    static constexpr int NP = DeltaIo<T>::planes;
+    static constexpr int PP = NP == 1 ? 2 : 3;   // planes of P: y in bf16 needs two
+    static constexpr int STAGES = NP == 1 ? 2 : 1;
+    static constexpr int pitch = DKP + 8;
+    static constexpr int plane = DL_C * pitch;
+    static __host__ __device__ constexpr int vpitch(int warps) { return warps * 16 + 16 / (int)sizeof(T); }
+    static __host__ __device__ constexpr size_t stage_bytes(int warps)
+    {
+        return (size_t)2 * NP * plane * 2 + (size_t)DL_C * vpitch(warps) * sizeof(T) +
+               (size_t)(3 + PP) * DL_C * DL_TPITCH * 2 + DL_VECS * 4;
+    }
+};
+
+template <typename T, int DKP, bool SAVE>
+__global__ void __launch_bounds__(256) delta_scan_kernel(const DeltaParams p)
+{
+    using Sh = ScanShape<T, DKP>;
+    constexpr int NP = Sh::NP, PP = Sh::PP, PITCH = Sh::pitch, PLANE = Sh::plane, NT = DKP / 8;
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int tid = threadIdx.x, nthreads = blockDim.x, warps = nthreads >> 5, warp = tid >> 5, lane = tid & 31;
+    const int gr = lane >> 2, tc = (lane & 3) * 2;
+    const int head = blockIdx.y, b = blockIdx.z, hk = head / p.group;
+    const int slice = blockIdx.x * 128;            // first value channel of the CTA
+    const int v0 = slice + warp * 16;              // and of this warp
+    const int VP = Sh::vpitch(warps);
+    const size_t stage_bytes = Sh::stage_bytes(warps);
+    const DeltaSeq s = delta_seq(p, b);
+    const int chunks = (s.len + DL_C - 1) / DL_C;
+    const long long img = delta_img(p, b);
+    const T* q = reinterpret_cast<const T*>(p.q) + img * p.q_img + (long long)hk * p.dk;
+    const T* k = reinterpret_cast<const T*>(p.k) + img * p.k_img + (long long)hk * p.dk;
+    const T* v = reinterpret_cast<const T*>(p.v) + img * p.v_img + (long long)head * p.dv + slice;
+    T* y = reinterpret_cast<T*>(p.y) + img * p.y_img + (long long)head * p.dv;
+
+    auto stage_k = [&](int st) { return reinterpret_cast<__nv_bfloat16*>(smem + st * stage_bytes); };
+    auto issue = [&](int c, int st) {
+        __nv_bfloat16* K = stage_k(st);
+        __nv_bfloat16* Q = K + NP * PLANE;
+        __nv_bfloat16* Tt = Q + NP * PLANE;
+        __nv_bfloat16* P = Tt + 3 * DL_C * DL_TPITCH;
+        T* V = reinterpret_cast<T*>(P + PP * DL_C * DL_TPITCH);
+        float* vec = reinterpret_cast<float*>(V + DL_C * VP);
+        const size_t rec = (size_t)(s.slot + c) * p.heads_v + head;
+        load_tile(K, PITCH, PLANE, k, p.k_tok, p, s, c * DL_C, DKP, p.dk, tid, nthreads);
+        if (!SAVE) load_tile(Q, PITCH, PLANE, q, p.q_tok, p, s, c * DL_C, DKP, p.dk, tid, nthreads);
+        load_planes(Tt, p.wT + rec * 3 * DL_PLANE, 3, tid, nthreads);
+        if (!SAVE) load_planes(P, p.wP + rec * p.tplanes * DL_PLANE, PP, tid, nthreads);
+        load_raw(V, VP, v, p.v_tok, p, s, c * DL_C, warps * 16, p.dv - slice, tid, nthreads);
+        for (int i = tid; i < DL_VECS / 4; i += nthreads)
+            cp_async16(vec + 4 * i, p.wvec + rec * DL_VECS + 4 * i, true);
+    };
+
+    // S^T: rows are value channels, columns key channels
+    float S[NT][4];
+    const size_t sbase = ((size_t)b * p.heads_v + head) * p.dk * p.dv;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int vc = v0 + gr + (e >> 1) * 8, kc = nt * 8 + tc + (e & 1);
+            S[nt][e] = p.s_in && vc < p.dv && kc < p.dk ? p.s_in[sbase + (size_t)kc * p.dv + vc] : 0.f;
+        }
+
+    if (Sh::STAGES == 2 && chunks > 0) {
+        issue(0, 0);
+        cp_async_commit();
+    }
+    for (int c = 0; c < chunks; ++c) {
+        const int st = Sh::STAGES == 2 ? c & 1 : 0;
+        if (Sh::STAGES == 2) {
+            if (c + 1 < chunks) issue(c + 1, st ^ 1);
+            cp_async_commit();
+            cp_async_wait<1>();
+        } else {
+            issue(c, 0);
+            cp_async_commit();
+            cp_async_wait<0>();
+        }
+        __syncthreads();
+        __nv_bfloat16* K = stage_k(st);
+        __nv_bfloat16* Q = K + NP * PLANE;
+        __nv_bfloat16* Tt = Q + NP * PLANE;
+        __nv_bfloat16* P = Tt + 3 * DL_C * DL_TPITCH;
+        T* V = reinterpret_cast<T*>(P + PP * DL_C * DL_TPITCH);
+        const float* vec = reinterpret_cast<const float*>(V + DL_C * VP);
+        const size_t rec = (size_t)(s.slot + c) * p.heads_v + head;
+
+        if (SAVE) {  // the state entering the chunk, for the gradients
+            float* o = p.wS + rec * p.dv * DKP;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (v0 + gr + h * 8 < p.dv)
+                        *reinterpret_cast<float2*>(o + (size_t)(v0 + gr + h * 8) * DKP + nt * 8 + tc) =
+                            make_float2(S[nt][2 * h], S[nt][2 * h + 1]);
+        }
+
+        // (K S)^T and (Q S)^T
+        float ks[8][4] = {}, o[8][4] = {};
+#pragma unroll
+        for (int kt = 0; kt < DKP / 16; ++kt) {
+            Frag4 sa[3];
+            split_tiles<3>(S[2 * kt], S[2 * kt + 1], sa);
+#pragma unroll
+            for (int nt = 0; nt < 8; nt += 2) {
+                Frag4 f[NP];
+#pragma unroll
+                for (int n = 0; n < NP; ++n) f[n] = load_b(K + n * PLANE, PITCH, nt * 8, kt * 16, lane);
+                mma_terms<3, NP>(ks[nt], ks[nt + 1], sa, f);
+                if (!SAVE) {
+#pragma unroll
+                    for (int n = 0; n < NP; ++n) f[n] = load_b(Q + n * PLANE, PITCH, nt * 8, kt * 16, lane);
+                    // y leaves in bf16: two terms of the state (2^-17) are far below its rounding
+                    mma_terms<3, NP, NP == 1 ? 1 : 2>(o[nt], o[nt + 1], sa, f);
+                }
+            }
+        }
+        // X^T = beta (V - e^G K S)^T
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = nt * 8 + tc + (e & 1);
+                const float x = to_float(V[r * VP + warp * 16 + gr + (e >> 1) * 8]);
+                ks[nt][e] = vec[2 * DL_C + r] * (x - vec[r] * ks[nt][e]);
+                if (!SAVE) o[nt][e] *= p.scale * vec[r];
+            }
+        // W^T = X^T T^T; T has nothing above the diagonal
+        float w[8][4] = {};
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) {
+            Frag4 xa[3];
+            split_tiles<3>(ks[2 * kt], ks[2 * kt + 1], xa);
+#pragma unroll
+            for (int nt = 2 * kt; nt < 8; nt += 2) {
+                Frag4 f[3];
+#pragma unroll
+                for (int n = 0; n < 3; ++n) f[n] = load_b(Tt + n * DL_C * DL_TPITCH, DL_TPITCH, nt * 8, kt * 16, lane);
+                mma_terms<3, 3>(w[nt], w[nt + 1], xa, f);
+            }
+        }
+        if (SAVE) {
+            float* ow = p.wW + rec * DL_C * p.dv;
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int vc = v0 + gr + (e >> 1) * 8;
+                    if (vc < p.dv) ow[(size_t)(nt * 8 + tc + (e & 1)) * p.dv + vc] = w[nt][e];
+                }
+        } else {
+            // y^T = scale e^G (Q S)^T + W^T P^T
+#pragma unroll
+            for (int kt = 0; kt < 4; ++kt) {
+                Frag4 wa[PP];
+                split_tiles<PP>(w[2 * kt], w[2 * kt + 1], wa);
+#pragma unroll
+                for (int nt = 2 * kt; nt < 8; nt += 2) {
+                    Frag4 f[PP];
+#pragma unroll
+                    for (int n = 0; n < PP; ++n) f[n] = load_b(P + n * DL_C * DL_TPITCH, DL_TPITCH, nt * 8, kt * 16, lane);
+                    mma_terms<PP, PP, PP - 1>(o[nt], o[nt + 1], wa, f);
+                }
+            }
+            // through this warp's own columns of V, now read, to whole rows
+            __syncwarp();
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    store_elem(V + (nt * 8 + tc + (e & 1)) * VP + warp * 16 + gr + (e >> 1) * 8, o[nt][e]);
+            __syncwarp();
+            constexpr int VE = 16 / sizeof(T), VR = 16 / VE;
+#pragma unroll
+            for (int i = 0; i < DL_C * VR / 32; ++i) {
+                const int r = (i * 32 + lane) / VR, cc = ((i * 32 + lane) % VR) * VE;
+                const int row = delta_row(p, s, c * DL_C + r);
+                if (row >= 0 && v0 + cc < p.dv)
+                    *reinterpret_cast<uint4*>(y + row * p.y_tok + v0 + cc) =
+                        *reinterpret_cast<const uint4*>(V + r * VP + warp * 16 + cc);
+            }
+        }
+        // S^T = e^{G_C} S^T + (e^{G_C - G} W)^T K
+        const float eC = vec[3 * DL_C];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[nt][e] *= eC;
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[2 * kt + h][e] *= vec[DL_C + (2 * kt + h) * 8 + tc + (e & 1)];
+            Frag4 wa[3];
+            split_tiles<3>(w[2 * kt], w[2 * kt + 1], wa);
+#pragma unroll
+            for (int nt = 0; nt < NT; nt += 2) {
+                Frag4 f[NP];
+#pragma unroll
+                for (int n = 0; n < NP; ++n) f[n] = load_b_t(K + n * PLANE, PITCH, nt * 8, kt * 16, lane);
+                mma_terms<3, NP>(S[nt], S[nt + 1], wa, f);
+            }
+        }
+        __syncthreads();  // the stage is free for the copies of chunk c + 2
+    }
+    if (p.s_out) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int vc = v0 + gr + (e >> 1) * 8, kc = nt * 8 + tc + (e & 1);
+                if (vc < p.dv && kc < p.dk) p.s_out[sbase + (size_t)kc * p.dv + vc] = S[nt][e];
+            }
+    }
+}
+
+// ---- one token ----------------------------------------------------------------------
+// One CTA per row, value head and 32 value channels: 8 lanes hold four channels
+// each of a state row, 16 such groups share the dk rows. The state is read once
+// into registers and written once: bound by those bytes.
+constexpr int DS_COLS = 32, DS_GROUPS = 16, DS_ROWS = 8;  // dk <= 128
+
+template <typename T>
+__global__ void __launch_bounds__(128) delta_step_kernel(const DeltaParams p)
+{
+    __shared__ float kq[2][128];
+    __shared__ float4 part[4][8];
+    const int tid = threadIdx.x, lane8 = tid & 7, grp = tid >> 3, warp = tid >> 5;
+    const int head = blockIdx.y, b = blockIdx.z, hk = head / p.group;
+    const int vc = blockIdx.x * DS_COLS + lane8 * 4;
+    const bool live = vc < p.dv;
+    const size_t sbase = ((size_t)b * p.heads_v + head) * p.dk * p.dv + vc;
+    float4 S[DS_ROWS];
+#pragma unroll
+    for (int i = 0; i < DS_ROWS; ++i) {
+        const int r = i * DS_GROUPS + grp;
+        S[i] = live && r < p.dk ? *reinterpret_cast<const float4*>(p.s_in + sbase + (size_t)r * p.dv)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (tid < p.dk) {
+        kq[0][tid] = to_float(reinterpret_cast<const T*>(p.k)[(long long)b * p.k_img + (long long)hk * p.dk + tid]);
+        kq[1][tid] = to_float(reinterpret_cast<const T*>(p.q)[(long long)b * p.q_img + (long long)hk * p.dk + tid]);
+    }
+    const float x = to_float(reinterpret_cast<const T*>(p.a)[(long long)b * p.a_img + head]) + (p.bias ? p.bias[head] : 0.f);
+    const float decay = expf(delta_decay(p.A[head], x));
+    const float beta = p.beta_scale * delta_sigmoid(to_float(reinterpret_cast<const T*>(p.b)[(long long)b * p.b_img + head]));
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (live) v = load4(reinterpret_cast<const T*>(p.v) + (long long)b * p.v_img + (long long)head * p.dv + vc);
+    __syncthreads();
+
+    // sum over the rows: over the registers, the four groups of a warp, the four warps
+    auto rows_dot = [&](const float* vec) {
+        float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < DS_ROWS; ++i) {
+            const int r = i * DS_GROUPS + grp;
+            const float c = r < p.dk ? vec[r] : 0.f;
+            d.x += c * S[i].x; d.y += c * S[i].y; d.z += c * S[i].z; d.w += c * S[i].w;
+        }
+#pragma unroll
+        for (int o = 8; o < 32; o <<= 1) {
+            d.x += __shfl_xor_sync(0xffffffffu, d.x, o);
+            d.y += __shfl_xor_sync(0xffffffffu, d.y, o);
+            d.z += __shfl_xor_sync(0xffffffffu, d.z, o);
+            d.w += __shfl_xor_sync(0xffffffffu, d.w, o);
+        }
+        if ((tid & 31) < 8) part[warp][lane8] = d;
+        __syncthreads();
+        d = part[0][lane8];
+#pragma unroll
+        for (int w = 1; w < 4; ++w) {
+            const float4 e = part[w][lane8];
+            d.x += e.x; d.y += e.y; d.z += e.z; d.w += e.w;
+        }
+        return d;
+    };
+#pragma unroll
+    for (int i = 0; i < DS_ROWS; ++i) { S[i].x *= decay; S[i].y *= decay; S[i].z *= decay; S[i].w *= decay; }
+    const float4 d = rows_dot(kq[0]);
+    const float4 w = make_float4(beta * (v.x - d.x), beta * (v.y - d.y), beta * (v.z - d.z), beta * (v.w - d.w));
+    __syncthreads();  // part is read before the second sum writes it
+#pragma unroll
+    for (int i = 0; i < DS_ROWS; ++i) {
+        const int r = i * DS_GROUPS + grp;
+        if (r < p.dk) {
+            const float c = kq[0][r];
+            S[i].x += c * w.x; S[i].y += c * w.y; S[i].z += c * w.z; S[i].w += c * w.w;
+            if (live) *reinterpret_cast<float4*>(p.s_out + sbase + (size_t)r * p.dv) = S[i];
+        }
+    }
+    float4 o = rows_dot(kq[1]);
+    if (tid < 8 && live) {
+        o.x *= p.scale; o.y *= p.scale; o.z *= p.scale; o.w *= p.scale;
+        store4(reinterpret_cast<T*>(p.y) + (long long)b * p.y_img + (long long)head * p.dv + vc, o);
+    }
+}
+
+}  // namespace vscan
