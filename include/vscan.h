@@ -497,6 +497,51 @@ vscan_status vscan_delta_workspace_size(const vscan_route* route, const vscan_de
 vscan_status vscan_delta_forward(const vscan_route* route, const vscan_delta_args* args, void* stream);
 
 /*
+ * Gradients of vscan_delta_forward, written (not accumulated): the reverse-mode
+ * derivative of the steps above. Token gradients are dense and in args->dtype, so
+ * that they can be the dy of the pass before; dA, dbias and the state's are
+ * float32. Any output may be NULL when that gradient is not wanted.
+ */
+typedef struct vscan_delta_grads {
+    void* dq;            /* device, [batch][tokens][heads_k][dim_k], 16-byte aligned */
+    void* dk;            /* device, [batch][tokens][heads_k][dim_k], 16-byte aligned */
+    void* dv;            /* device, [batch][tokens][heads_v][dim_v], 16-byte aligned */
+    void* da;            /* device, [batch][tokens][heads_v], w.r.t. the raw step    */
+    void* db;            /* device, [batch][tokens][heads_v], w.r.t. the raw strength */
+    float* dA;           /* device, [heads_v]                                        */
+    float* dbias;        /* device, [heads_v] (also when args->bias is NULL)         */
+    float* d_initial_state;     /* device, [batch][heads_v][dim_k][dim_v]            */
+    const float* d_final_state; /* device, dL/dfinal_state, the same shape, or NULL
+                            for zero; may not be d_initial_state's memory            */
+    void* workspace;     /* device scratch, 16-byte aligned, of at least
+                            vscan_delta_backward_workspace_size() bytes              */
+    uint64_t workspace_bytes;
+} vscan_delta_grads;
+
+/*
+ * Device scratch bytes vscan_delta_backward needs (host only). Per chunk of 64
+ * steps and value head: the forward's scratch, the state entering the chunk and
+ * the gradient of the one leaving it ([dim_v][dim_k rounded up to 32] float32 each)
+ * and two [64][dim_v] float32 arrays; with shared key heads also dq and dk per
+ * value head in float32.
+ */
+vscan_status vscan_delta_backward_workspace_size(const vscan_route* route, const vscan_delta_args* args,
+                                                 uint64_t* bytes);
+
+/*
+ * Backward pass. args are the forward's (args->y, args->final_state and
+ * args->workspace are not used; y's strides are dy's); dy is dL/dy, 16-byte
+ * aligned. Runs the forward recurrence once more, then the chunks in reverse, then
+ * every chunk's token gradients; enqueued on stream (five launches, one more with
+ * shared key heads); allocates nothing; never synchronizes. Rows that no step
+ * visits (ATROUS2, packed sequences) get gradients of 0. All sums have a fixed
+ * order: equal calls give equal bits.
+ * Errors: as vscan_delta_forward; INVALID_ARGUMENT for dy or grads NULL.
+ */
+vscan_status vscan_delta_backward(const vscan_route* route, const vscan_delta_args* args, const void* dy,
+                                  const vscan_delta_grads* grads, void* stream);
+
+/*
  * One token of each of `batch` sequences (tokens must be 1; no route, no
  * seq_offsets): reads initial_state, which must be given, writes the updated
  * state to final_state (which may be the same memory) and y. One launch; no

@@ -22,16 +22,16 @@ ACC_FORWARD = 4 * 48 * 2.0 ** -23
 ACC_BACKWARD = 2 * ACC_FORWARD
 
 
-def close(got, ref, dtype, acc, what=""):
+def close(got, ref, dtype, acc, what="", size=None):
     """got within a rounding to its type plus acc of the tensor's magnitude (its rms, or the
-    element where that is larger) of ref."""
+    element where that is larger, or `size`) of ref."""
     got, ref = got.detach().double().cpu(), ref.detach().double().cpu()
     assert got.shape == ref.shape, (what, got.shape, ref.shape)
     if ref.numel() == 0:
         return
     assert torch.isfinite(got).all(), what
     rms = ref.square().mean().sqrt()
-    bound = half_step(dtype) * ref.abs() + acc * torch.maximum(ref.abs(), rms)
+    bound = half_step(dtype) * ref.abs() + acc * (torch.maximum(ref.abs(), rms) if size is None else size)
     off = ((got - ref).abs() - bound).max()
     worst = ((got - ref).abs() / torch.maximum(ref.abs(), rms).clamp(min=1e-300)).max()
     assert off <= 0, f"{what}: error {worst:.3e} of the magnitude, bound {half_step(dtype):.1e} + {acc:.1e}"
@@ -84,7 +84,8 @@ def delta_inputs(seed, batch, tokens, hk, hv, dk, dv, dtype, correlated=False, d
 
 # ------------------------------------------------------------------ the definition
 def _one(q, k, v, a, b, A, bias, S, scale, beta_scale):
-    """Steps [L, heads, .] of one sequence in float64; q and k per value head."""
+    """Steps [L, heads, .] of one sequence in float64; q and k per value head. A and bias are
+    per head, or per step and head."""
     x = a + (0 if bias is None else bias)
     decay = torch.exp(A * torch.logaddexp(x, torch.zeros_like(x)))
     beta = beta_scale * torch.sigmoid(b)
@@ -123,7 +124,8 @@ def delta_ref(x, *, kind=None, direction=0, h=0, w=0, offsets=None, scale=None, 
             return s * live.reshape((-1,) + (1,) * (s.dim() - 1))
 
         S0 = v.new_zeros(v.shape[2], q.shape[3], v.shape[3]) if state is None else state[n]
-        ys, S = _one(take(q), take(k), take(v), take(x["a"]), take(x["b"]), x["A"], bias, S0, scale, beta_scale)
+        A, c = (z if z is None or z.dim() == 1 else z[i][at] for z in (x["A"], bias))
+        ys, S = _one(take(q), take(k), take(v), take(x["a"]), take(x["b"]), A, c, S0, scale, beta_scale)
         y = y.index_put((torch.tensor(i), at[live]), ys[live])
         states.append(S)
     return y, (torch.stack(states) if states else v.new_zeros(0, v.shape[2], q.shape[3], v.shape[3]))
@@ -149,6 +151,14 @@ def norm_ref(x, weight, norm, eps, inv_freq=None, positions=None, axes=1):
         u, v = y[..., :pairs], y[..., pairs:2 * pairs]
         y = torch.cat([u * t.cos() - v * t.sin(), u * t.sin() + v * t.cos(), y[..., 2 * pairs:]], -1)
     return y
+
+
+def sum_size(terms):
+    """Magnitude of a sum over tokens, per head: each term [batch, tokens, heads] is off by its
+    accumulated error, relative to the larger of itself and the terms' rms, and the errors of a
+    sum add up whatever its terms' signs, so a sum that cancels is off by more of its own value."""
+    rms = terms.square().mean().sqrt()
+    return torch.maximum(terms.abs(), rms).sum((0, 1))
 
 
 def finite_difference(f, x, direction, eps=1e-6):

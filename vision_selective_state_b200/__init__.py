@@ -415,6 +415,6 @@ __all__.append("BackwardPlan")
 
 
 # the matrix-state mixer and the query/key norm that feeds it
-from .delta import delta_forward, delta_step  # noqa: E402
+from .delta import delta_backward, delta_forward, delta_step  # noqa: E402
 
-__all__ += ["delta_forward", "delta_step"]
+__all__ += ["delta_forward", "delta_backward", "delta_step"]

@@ -88,6 +88,14 @@ class VscanDeltaArgs(ctypes.Structure):
     )
 
 
+class VscanDeltaGrads(ctypes.Structure):
+    """Mirror of struct vscan_delta_grads (include/vscan.h)."""
+
+    _fields_ = [(name, ctypes.c_void_p) for name in
+                ("dq", "dk", "dv", "da", "db", "dA", "dbias", "d_initial_state", "d_final_state", "workspace")] + [
+        ("workspace_bytes", ctypes.c_uint64)]
+
+
 class VscanError(RuntimeError):
     def __init__(self, status, message):
         self.status = status
@@ -120,6 +128,8 @@ def _load():
         "vscan_backward": ([p, pa, p, ctypes.POINTER(VscanGrads), p], i32),
         "vscan_delta_workspace_size": ([p, pd, ctypes.POINTER(u64)], i32),
         "vscan_delta_forward": ([p, pd, p], i32),
+        "vscan_delta_backward_workspace_size": ([p, pd, ctypes.POINTER(u64)], i32),
+        "vscan_delta_backward": ([p, pd, p, ctypes.POINTER(VscanDeltaGrads), p], i32),
         "vscan_delta_step": ([pd, p], i32),
         "vscan_last_error": ([], ctypes.c_char_p),
         "vscan_status_string": ([i32], ctypes.c_char_p),

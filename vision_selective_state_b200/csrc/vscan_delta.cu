@@ -5,6 +5,7 @@
 
 #include "vscan.h"
 #include "vscan_delta.cuh"
+#include "vscan_delta_grad.cuh"
 #include "vscan_host.h"
 
 namespace {
@@ -123,6 +124,7 @@ bool empty(const vscan_delta_args* a) { return a->batch == 0; }
 
 struct Layout {
     size_t T, P, vec, total;
+    size_t L, S, dS, W, dX, part, dq, dk, grad_total;  // backward
 };
 
 Layout forward_layout(const vscan_route* r, const vscan_delta_args* a, int pplanes)
@@ -133,6 +135,27 @@ Layout forward_layout(const vscan_route* r, const vscan_delta_args* a, int pplan
     l.P = l.T + round256(n * 3 * vscan::DL_PLANE * 2);
     l.vec = l.P + round256(n * pplanes * vscan::DL_PLANE * 2);
     l.total = l.vec + round256(n * vscan::DL_VECS * 4);
+    return l;
+}
+
+// The forward's scratch with P in three planes, and what the walks leave for the
+// per-chunk gradients.
+Layout backward_layout(const vscan_route* r, const vscan_delta_args* a)
+{
+    Layout l = forward_layout(r, a, 3);
+    const size_t n = (size_t)slots_of(r, a) * a->heads_v, state = (size_t)a->dim_v * padded_dim_k(a->dim_k) * 4;
+    const size_t rows = (size_t)DL_C * a->dim_v * 4;
+    l.L = l.total;
+    l.S = l.L + round256(n * vscan::DL_PLANE * 4);
+    l.dS = l.S + round256(n * state);
+    l.W = l.dS + round256(n * state);
+    l.dX = l.W + round256(n * rows);
+    l.part = l.dX + round256(n * rows);
+    l.dq = l.part + round256(n * 8);
+    const size_t images = a->seq_offsets ? 1 : a->batch;
+    const size_t shared = a->heads_v == a->heads_k ? 0 : round256(images * a->tokens * a->heads_v * a->dim_k * 4);
+    l.dk = l.dq + shared;
+    l.grad_total = l.dk + shared;
     return l;
 }
 
@@ -204,6 +227,36 @@ cudaError_t run_forward(const DeltaParams& p, cudaStream_t stream)
     return launch_scan<T, DKP, false>(p, stream);
 }
 
+template <typename T, int DKP>
+cudaError_t run_backward(const DeltaParams& p, cudaStream_t stream)
+{
+    static int done_r[kAttrDevices], done_g[kAttrDevices];
+    cudaError_t e;
+    if (p.tokens > 0 && p.slots > 0) {
+        if ((e = launch_prep<T, DKP>(p, stream)) != cudaSuccess) return e;
+        if ((e = launch_scan<T, DKP, true>(p, stream)) != cudaSuccess) return e;
+    }
+    using Sh = vscan::RscanShape<T, DKP>;
+    const int warps = p.dv >= 128 ? 8 : (p.dv + 15) / 16;
+    size_t smem = Sh::STAGES * Sh::stage_bytes(warps);
+    if ((e = set_smem_once(vscan::delta_rscan_kernel<T, DKP>, (int)smem, done_r, kAttrDevices)) != cudaSuccess) return e;
+    vscan::delta_rscan_kernel<T, DKP><<<dim3((p.dv + 127) / 128, p.heads_v, p.batch), warps * 32, smem, stream>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (p.tokens > 0 && p.slots > 0) {
+        smem = vscan::GradShape<T, DKP>::smem;
+        if ((e = set_smem_once(vscan::delta_grad_kernel<T, DKP>, (int)smem, done_g, kAttrDevices)) != cudaSuccess) return e;
+        vscan::delta_grad_kernel<T, DKP><<<dim3((unsigned)p.slots, p.heads_v), 256, smem, stream>>>(p);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if (p.wdq && (p.dq || p.dkey)) {
+            const long long vecs = (long long)(p.offsets ? 1 : p.batch) * p.tokens * p.heads_k * (p.dk / 4);
+            vscan::delta_group_kernel<T><<<dim3((unsigned)((vecs + 255) / 256), 2), 256, 0, stream>>>(p, vecs);
+            if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        }
+    }
+    if (p.dA || p.dbias) vscan::delta_param_grad_kernel<<<p.heads_v, 256, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
 // f(width) with the I/O type and the padded key width as template arguments.
 #define DELTA_DISPATCH(FN, a, ...)                                                              \
     (a->dtype == VSCAN_F32                                                                      \
@@ -253,6 +306,94 @@ vscan_status vscan_delta_forward(const vscan_route* route, const vscan_delta_arg
     p.wvec = reinterpret_cast<float*>(ws + l.vec);
     const cudaError_t e = DELTA_DISPATCH(run_forward, args, p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? VSCAN_OK : cuda_fail(e, "vscan_delta_forward");
+}
+
+vscan_status vscan_delta_backward_workspace_size(const vscan_route* route, const vscan_delta_args* args, uint64_t* bytes)
+{
+    if (!bytes) return fail(VSCAN_ERR_INVALID_ARGUMENT, "bytes is NULL");
+    const vscan_status st = check_shape(route, args);
+    if (st != VSCAN_OK) return st;
+    *bytes = empty(args) ? 0 : backward_layout(route, args).grad_total;
+    return VSCAN_OK;
+}
+
+vscan_status vscan_delta_backward(const vscan_route* route, const vscan_delta_args* args, const void* dy,
+                                  const vscan_delta_grads* grads, void* stream)
+{
+    vscan_status st = check_shape(route, args);
+    if (st != VSCAN_OK) return st;
+    if (!grads) return fail(VSCAN_ERR_INVALID_ARGUMENT, "grads is NULL");
+    const bool none = empty(args) || args->tokens == 0;
+    if (!none && (st = check_pointers(args, dy)) != VSCAN_OK) return st;
+    if (!aligned16(grads->dq) || !aligned16(grads->dk) || !aligned16(grads->dv) || !aligned16(grads->d_initial_state) ||
+        !aligned16(grads->d_final_state) || !aligned16(grads->workspace))
+        return fail(VSCAN_ERR_ALIGNMENT, "dq, dk, dv, the states' gradients and the workspace must be 16-byte aligned");
+    const uintptr_t el = args->dtype == VSCAN_F32 ? 3 : 1;
+    if (((uintptr_t)grads->da & el) || ((uintptr_t)grads->db & el) || ((uintptr_t)grads->dA & 3) ||
+        ((uintptr_t)grads->dbias & 3))
+        return fail(VSCAN_ERR_ALIGNMENT, "da, db, dA or dbias is not aligned to its element");
+    if (grads->d_final_state && grads->d_final_state == grads->d_initial_state)
+        return fail(VSCAN_ERR_INVALID_ARGUMENT, "d_final_state and d_initial_state must not be the same memory");
+    const Layout l = backward_layout(route, args);
+    if (!none && (!grads->workspace || grads->workspace_bytes < l.grad_total))
+        return fail(VSCAN_ERR_WORKSPACE, "workspace of %llu bytes, %llu needed", (unsigned long long)grads->workspace_bytes,
+                    (unsigned long long)l.grad_total);
+    if (slots_of(route, args) > 0x7fffffffLL)
+        return fail(VSCAN_ERR_UNSUPPORTED, "more than 2^31 chunks of %d steps", DL_C);
+    NvtxRange range("vscan_delta_backward");
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    auto zero = [&](void* ptr, size_t bytes) {
+        if (ptr && bytes && e == cudaSuccess) e = cudaMemsetAsync(ptr, 0, bytes, s);
+    };
+    if (none) {  // no step: the state's gradient passes through
+        zero(grads->dA, (size_t)args->heads_v * 4);
+        zero(grads->dbias, (size_t)args->heads_v * 4);
+        const size_t bytes = (size_t)args->batch * args->heads_v * args->dim_k * args->dim_v * 4;
+        if (grads->d_initial_state && grads->d_final_state && bytes && e == cudaSuccess)
+            e = cudaMemcpyAsync(grads->d_initial_state, grads->d_final_state, bytes, cudaMemcpyDeviceToDevice, s);
+        else
+            zero(grads->d_initial_state, bytes);
+        return e == cudaSuccess ? VSCAN_OK : cuda_fail(e, "vscan_delta_backward");
+    }
+    DeltaParams p = make_params(route, args);
+    char* ws = static_cast<char*>(grads->workspace);
+    p.s_out = nullptr;
+    p.tplanes = 3;
+    p.wT = reinterpret_cast<__nv_bfloat16*>(ws + l.T);
+    p.wP = reinterpret_cast<__nv_bfloat16*>(ws + l.P);
+    p.wvec = reinterpret_cast<float*>(ws + l.vec);
+    p.wL = reinterpret_cast<float*>(ws + l.L);
+    p.wS = reinterpret_cast<float*>(ws + l.S);
+    p.wdS = reinterpret_cast<float*>(ws + l.dS);
+    p.wW = reinterpret_cast<float*>(ws + l.W);
+    p.wdX = reinterpret_cast<float*>(ws + l.dX);
+    p.wpart = reinterpret_cast<float*>(ws + l.part);
+    if (p.group > 1) {
+        p.wdq = reinterpret_cast<float*>(ws + l.dq);
+        p.wdk = reinterpret_cast<float*>(ws + l.dk);
+    }
+    p.dy = dy;
+    p.ds_in = grads->d_final_state;
+    p.ds_out = grads->d_initial_state;
+    p.dq = grads->dq; p.dkey = grads->dk; p.dvalue = grads->dv;
+    p.da = grads->da; p.db = grads->db;
+    p.dA = grads->dA; p.dbias = grads->dbias;
+    if (args->seq_offsets || (route && route->g.kind == vscan::RK_ATROUS2)) {
+        // rows without a step, and chunk slots without a chunk
+        const size_t el_bytes = vscan_host::elem_bytes(args->dtype);
+        const size_t rows = (size_t)(args->seq_offsets ? 1 : args->batch) * args->tokens;
+        zero(grads->dq, rows * args->heads_k * args->dim_k * el_bytes);
+        zero(grads->dk, rows * args->heads_k * args->dim_k * el_bytes);
+        zero(grads->dv, rows * args->heads_v * args->dim_v * el_bytes);
+        zero(grads->da, rows * args->heads_v * el_bytes);
+        zero(grads->db, rows * args->heads_v * el_bytes);
+        zero(p.wpart, (size_t)p.slots * p.heads_v * 8);
+        if (p.wdq) zero(p.wdq, l.grad_total - l.dq);
+        if (e != cudaSuccess) return cuda_fail(e, "vscan_delta_backward");
+    }
+    e = DELTA_DISPATCH(run_backward, args, p, s);
+    return e == cudaSuccess ? VSCAN_OK : cuda_fail(e, "vscan_delta_backward");
 }
 
 vscan_status vscan_delta_step(const vscan_delta_args* args, void* stream)

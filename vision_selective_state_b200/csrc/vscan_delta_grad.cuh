@@ -1,0 +1,710 @@
+// Gated delta rule: device code of the backward pass.
+//
+// With dO the gradient of y and dS that of the state leaving a chunk, the chunk's
+// forward (see vscan_delta.cuh) turned round is
+//
+//   dW = P^T dO + (e^{G_C - G_j} k_j) dS          dX = T^T dW          dV = beta dX
+//   dS0 = e^{G_C} dS + sum_i scale e^{G_i} q_i dO_i^T - sum_i e^{G_i} k_i dV_i^T
+//   E_ij = scale e^{G_i - G_j} dO_i.w_j (j <= i)   M_ij = -e^{G_i - G_j} dV_i.w_j (j < i)
+//   dq_i  = scale e^{G_i} S0 dO_i + sum_j E_ij k_j
+//   dkr_i = -e^{G_i} S0 dV_i + sum_j M_ij k_j                        (k_i as the key that reads)
+//   dkc_j = e^{G_C - G_j} dS w_j + sum_i E_ij q_i + sum_i M_ij k_i   (k_j as the key that writes)
+//   dg_i  = sum_{r >= i > j} H_rj + sum_{r >= i} U_r + sum_{j < i} V_j + e^{G_C} <dS, S0>
+//           H_rj = E_rj q_r.k_j + M_rj k_r.k_j
+//           U_r = scale e^{G_r} q_r.S0 dO_r - e^{G_r} k_r.S0 dV_r      V_j = e^{G_C - G_j} k_j.dS w_j
+//   db_i  = (dX_i.w_i)(1 - sigmoid(b_i))
+//
+// The first two lines need the chunks in order and only this head's slice of the
+// value channels (delta_rscan_kernel); the rest is independent chunk by chunk
+// (delta_grad_kernel). dg_i gathers the terms whose decay factor spans step i; the
+// pairs (r, j) that do are the row sums of H from i on less its column sums from i
+// on, in which a pair that lies wholly behind i cancels: both sums run in float64
+// over the same rounded H, so it cancels to 2^-53 of itself. (q.dq + k.dk over the
+// finished gradients has the same value, but its cancelling parts are rounded
+// apart, which strong decays - dg small, A large - turn into an error of da.)
+#pragma once
+
+#include "vscan_delta.cuh"
+
+namespace vscan {
+
+// ---- the walk backwards ---------------------------------------------------------------
+template <typename T, int DKP>
+struct RscanShape {
+    static constexpr int NP = DeltaIo<T>::planes;
+    static constexpr int STAGES = NP == 1 ? 2 : 1;
+    static constexpr int pitch = DKP + 8;
+    static constexpr int plane = DL_C * pitch;
+    static __host__ __device__ constexpr int vpitch(int warps) { return warps * 16 + 16 / (int)sizeof(T); }
+    static __host__ __device__ constexpr size_t stage_bytes(int warps)
+    {
+        return (size_t)2 * NP * plane * 2 + (size_t)DL_C * vpitch(warps) * sizeof(T) + (size_t)6 * DL_C * DL_TPITCH * 2 +
+               DL_SCANVECS * 4;
+    }
+};
+
+template <typename T, int DKP>
+__global__ void __launch_bounds__(256) delta_rscan_kernel(const DeltaParams p)
+{
+    using Sh = RscanShape<T, DKP>;
+    constexpr int NP = Sh::NP, PITCH = Sh::pitch, PLANE = Sh::plane, NT = DKP / 8;
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int tid = threadIdx.x, nthreads = blockDim.x, warps = nthreads >> 5, warp = tid >> 5, lane = tid & 31;
+    const int gr = lane >> 2, tc = (lane & 3) * 2;
+    const int head = blockIdx.y, b = blockIdx.z, hk = head / p.group;
+    const int slice = blockIdx.x * 128, v0 = slice + warp * 16;
+    const int VP = Sh::vpitch(warps);
+    const size_t stage_bytes = Sh::stage_bytes(warps);
+    const DeltaSeq s = delta_seq(p, b);
+    const int chunks = (s.len + DL_C - 1) / DL_C;
+    const long long img = delta_img(p, b);
+    const T* q = reinterpret_cast<const T*>(p.q) + img * p.q_img + (long long)hk * p.dk;
+    const T* k = reinterpret_cast<const T*>(p.k) + img * p.k_img + (long long)hk * p.dk;
+    const T* dy = reinterpret_cast<const T*>(p.dy) + img * p.y_img + (long long)head * p.dv + slice;
+
+    auto stage_k = [&](int st) { return reinterpret_cast<__nv_bfloat16*>(smem + st * stage_bytes); };
+    auto issue = [&](int c, int st) {
+        __nv_bfloat16* K = stage_k(st);
+        __nv_bfloat16* Q = K + NP * PLANE;
+        __nv_bfloat16* Tt = Q + NP * PLANE;
+        T* O = reinterpret_cast<T*>(Tt + 6 * DL_C * DL_TPITCH);
+        float* vec = reinterpret_cast<float*>(O + DL_C * VP);
+        const size_t rec = (size_t)(s.slot + c) * p.heads_v + head;
+        load_tile(K, PITCH, PLANE, k, p.k_tok, p, s, c * DL_C, DKP, p.dk, tid, nthreads);
+        load_tile(Q, PITCH, PLANE, q, p.q_tok, p, s, c * DL_C, DKP, p.dk, tid, nthreads);
+        load_planes(Tt, p.wT + rec * 3 * DL_PLANE, 3, tid, nthreads);
+        load_planes(Tt + 3 * DL_C * DL_TPITCH, p.wP + rec * 3 * DL_PLANE, 3, tid, nthreads);
+        load_raw(O, VP, dy, p.y_tok, p, s, c * DL_C, warps * 16, p.dv - slice, tid, nthreads);
+        for (int i = tid; i < DL_SCANVECS / 4; i += nthreads)
+            cp_async16(vec + 4 * i, p.wvec + rec * DL_VECS + 4 * i, true);
+    };
+
+    float S[NT][4];  // dS^T
+    const size_t sbase = ((size_t)b * p.heads_v + head) * p.dk * p.dv;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int vc = v0 + gr + (e >> 1) * 8, kc = nt * 8 + tc + (e & 1);
+            S[nt][e] = p.ds_in && vc < p.dv && kc < p.dk ? p.ds_in[sbase + (size_t)kc * p.dv + vc] : 0.f;
+        }
+
+    if (Sh::STAGES == 2 && chunks > 0) {
+        issue(chunks - 1, 0);
+        cp_async_commit();
+    }
+    for (int n = 0; n < chunks; ++n) {
+        const int c = chunks - 1 - n, st = Sh::STAGES == 2 ? n & 1 : 0;
+        if (Sh::STAGES == 2) {
+            if (c > 0) issue(c - 1, st ^ 1);
+            cp_async_commit();
+            cp_async_wait<1>();
+        } else {
+            issue(c, 0);
+            cp_async_commit();
+            cp_async_wait<0>();
+        }
+        __syncthreads();
+        __nv_bfloat16* K = stage_k(st);
+        __nv_bfloat16* Q = K + NP * PLANE;
+        __nv_bfloat16* Tt = Q + NP * PLANE;
+        __nv_bfloat16* P = Tt + 3 * DL_C * DL_TPITCH;
+        T* O = reinterpret_cast<T*>(P + 3 * DL_C * DL_TPITCH);
+        const float* vec = reinterpret_cast<const float*>(O + DL_C * VP);
+        const size_t rec = (size_t)(s.slot + c) * p.heads_v + head;
+
+        {
+            float* o = p.wdS + rec * p.dv * DKP;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (v0 + gr + h * 8 < p.dv)
+                        *reinterpret_cast<float2*>(o + (size_t)(v0 + gr + h * 8) * DKP + nt * 8 + tc) =
+                            make_float2(S[nt][2 * h], S[nt][2 * h + 1]);
+        }
+        // dW^T = e^{G_C - G} (dS^T K^T) + dO^T P
+        float dw[8][4] = {};
+#pragma unroll
+        for (int kt = 0; kt < DKP / 16; ++kt) {
+            Frag4 sa[3];
+            split_tiles<3>(S[2 * kt], S[2 * kt + 1], sa);
+#pragma unroll
+            for (int nt = 0; nt < 8; nt += 2) {
+                Frag4 f[NP];
+#pragma unroll
+                for (int i = 0; i < NP; ++i) f[i] = load_b(K + i * PLANE, PITCH, nt * 8, kt * 16, lane);
+                mma_terms<3, NP>(dw[nt], dw[nt + 1], sa, f);
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dw[nt][e] *= vec[DL_C + nt * 8 + tc + (e & 1)];
+        // a pair of 8-step tiles of dO^T
+        auto tile = [&](int kt, float (&lo)[4], float (&hi)[4]) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int col = warp * 16 + gr + (e >> 1) * 8;
+                lo[e] = to_float(O[(kt * 16 + tc + (e & 1)) * VP + col]);
+                hi[e] = to_float(O[(kt * 16 + 8 + tc + (e & 1)) * VP + col]);
+            }
+        };
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) {
+            float lo[4], hi[4];
+            tile(kt, lo, hi);
+            Frag4 oa[NP];
+            split_tiles<NP>(lo, hi, oa);
+#pragma unroll
+            for (int nt = 0; nt <= 2 * kt; nt += 2) {
+                Frag4 f[3];
+#pragma unroll
+                for (int i = 0; i < 3; ++i) f[i] = load_b_t(P + i * DL_C * DL_TPITCH, DL_TPITCH, nt * 8, kt * 16, lane);
+                mma_terms<NP, 3>(dw[nt], dw[nt + 1], oa, f);
+            }
+        }
+        // dX^T = dW^T T
+        float dx[8][4] = {};
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) {
+            Frag4 wa[3];
+            split_tiles<3>(dw[2 * kt], dw[2 * kt + 1], wa);
+#pragma unroll
+            for (int nt = 0; nt <= 2 * kt; nt += 2) {
+                Frag4 f[3];
+#pragma unroll
+                for (int i = 0; i < 3; ++i) f[i] = load_b_t(Tt + i * DL_C * DL_TPITCH, DL_TPITCH, nt * 8, kt * 16, lane);
+                mma_terms<3, 3>(dx[nt], dx[nt + 1], wa, f);
+            }
+        }
+        // dS^T = e^{G_C} dS^T + (scale e^G dO)^T Q - (e^G dV)^T K
+        const float eC = vec[3 * DL_C];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[nt][e] *= eC;
+        float* ox = p.wdX + rec * DL_C * p.dv;
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) {
+            float lo[4], hi[4];
+            tile(kt, lo, hi);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                lo[e] *= p.scale * vec[kt * 16 + tc + (e & 1)];
+                hi[e] *= p.scale * vec[kt * 16 + 8 + tc + (e & 1)];
+            }
+            Frag4 oa[3], va[3];
+            split_tiles<3>(lo, hi, oa);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = (2 * kt + h) * 8 + tc + (e & 1), vc = v0 + gr + (e >> 1) * 8;
+                    float& x = dx[2 * kt + h][e];
+                    if (vc < p.dv) ox[(size_t)r * p.dv + vc] = x;
+                    x *= vec[2 * DL_C + r];  // dV from here on
+                    (h ? hi : lo)[e] = -vec[r] * x;
+                }
+            split_tiles<3>(lo, hi, va);
+#pragma unroll
+            for (int nt = 0; nt < NT; nt += 2) {
+                Frag4 f[NP];
+#pragma unroll
+                for (int i = 0; i < NP; ++i) f[i] = load_b_t(Q + i * PLANE, PITCH, nt * 8, kt * 16, lane);
+                mma_terms<3, NP>(S[nt], S[nt + 1], oa, f);
+#pragma unroll
+                for (int i = 0; i < NP; ++i) f[i] = load_b_t(K + i * PLANE, PITCH, nt * 8, kt * 16, lane);
+                mma_terms<3, NP>(S[nt], S[nt + 1], va, f);
+            }
+        }
+        if (p.dvalue) {  // through this warp's own columns of dO, now read, to whole rows
+            T* o = reinterpret_cast<T*>(p.dvalue) + (img * p.tokens * p.heads_v + head) * (long long)p.dv;
+            __syncwarp();
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    store_elem(O + (nt * 8 + tc + (e & 1)) * VP + warp * 16 + gr + (e >> 1) * 8, dx[nt][e]);
+            __syncwarp();
+            constexpr int VE = 16 / sizeof(T), VR = 16 / VE;
+#pragma unroll
+            for (int i = 0; i < DL_C * VR / 32; ++i) {
+                const int r = (i * 32 + lane) / VR, cc = ((i * 32 + lane) % VR) * VE;
+                const int row = delta_row(p, s, c * DL_C + r);
+                if (row >= 0 && v0 + cc < p.dv)
+                    *reinterpret_cast<uint4*>(o + (long long)row * p.heads_v * p.dv + v0 + cc) =
+                        *reinterpret_cast<const uint4*>(O + r * VP + warp * 16 + cc);
+            }
+        }
+        __syncthreads();
+    }
+    if (p.ds_out) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int vc = v0 + gr + (e >> 1) * 8, kc = nt * 8 + tc + (e & 1);
+                if (vc < p.dv && kc < p.dk) p.ds_out[sbase + (size_t)kc * p.dv + vc] = S[nt][e];
+            }
+    }
+}
+
+// ---- per-chunk gradients -------------------------------------------------------------
+// One CTA of eight warps per chunk and value head: four row blocks of 16 steps
+// times two halves of the key channels (of the steps j for E and M). The states
+// pass through shared memory in slabs of 64 value channels, split into bf16
+// terms once for all warps; dO, X's gradient and W go to registers directly.
+template <typename T, int DKP>
+struct GradShape {
+    static constexpr int NP = DeltaIo<T>::planes;
+    static constexpr int pitch = DKP + 8;
+    static constexpr int plane = DL_C * pitch;
+    // K, Q, a slab of a state in three planes; E and M in three planes each; row sums
+    static constexpr size_t smem = (size_t)(2 * NP + 3) * plane * 2 + (size_t)6 * DL_C * DL_TPITCH * 2 +
+                                   6 * DL_C * 8 + (5 * DL_C + 16) * 4;
+};
+
+__device__ __forceinline__ float2 load_pair(const float* p) { return __ldg(reinterpret_cast<const float2*>(p)); }
+__device__ __forceinline__ float2 load_pair(const __nv_bfloat16* p)
+{
+    const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(p));
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+__device__ __forceinline__ void store_pair(float* p, float x, float y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); }
+__device__ __forceinline__ void store_pair(__nv_bfloat16* p, float x, float y)
+{
+    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(x, y);
+}
+
+template <typename T, int DKP>
+__global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaParams p)
+{
+    using Sh = GradShape<T, DKP>;
+    constexpr int NP = Sh::NP, PITCH = Sh::pitch, PLANE = Sh::plane;
+    constexpr int NH = DKP / 16;  // 8-wide tiles in half of the key channels (2 at DKP = 32)
+    extern __shared__ __align__(16) unsigned char smem[];
+    double* hrow = reinterpret_cast<double*>(smem);  // [2 halves][64] row sums of H
+    double* hcol = hrow + 2 * DL_C;                  // [4 row blocks][64] column sums of H
+    float* rows = reinterpret_cast<float*>(hcol + 4 * DL_C);  // [2 halves][64] U, then V; [64] dX.w
+    float* red = rows + 5 * DL_C;                    // [8] <dS, S0>
+    __nv_bfloat16* K = reinterpret_cast<__nv_bfloat16*>(red + 16);
+    __nv_bfloat16* Q = K + NP * PLANE;
+    __nv_bfloat16* St = Q + NP * PLANE;
+    __nv_bfloat16* E = St + 3 * PLANE;
+    __nv_bfloat16* M = E + 3 * DL_C * DL_TPITCH;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tc = (lane & 3) * 2;
+    const int head = blockIdx.y, hk = head / p.group;
+    const int m0 = (warp & 3) * 16, half = warp >> 2, n0 = half * (DKP / 2);
+
+    int b;
+    if (p.offsets) {
+        int lo = 0, hi = p.batch;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (delta_seq(p, mid).slot <= (long long)blockIdx.x) lo = mid; else hi = mid;
+        }
+        b = lo;
+    } else {
+        b = blockIdx.x / p.chunks;
+    }
+    const DeltaSeq s = delta_seq(p, b);
+    const long long c = (long long)blockIdx.x - s.slot;
+    if (c < 0 || c * DL_C >= s.len) return;
+    const int t0 = (int)c * DL_C;
+    const long long img = delta_img(p, b);
+    const size_t rec = (size_t)blockIdx.x * p.heads_v + head;
+    const float* vec = p.wvec + rec * DL_VECS;
+    const float* wS = p.wS + rec * p.dv * DKP;
+    const float* wdS = p.wdS + rec * p.dv * DKP;
+    const float* wW = p.wW + rec * DL_C * p.dv;
+    const float* wdX = p.wdX + rec * DL_C * p.dv;
+
+    load_tile(K, PITCH, PLANE, reinterpret_cast<const T*>(p.k) + img * p.k_img + (long long)hk * p.dk, p.k_tok, p, s, t0,
+              DKP, p.dk, tid, 256);
+    load_tile(Q, PITCH, PLANE, reinterpret_cast<const T*>(p.q) + img * p.q_img + (long long)hk * p.dk, p.q_tok, p, s, t0,
+              DKP, p.dk, tid, 256);
+    cp_async_commit();
+
+    // this thread's two rows of the chunk
+    const int r0 = m0 + gr, r1 = r0 + 8;
+    const int row0 = delta_row(p, s, t0 + r0), row1 = delta_row(p, s, t0 + r1);
+    const T* dy = reinterpret_cast<const T*>(p.dy) + img * p.y_img + (long long)head * p.dv;
+    const float eG0 = vec[r0], eG1 = vec[r1], eD0 = vec[DL_C + r0], eD1 = vec[DL_C + r1];
+    const float beta0 = vec[2 * DL_C + r0], beta1 = vec[2 * DL_C + r1];
+
+    float dq[NH][4] = {}, dkr[NH][4] = {}, dkc[NH][4] = {}, e[4][4] = {}, m[4][4] = {};
+    float xw0 = 0.f, xw1 = 0.f, dots = 0.f;
+    for (int slab = 0; slab < p.dv; slab += DL_C) {
+        const int cols = min(DL_C, p.dv - slab);
+        auto load_state = [&](const float* src, const float* other) {
+            for (int i = tid; i < DL_C * (DKP / 4); i += 256) {
+                const int r = i / (DKP / 4), cc = (i - r * (DKP / 4)) * 4;
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (r < cols) {
+                    x = __ldg(reinterpret_cast<const float4*>(src + (size_t)(slab + r) * DKP + cc));
+                    if (other) {
+                        const float4 z = __ldg(reinterpret_cast<const float4*>(other + (size_t)(slab + r) * DKP + cc));
+                        dots += x.x * z.x + x.y * z.y + x.z * z.z + x.w * z.w;
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < 3; ++n) {
+                    uint2 u;
+                    u.x = split_bf16(x.x, x.y);
+                    u.y = split_bf16(x.z, x.w);
+                    *reinterpret_cast<uint2*>(St + n * PLANE + r * PITCH + cc) = u;
+                }
+            }
+        };
+        // rows r0, r1 at columns col and col + 8 of a [64][dv] array, as two C tiles
+        auto rows_of = [&](const float* src, int col, float (&lo)[4], float (&hi)[4]) {
+            const float2 z = make_float2(0.f, 0.f);
+            const float2 a = col < p.dv ? load_pair(src + (size_t)r0 * p.dv + col) : z;
+            const float2 bb = col < p.dv ? load_pair(src + (size_t)r1 * p.dv + col) : z;
+            const float2 cc = col + 8 < p.dv ? load_pair(src + (size_t)r0 * p.dv + col + 8) : z;
+            const float2 d = col + 8 < p.dv ? load_pair(src + (size_t)r1 * p.dv + col + 8) : z;
+            lo[0] = a.x; lo[1] = a.y; lo[2] = bb.x; lo[3] = bb.y;
+            hi[0] = cc.x; hi[1] = cc.y; hi[2] = d.x; hi[3] = d.y;
+        };
+        load_state(wS, nullptr);
+        cp_async_wait<0>();
+        __syncthreads();
+        for (int kt = 0; kt * 16 < cols; ++kt) {
+            const int col = slab + kt * 16 + tc;
+            float lo[4], hi[4], wl[4], wh[4];
+            Frag4 oa[NP], va[3];
+            {
+                const float2 z = make_float2(0.f, 0.f);
+                const float2 a = row0 >= 0 && col < p.dv ? load_pair(dy + row0 * p.y_tok + col) : z;
+                const float2 bb = row1 >= 0 && col < p.dv ? load_pair(dy + row1 * p.y_tok + col) : z;
+                const float2 cc = row0 >= 0 && col + 8 < p.dv ? load_pair(dy + row0 * p.y_tok + col + 8) : z;
+                const float2 d = row1 >= 0 && col + 8 < p.dv ? load_pair(dy + row1 * p.y_tok + col + 8) : z;
+                lo[0] = a.x; lo[1] = a.y; lo[2] = bb.x; lo[3] = bb.y;
+                hi[0] = cc.x; hi[1] = cc.y; hi[2] = d.x; hi[3] = d.y;
+            }
+            split_tiles<NP>(lo, hi, oa);
+            rows_of(wdX, col, lo, hi);
+            rows_of(wW, col, wl, wh);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                xw0 += lo[i] * wl[i] + hi[i] * wh[i];
+                xw1 += lo[2 + i] * wl[2 + i] + hi[2 + i] * wh[2 + i];
+                lo[i] *= beta0; hi[i] *= beta0;
+                lo[2 + i] *= beta1; hi[2 + i] *= beta1;
+            }
+            split_tiles<3>(lo, hi, va);
+            // dO S0^T and dV S0^T
+#pragma unroll
+            for (int nt = 0; nt < NH; nt += 2) {
+                Frag4 f[3];
+#pragma unroll
+                for (int n = 0; n < 3; ++n) f[n] = load_b_t(St + n * PLANE, PITCH, n0 + nt * 8, kt * 16, lane);
+                mma_terms<NP, 3>(dq[nt], dq[nt + 1], oa, f);
+                mma_terms<3, 3>(dkr[nt], dkr[nt + 1], va, f);
+            }
+            // dO W^T and dV W^T, columns 32 half .. of the steps j up to this row block
+#pragma unroll
+            for (int nt = 0; nt < 4; nt += 2) {
+                const int j = half * 32 + nt * 8;
+                if (j <= m0 + 15) {
+                    float b0[4], b1[4];  // step j + gr, then j + 8 + gr: channels col.. and col + 8..
+                    const float2 z = make_float2(0.f, 0.f);
+                    const float2 w00 = col < p.dv ? load_pair(wW + (size_t)(j + gr) * p.dv + col) : z;
+                    const float2 w01 = col + 8 < p.dv ? load_pair(wW + (size_t)(j + gr) * p.dv + col + 8) : z;
+                    const float2 w10 = col < p.dv ? load_pair(wW + (size_t)(j + 8 + gr) * p.dv + col) : z;
+                    const float2 w11 = col + 8 < p.dv ? load_pair(wW + (size_t)(j + 8 + gr) * p.dv + col + 8) : z;
+                    b0[0] = w00.x; b0[1] = w00.y; b0[2] = w01.x; b0[3] = w01.y;
+                    b1[0] = w10.x; b1[1] = w10.y; b1[2] = w11.x; b1[3] = w11.y;
+                    Frag4 f[3];
+                    split_tiles<3>(b0, b1, f);
+                    mma_terms<NP, 3>(e[nt], e[nt + 1], oa, f);
+                    mma_terms<3, 3>(m[nt], m[nt + 1], va, f);
+                }
+            }
+        }
+        __syncthreads();
+        load_state(wdS, wS);
+        __syncthreads();
+        for (int kt = 0; kt * 16 < cols; ++kt) {  // W dS^T
+            float lo[4], hi[4];
+            rows_of(wW, slab + kt * 16 + tc, lo, hi);
+            Frag4 wa[3];
+            split_tiles<3>(lo, hi, wa);
+#pragma unroll
+            for (int nt = 0; nt < NH; nt += 2) {
+                Frag4 f[3];
+#pragma unroll
+                for (int n = 0; n < 3; ++n) f[n] = load_b_t(St + n * PLANE, PITCH, n0 + nt * 8, kt * 16, lane);
+                mma_terms<3, 3>(dkc[nt], dkc[nt + 1], wa, f);
+            }
+        }
+        __syncthreads();
+    }
+
+    // the decays, and E and M to shared memory
+    auto k_at = [&](const __nv_bfloat16* t, int r, int col) {  // a pair of the tile's values
+        float2 x = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int n = NP - 1; n >= 0; --n) {
+            const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162*>(t + n * PLANE + r * PITCH + col);
+            x.x += __low2float(h);
+            x.y += __high2float(h);
+        }
+        return x;
+    };
+    float u0 = 0.f, u1 = 0.f, v0 = 0.f, v1 = 0.f;  // this thread's part of U and V of its rows
+#pragma unroll
+    for (int nt = 0; nt < NH; ++nt) {
+        const int col = n0 + nt * 8 + tc;
+        const float2 k0 = k_at(K, r0, col), k1 = k_at(K, r1, col), q0 = k_at(Q, r0, col), q1 = k_at(Q, r1, col);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            dq[nt][i] *= p.scale * (i < 2 ? eG0 : eG1);
+            dkr[nt][i] *= -(i < 2 ? eG0 : eG1);
+            dkc[nt][i] *= i < 2 ? eD0 : eD1;
+        }
+        u0 += q0.x * dq[nt][0] + q0.y * dq[nt][1] + k0.x * dkr[nt][0] + k0.y * dkr[nt][1];
+        u1 += q1.x * dq[nt][2] + q1.y * dq[nt][3] + k1.x * dkr[nt][2] + k1.y * dkr[nt][3];
+        v0 += k0.x * dkc[nt][0] + k0.y * dkc[nt][1];
+        v1 += k1.x * dkc[nt][2] + k1.y * dkc[nt][3];
+    }
+    {
+        const double* G = reinterpret_cast<const double*>(vec + 4 * DL_C);
+        const double g0 = G[r0], g1 = G[r1];
+        const __nv_bfloat16* wP = p.wP + rec * 3 * DL_PLANE;
+        const float* wL = p.wL + rec * DL_PLANE;
+        double hr0 = 0.0, hr1 = 0.0;
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) {
+            const int j = half * 32 + nt * 8 + tc;
+            float ev[4], mv[4];
+            double hc[2] = {0.0, 0.0};
+            if (j <= r1) {
+                float pv[4] = {}, lv[4];
+#pragma unroll
+                for (int n = 2; n >= 0; --n) {
+                    const float2 x = load_pair(wP + n * DL_PLANE + r0 * DL_C + j);
+                    const float2 z = load_pair(wP + n * DL_PLANE + r1 * DL_C + j);
+                    pv[0] += x.x; pv[1] += x.y; pv[2] += z.x; pv[3] += z.y;
+                }
+                const float2 l0 = load_pair(wL + r0 * DL_C + j), l1 = load_pair(wL + r1 * DL_C + j);
+                lv[0] = l0.x; lv[1] = l0.y; lv[2] = l1.x; lv[3] = l1.y;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = i < 2 ? r0 : r1, jj = j + (i & 1);
+                    // a step's own product carries no decay: it is no part of dg
+                    const float h = jj < r ? e[nt][i] * pv[i] - m[nt][i] * lv[i] : 0.f;
+                    (i < 2 ? hr0 : hr1) += (double)h;
+                    hc[i & 1] += (double)h;
+                }
+            }
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+                hc[0] += __shfl_xor_sync(0xffffffffu, hc[0], o);
+                hc[1] += __shfl_xor_sync(0xffffffffu, hc[1], o);
+            }
+            if (gr == 0) {
+                hcol[(warp & 3) * DL_C + j] = hc[0];
+                hcol[(warp & 3) * DL_C + j + 1] = hc[1];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = i < 2 ? r0 : r1, jj = j + (i & 1);
+                const float d = jj <= r ? exp_diff((i < 2 ? g0 : g1) - G[jj]) : 0.f;
+                ev[i] = jj <= r ? p.scale * (d * e[nt][i]) : 0.f;
+                mv[i] = jj < r ? -d * m[nt][i] : 0.f;
+            }
+#pragma unroll
+            for (int n = 0; n < 3; ++n) {
+                __nv_bfloat16 *eo = E + n * DL_C * DL_TPITCH, *mo = M + n * DL_C * DL_TPITCH;
+                *reinterpret_cast<uint32_t*>(eo + r0 * DL_TPITCH + j) = split_bf16(ev[0], ev[1]);
+                *reinterpret_cast<uint32_t*>(eo + r1 * DL_TPITCH + j) = split_bf16(ev[2], ev[3]);
+                *reinterpret_cast<uint32_t*>(mo + r0 * DL_TPITCH + j) = split_bf16(mv[0], mv[1]);
+                *reinterpret_cast<uint32_t*>(mo + r1 * DL_TPITCH + j) = split_bf16(mv[2], mv[3]);
+            }
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            hr0 += __shfl_xor_sync(0xffffffffu, hr0, o);
+            hr1 += __shfl_xor_sync(0xffffffffu, hr1, o);
+            u0 += __shfl_xor_sync(0xffffffffu, u0, o);
+            u1 += __shfl_xor_sync(0xffffffffu, u1, o);
+            v0 += __shfl_xor_sync(0xffffffffu, v0, o);
+            v1 += __shfl_xor_sync(0xffffffffu, v1, o);
+            xw0 += __shfl_xor_sync(0xffffffffu, xw0, o);
+            xw1 += __shfl_xor_sync(0xffffffffu, xw1, o);
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) dots += __shfl_xor_sync(0xffffffffu, dots, o);
+        if ((lane & 3) == 0) {
+            hrow[half * DL_C + r0] = hr0;
+            hrow[half * DL_C + r1] = hr1;
+            rows[half * DL_C + r0] = u0;
+            rows[half * DL_C + r1] = u1;
+            rows[(2 + half) * DL_C + r0] = v0;
+            rows[(2 + half) * DL_C + r1] = v1;
+            if (half == 0) {
+                rows[4 * DL_C + r0] = xw0;
+                rows[4 * DL_C + r1] = xw1;
+            }
+        }
+        if (lane == 0) red[warp] = dots;
+    }
+    __syncthreads();
+    // dq += E K, dkr += M K over the steps up to the row block
+    for (int kt = 0; kt * 16 <= m0; ++kt) {
+        Frag4 ea[3], ma[3];
+#pragma unroll
+        for (int n = 0; n < 3; ++n) {
+            ea[n] = load_a(E + n * DL_C * DL_TPITCH, DL_TPITCH, m0, kt * 16, lane);
+            ma[n] = load_a(M + n * DL_C * DL_TPITCH, DL_TPITCH, m0, kt * 16, lane);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NH; nt += 2) {
+            Frag4 f[NP];
+#pragma unroll
+            for (int n = 0; n < NP; ++n) f[n] = load_b_t(K + n * PLANE, PITCH, n0 + nt * 8, kt * 16, lane);
+            mma_terms<3, NP>(dq[nt], dq[nt + 1], ea, f);
+            mma_terms<3, NP>(dkr[nt], dkr[nt + 1], ma, f);
+        }
+    }
+    // dkc += E^T Q + M^T K over the steps from the row block on
+    for (int kt = m0 / 16; kt < 4; ++kt) {
+        Frag4 ea[3], ma[3];
+#pragma unroll
+        for (int n = 0; n < 3; ++n) {
+            ea[n] = load_a_t(E + n * DL_C * DL_TPITCH, DL_TPITCH, m0, kt * 16, lane);
+            ma[n] = load_a_t(M + n * DL_C * DL_TPITCH, DL_TPITCH, m0, kt * 16, lane);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NH; nt += 2) {
+            Frag4 f[NP];
+#pragma unroll
+            for (int n = 0; n < NP; ++n) f[n] = load_b_t(Q + n * PLANE, PITCH, n0 + nt * 8, kt * 16, lane);
+            mma_terms<3, NP>(dkc[nt], dkc[nt + 1], ea, f);
+#pragma unroll
+            for (int n = 0; n < NP; ++n) f[n] = load_b_t(K + n * PLANE, PITCH, n0 + nt * 8, kt * 16, lane);
+            mma_terms<3, NP>(dkc[nt], dkc[nt + 1], ma, f);
+        }
+    }
+    // rows out
+#pragma unroll
+    for (int nt = 0; nt < NH; ++nt) {
+        const int col = n0 + nt * 8 + tc;
+        if (col < p.dk) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int row = h ? row1 : row0;
+                if (row < 0) continue;
+                const float x0 = dkr[nt][2 * h] + dkc[nt][2 * h], x1 = dkr[nt][2 * h + 1] + dkc[nt][2 * h + 1];
+                const size_t at = (size_t)(img * p.tokens + row);
+                if (p.wdq) {
+                    const size_t o = (at * p.heads_v + head) * p.dk + col;
+                    store_pair(p.wdq + o, dq[nt][2 * h], dq[nt][2 * h + 1]);
+                    store_pair(p.wdk + o, x0, x1);
+                } else {
+                    const size_t o = (at * p.heads_k + hk) * p.dk + col;
+                    if (p.dq) store_pair(reinterpret_cast<T*>(p.dq) + o, dq[nt][2 * h], dq[nt][2 * h + 1]);
+                    if (p.dkey) store_pair(reinterpret_cast<T*>(p.dkey) + o, x0, x1);
+                }
+            }
+        }
+    }
+    if (warp == 0) {  // dg, two steps a lane; then a, b and the sums for A and bias
+        double x[2], v[2], base = 0.0;
+        for (int w = 0; w < 8; ++w) base += (double)red[w];
+        base *= (double)vec[3 * DL_C];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = 2 * lane + i;
+            x[i] = hrow[r] + hrow[DL_C + r] - (hcol[r] + hcol[DL_C + r] + hcol[2 * DL_C + r] + hcol[3 * DL_C + r]) +
+                   (double)rows[r] + (double)rows[DL_C + r];
+            v[i] = (double)rows[2 * DL_C + r] + (double)rows[3 * DL_C + r];
+        }
+        double sum = x[0] + x[1], before = v[0] + v[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double other = __shfl_down_sync(0xffffffffu, sum, o), prior = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane + o < 32) sum += other;
+            if (lane >= o) before += prior;
+        }
+        before -= v[0] + v[1];
+        const double dg[2] = {base + sum + before, base + (sum - x[0]) + (before + v[0])};
+        const float A = p.A[head], bias = p.bias ? p.bias[head] : 0.f;
+        double sA = 0.0, sb = 0.0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = 2 * lane + i;
+            if (t0 + r >= s.len) continue;
+            const int row = delta_row(p, s, t0 + r);
+            const float a = row >= 0 ? to_float(reinterpret_cast<const T*>(p.a)[img * p.a_img + row * p.a_tok + head]) : 0.f;
+            const float da = (float)dg[i] * A * delta_sigmoid(a + bias);
+            sA += dg[i] * (double)delta_softplus(a + bias);
+            sb += (double)da;
+            if (row >= 0) {
+                const size_t o = (size_t)(img * p.tokens + row) * p.heads_v + head;
+                const float bb = to_float(reinterpret_cast<const T*>(p.b)[img * p.b_img + row * p.b_tok + head]);
+                if (p.da) store_elem(reinterpret_cast<T*>(p.da) + o, da);
+                if (p.db) store_elem(reinterpret_cast<T*>(p.db) + o, rows[4 * DL_C + r] * delta_sigmoid(-bb));
+            }
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            sA += __shfl_xor_sync(0xffffffffu, sA, o);
+            sb += __shfl_xor_sync(0xffffffffu, sb, o);
+        }
+        if (lane == 0) {
+            p.wpart[2 * rec] = (float)sA;
+            p.wpart[2 * rec + 1] = (float)sb;
+        }
+    }
+}
+
+// dA and dbias of one head: its chunks' sums added in a fixed order.
+__global__ void __launch_bounds__(256) delta_param_grad_kernel(const DeltaParams p)
+{
+    __shared__ double part[2][8];
+    const int head = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    double sA = 0.0, sb = 0.0;
+    for (long long i = tid; i < p.slots; i += 256) {
+        const float2 x = *reinterpret_cast<const float2*>(p.wpart + 2 * ((size_t)i * p.heads_v + head));
+        sA += x.x;
+        sb += x.y;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        sA += __shfl_down_sync(0xffffffffu, sA, o);
+        sb += __shfl_down_sync(0xffffffffu, sb, o);
+    }
+    if (lane == 0) { part[0][warp] = sA; part[1][warp] = sb; }
+    __syncthreads();
+    if (tid == 0) {
+        sA = sb = 0.0;
+        for (int w = 0; w < 8; ++w) { sA += part[0][w]; sb += part[1][w]; }
+        if (p.dA) p.dA[head] = (float)sA;
+        if (p.dbias) p.dbias[head] = (float)sb;
+    }
+}
+
+// dq and dk of a shared key head: its value heads' parts added in order.
+template <typename T>
+__global__ void __launch_bounds__(256) delta_group_kernel(const DeltaParams p, long long vecs)
+{
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;  // four channels of one row and key head
+    if (i >= vecs) return;
+    const int per = p.dk / 4;
+    const long long rh = i / per;
+    const int c = (int)(i - rh * per) * 4;
+    const float* src = blockIdx.y ? p.wdk : p.wdq;
+    T* dst = reinterpret_cast<T*>(blockIdx.y ? p.dkey : p.dq);
+    if (!dst) return;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int g = 0; g < p.group; ++g) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(src + (rh * p.group + g) * p.dk + c));
+        sum.x += x.x; sum.y += x.y; sum.z += x.z; sum.w += x.w;
+    }
+    store4(dst + rh * p.dk + c, sum);
+}
+
+}  // namespace vscan

@@ -21,7 +21,7 @@ import ctypes
 
 import torch
 
-from ._abi import BF16, F32, ROUTES, VscanDeltaArgs, check, lib
+from ._abi import BF16, F32, ROUTES, VscanDeltaArgs, VscanDeltaGrads, check, lib
 
 _CODES = {torch.float32: F32, torch.bfloat16: BF16}
 
@@ -168,6 +168,45 @@ def delta_forward(q, k, v, a, b, A, bias=None, *, route=None, direction=0, seq_o
     with on_device(q.device):
         check(lib.vscan_delta_forward(handle, ref, stream_handle(stream, q.device, out, final_state, workspace)))
     return out if final_state is None else (out, final_state)
+
+
+GRADIENTS = ("dq", "dk", "dv", "da", "db", "dA", "dbias", "d_initial_state")
+
+
+def delta_backward(q, k, v, a, b, A, bias=None, *, dy, route=None, direction=0, seq_offsets=None, scale=None,
+                   beta_scale=1.0, initial_state=None, d_final_state=None, want=None, workspace=None, stream=None):
+    """Gradients of delta_forward (vscan_delta_backward) in a dict, from its arguments, dy = dL/dy
+    and d_final_state = dL/d(final state).
+
+    Keys: dq, dk, dv, da, db (dense, in the dtype of q), dA, dbias and, with initial_state,
+    d_initial_state (float32). `want` limits the keys computed. Tokens that no step visits get
+    zeros. Equal calls give equal bits.
+    """
+    args = _marshal(q, k, v, a, b, A, bias, dy, route=route, direction=direction, seq_offsets=seq_offsets, scale=scale,
+                    beta_scale=beta_scale, initial_state=initial_state, final_state=None)
+    dev, grads, out = q.device, VscanDeltaGrads(), {}
+    like = {"dq": q, "dk": k, "dv": v, "da": a, "db": b, "dA": A, "dbias": A, "d_initial_state": initial_state}
+    if want is not None and not set(want) <= set(GRADIENTS):
+        raise ValueError(f"want holds unknown gradients {sorted(set(want) - set(GRADIENTS))}")
+    for name in GRADIENTS if want is None else want:
+        t = like[name]
+        if t is not None:
+            out[name] = torch.empty(t.shape, dtype=t.dtype, device=dev)
+            setattr(grads, name, out[name].data_ptr())
+    if d_final_state is not None:
+        check_dense("d_final_state", d_final_state, (_state_rows(q, seq_offsets), *v.shape[2:3], q.shape[3], v.shape[3]),
+                    torch.float32, dev)
+        grads.d_final_state = d_final_state.data_ptr()
+    handle, ref = _route_handle(route), ctypes.byref(args)
+    if workspace is None:
+        need = ctypes.c_uint64()
+        check(lib.vscan_delta_backward_workspace_size(handle, ref, ctypes.byref(need)))
+        workspace = torch.empty(need.value, dtype=torch.uint8, device=dev)
+    grads.workspace, grads.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    with on_device(dev):
+        check(lib.vscan_delta_backward(handle, ref, dy.data_ptr(), ctypes.byref(grads),
+                                       stream_handle(stream, dev, workspace, *out.values())))
+    return out
 
 
 def delta_step(q, k, v, a, b, A, bias=None, *, state, state_out=None, scale=None, beta_scale=1.0, out=None,
