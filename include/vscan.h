@@ -549,6 +549,82 @@ vscan_status vscan_delta_backward(const vscan_route* route, const vscan_delta_ar
  */
 vscan_status vscan_delta_step(const vscan_delta_args* args, void* stream);
 
+/*
+ * ---- Norm of queries and keys with position rotation -------------------------
+ *
+ * For every head of q and k in one pass (an addition of this library; the pages
+ * have no counterpart; the delta rule wants keys of length 1):
+ *
+ *   n = x * w / sqrt(sum x^2 + eps)        (VSCAN_NORM_L2)
+ *   n = x * w / sqrt(sum x^2 / dim + eps)  (VSCAN_NORM_RMS)
+ *   (y_p, y_{p + pairs}) = (n_p cos t - n_{p + pairs} sin t, n_p sin t + n_{p + pairs} cos t),
+ *   t = position * inv_freq[p], p < pairs; channels from 2 * pairs on: y = n
+ *
+ * With axes = 2 the first half of the pairs turns by the position's first entry
+ * (a grid row), the second half by its second (a grid column). Angles are formed in
+ * float64; sums and the norm in float32.
+ */
+typedef enum vscan_norm { VSCAN_NORM_L2 = 0, VSCAN_NORM_RMS = 1 } vscan_norm;
+
+typedef struct vscan_qknorm_args {
+    int32_t batch;       /* images, >= 0                                             */
+    int32_t tokens;      /* tokens per image, >= 0                                   */
+    int32_t heads_q;     /* >= 1                                                     */
+    int32_t heads_k;     /* >= 1                                                     */
+    int32_t dim;         /* head width: <= 256, a multiple of 4 (f32) or 8 (bf16)    */
+    int32_t pairs;       /* rotated pairs, 0 .. dim / 2                              */
+    int32_t axes;        /* 1 or 2 positions per token; divides pairs                */
+    int32_t dtype;       /* vscan_dtype of q, k, yq and yk                           */
+    int32_t norm;        /* vscan_norm                                               */
+    float eps;           /* >= 0                                                     */
+    const void* q;       /* device, [batch][tokens][heads_q][dim], 16-byte aligned   */
+    const void* k;       /* device, [batch][tokens][heads_k][dim], 16-byte aligned   */
+    void* yq;            /* device, like q; may be q itself (same strides)           */
+    void* yk;            /* device, like k; may be k itself (same strides)           */
+    const float* wq;     /* device, [dim], or NULL for ones                          */
+    const float* wk;     /* device, [dim], or NULL for ones                          */
+    const float* inv_freq;      /* device, [pairs]; NULL with pairs = 0              */
+    const int32_t* positions;   /* device, [tokens][axes], or [batch][tokens][axes]
+                            with pos_per_image; NULL with pairs = 0                  */
+    int32_t pos_per_image;      /* 0 or 1                                            */
+    int32_t reserved;    /* must be 0                                                */
+    /* Strides in elements (0 = dense), multiples of 4 (f32) or 8 (bf16); the heads
+     * of one token are contiguous.                                               */
+    int64_t q_tok_stride, q_batch_stride;
+    int64_t k_tok_stride, k_batch_stride;
+    int64_t yq_tok_stride, yq_batch_stride;
+    int64_t yk_tok_stride, yk_batch_stride;
+} vscan_qknorm_args;
+
+/*
+ * Normalise and rotate. One launch, enqueued on stream; no workspace; never
+ * synchronizes. Errors: INVALID_ARGUMENT, SHAPE (pairs or axes that do not fit),
+ * ALIGNMENT, UNSUPPORTED (dim above 256), CUDA.
+ */
+vscan_status vscan_qknorm_forward(const vscan_qknorm_args* args, void* stream);
+
+/* Gradients of vscan_qknorm_forward, written (not accumulated). Any output may be NULL. */
+typedef struct vscan_qknorm_grads {
+    const void* dyq;     /* device, dL/dyq at yq's strides, 16-byte aligned          */
+    const void* dyk;     /* device, dL/dyk at yk's strides, 16-byte aligned          */
+    void* dq;            /* device, dense, in args->dtype, 16-byte aligned           */
+    void* dk;            /* device, dense, in args->dtype, 16-byte aligned           */
+    float* dwq;          /* device, [dim] (also when args->wq is NULL)               */
+    float* dwk;          /* device, [dim] (also when args->wk is NULL)               */
+    void* workspace;     /* device scratch of vscan_qknorm_backward_workspace_size() */
+    uint64_t workspace_bytes;
+} vscan_qknorm_grads;
+
+/* Device scratch bytes vscan_qknorm_backward needs when dwq or dwk is wanted (host only). */
+vscan_status vscan_qknorm_backward_workspace_size(const vscan_qknorm_args* args, uint64_t* bytes);
+
+/*
+ * Backward pass (args->yq and args->yk are not used): one launch, one more for dwq
+ * and dwk. dq may be dyq (dk may be dyk) where that is dense. The sums over tokens
+ * have a fixed order. Errors as vscan_qknorm_forward; WORKSPACE.
+ */
+vscan_status vscan_qknorm_backward(const vscan_qknorm_args* args, const vscan_qknorm_grads* grads, void* stream);
+
 /* Message for the last non-OK status on this thread ("" if none). */
 const char* vscan_last_error(void);
 

@@ -416,5 +416,6 @@ __all__.append("BackwardPlan")
 
 # the matrix-state mixer and the query/key norm that feeds it
 from .delta import delta_backward, delta_forward, delta_step  # noqa: E402
+from .qknorm import qk_norm, qk_norm_backward  # noqa: E402
 
-__all__ += ["delta_forward", "delta_backward", "delta_step"]
+__all__ += ["delta_forward", "delta_backward", "delta_step", "qk_norm", "qk_norm_backward"]

@@ -96,6 +96,26 @@ class VscanDeltaGrads(ctypes.Structure):
         ("workspace_bytes", ctypes.c_uint64)]
 
 
+class VscanQkNormArgs(ctypes.Structure):
+    """Mirror of struct vscan_qknorm_args (include/vscan.h)."""
+
+    _fields_ = (
+        [(name, ctypes.c_int32) for name in
+         ("batch", "tokens", "heads_q", "heads_k", "dim", "pairs", "axes", "dtype", "norm")]
+        + [("eps", ctypes.c_float)]
+        + [(name, ctypes.c_void_p) for name in ("q", "k", "yq", "yk", "wq", "wk", "inv_freq", "positions")]
+        + [("pos_per_image", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+        + [(f"{name}_{axis}_stride", ctypes.c_int64) for name in ("q", "k", "yq", "yk") for axis in ("tok", "batch")]
+    )
+
+
+class VscanQkNormGrads(ctypes.Structure):
+    """Mirror of struct vscan_qknorm_grads (include/vscan.h)."""
+
+    _fields_ = [(name, ctypes.c_void_p) for name in ("dyq", "dyk", "dq", "dk", "dwq", "dwk", "workspace")] + [
+        ("workspace_bytes", ctypes.c_uint64)]
+
+
 class VscanError(RuntimeError):
     def __init__(self, status, message):
         self.status = status
@@ -111,6 +131,7 @@ def _load():
     i32, p, u64 = ctypes.c_int32, ctypes.c_void_p, ctypes.c_uint64
     pa = ctypes.POINTER(VscanArgs)
     pd = ctypes.POINTER(VscanDeltaArgs)
+    pn = ctypes.POINTER(VscanQkNormArgs)
     sigs = {
         "vscan_create_route": ([ctypes.POINTER(p), i32, i32, i32, i32], i32),
         "vscan_destroy": ([p], i32),
@@ -131,6 +152,9 @@ def _load():
         "vscan_delta_backward_workspace_size": ([p, pd, ctypes.POINTER(u64)], i32),
         "vscan_delta_backward": ([p, pd, p, ctypes.POINTER(VscanDeltaGrads), p], i32),
         "vscan_delta_step": ([pd, p], i32),
+        "vscan_qknorm_forward": ([pn, p], i32),
+        "vscan_qknorm_backward_workspace_size": ([pn, ctypes.POINTER(u64)], i32),
+        "vscan_qknorm_backward": ([pn, ctypes.POINTER(VscanQkNormGrads), p], i32),
         "vscan_last_error": ([], ctypes.c_char_p),
         "vscan_status_string": ([i32], ctypes.c_char_p),
         "vscan_status_from_device_word": ([i32], i32),

@@ -8,7 +8,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libvscan.so")
-SOURCES = [os.path.join(CSRC, name) for name in ("vscan_api.cu", "vscan_delta.cu")]
+SOURCES = [os.path.join(CSRC, name) for name in ("vscan_api.cu", "vscan_delta.cu", "vscan_qknorm.cu")]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
