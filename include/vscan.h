@@ -472,6 +472,9 @@ typedef struct vscan_delta_args {
     int64_t y_tok_stride, y_batch_stride;
     void* workspace;     /* device scratch, 16-byte aligned                          */
     uint64_t workspace_bytes;
+    int32_t* status;     /* device int32 or NULL: kernels OR in 2 when an internal
+                            wait gave up (outputs invalid) and never trap; decode
+                            with vscan_status_from_device_word                       */
 } vscan_delta_args;
 
 /*
@@ -521,7 +524,8 @@ typedef struct vscan_delta_grads {
 /*
  * Device scratch bytes vscan_delta_backward needs (host only). Per chunk of 64
  * steps and value head: the forward's scratch, the state entering the chunk and
- * the gradient of the one leaving it ([dim_v][dim_k rounded up to 32] float32 each)
+ * the gradient of the one leaving it ([dim_v][dim_k rounded up to 64 or 128] float32
+ * each)
  * and two [64][dim_v] float32 arrays; with shared key heads also dq and dk per
  * value head in float32.
  */

@@ -84,7 +84,7 @@ class VscanDeltaArgs(ctypes.Structure):
            ("q", "k", "v", "a", "b", "y", "A", "bias", "initial_state", "final_state", "seq_offsets")]
         + [("scale", ctypes.c_float), ("beta_scale", ctypes.c_float)]
         + [(f"{name}_{axis}_stride", ctypes.c_int64) for name in "qkvaby" for axis in ("tok", "batch")]
-        + [("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_uint64)]
+        + [("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_uint64), ("status", ctypes.c_void_p)]
     )
 
 

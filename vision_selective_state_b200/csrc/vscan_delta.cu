@@ -23,7 +23,7 @@ constexpr int kAttrDevices = 64;
 constexpr int kMaxDimK = 128, kMaxDimV = 256, kMaxGrid = 65535;
 
 // Widths the kernels are built for: dim_k is rounded up to one of them.
-int padded_dim_k(int dk) { return (dk + 31) / 32 * 32; }
+int padded_dim_k(int dk) { return dk <= 64 ? 64 : 128; }
 
 struct Stride { int64_t tok, img; };
 
@@ -102,8 +102,8 @@ vscan_status check_pointers(const vscan_delta_args* a, const void* y)
         return fail(VSCAN_ERR_ALIGNMENT, "q, k, v, y (dy) and the states must be 16-byte aligned");
     const uintptr_t el = a->dtype == VSCAN_F32 ? 3 : 1;
     if (((uintptr_t)a->a & el) || ((uintptr_t)a->b & el) || ((uintptr_t)a->A & 3) || ((uintptr_t)a->bias & 3) ||
-        ((uintptr_t)a->seq_offsets & 3))
-        return fail(VSCAN_ERR_ALIGNMENT, "a, b, A, bias or seq_offsets is not aligned to its element");
+        ((uintptr_t)a->seq_offsets & 3) || ((uintptr_t)a->status & 3))
+        return fail(VSCAN_ERR_ALIGNMENT, "a, b, A, bias, seq_offsets or status is not aligned to its element");
     return VSCAN_OK;
 }
 
@@ -180,6 +180,7 @@ DeltaParams make_params(const vscan_route* r, const vscan_delta_args* a)
     p.A = a->A; p.bias = a->bias;
     p.s_in = a->initial_state;
     p.s_out = a->final_state;
+    p.status = a->status;
     p.scale = a->scale;
     p.beta_scale = a->beta_scale;
     const int64_t wk = (int64_t)a->heads_k * a->dim_k, wv = (int64_t)a->heads_v * a->dim_v;
@@ -205,17 +206,17 @@ cudaError_t launch_prep(const DeltaParams& p, cudaStream_t stream)
     return cudaGetLastError();
 }
 
+dim3 walk_grid(const DeltaParams& p) { return dim3((p.dv + 127) / 128, p.heads_v, p.batch); }
+
 template <typename T, int DKP, bool SAVE>
 cudaError_t launch_scan(const DeltaParams& p, cudaStream_t stream)
 {
-    using Sh = vscan::ScanShape<T, DKP>;
+    using Sh = vscan::WalkShape<T, DKP>;
     static int done[kAttrDevices];
-    const int warps = p.dv >= 128 ? 8 : (p.dv + 15) / 16;
-    const size_t smem = Sh::STAGES * Sh::stage_bytes(warps);
-    cudaError_t e = set_smem_once(vscan::delta_scan_kernel<T, DKP, SAVE>, (int)smem, done, kAttrDevices);
+    constexpr size_t smem = Sh::smem(Sh::PP);
+    const cudaError_t e = set_smem_once(vscan::delta_scan_kernel<T, DKP, SAVE>, (int)smem, done, kAttrDevices);
     if (e != cudaSuccess) return e;
-    const dim3 grid((p.dv + 127) / 128, p.heads_v, p.batch);
-    vscan::delta_scan_kernel<T, DKP, SAVE><<<grid, warps * 32, smem, stream>>>(p);
+    vscan::delta_scan_kernel<T, DKP, SAVE><<<walk_grid(p), vscan::DW_THREADS, smem, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -236,14 +237,12 @@ cudaError_t run_backward(const DeltaParams& p, cudaStream_t stream)
         if ((e = launch_prep<T, DKP>(p, stream)) != cudaSuccess) return e;
         if ((e = launch_scan<T, DKP, true>(p, stream)) != cudaSuccess) return e;
     }
-    using Sh = vscan::RscanShape<T, DKP>;
-    const int warps = p.dv >= 128 ? 8 : (p.dv + 15) / 16;
-    size_t smem = Sh::STAGES * Sh::stage_bytes(warps);
-    if ((e = set_smem_once(vscan::delta_rscan_kernel<T, DKP>, (int)smem, done_r, kAttrDevices)) != cudaSuccess) return e;
-    vscan::delta_rscan_kernel<T, DKP><<<dim3((p.dv + 127) / 128, p.heads_v, p.batch), warps * 32, smem, stream>>>(p);
+    constexpr size_t walk = vscan::WalkShape<T, DKP>::smem(3);
+    if ((e = set_smem_once(vscan::delta_rscan_kernel<T, DKP>, (int)walk, done_r, kAttrDevices)) != cudaSuccess) return e;
+    vscan::delta_rscan_kernel<T, DKP><<<walk_grid(p), vscan::DW_THREADS, walk, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (p.tokens > 0 && p.slots > 0) {
-        smem = vscan::GradShape<T, DKP>::smem;
+        constexpr size_t smem = vscan::GradShape<T, DKP>::smem;
         if ((e = set_smem_once(vscan::delta_grad_kernel<T, DKP>, (int)smem, done_g, kAttrDevices)) != cudaSuccess) return e;
         vscan::delta_grad_kernel<T, DKP><<<dim3((unsigned)p.slots, p.heads_v), 256, smem, stream>>>(p);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -258,16 +257,10 @@ cudaError_t run_backward(const DeltaParams& p, cudaStream_t stream)
 }
 
 // f(width) with the I/O type and the padded key width as template arguments.
-#define DELTA_DISPATCH(FN, a, ...)                                                              \
-    (a->dtype == VSCAN_F32                                                                      \
-         ? (padded_dim_k(a->dim_k) == 32   ? FN<float, 32>(__VA_ARGS__)                         \
-            : padded_dim_k(a->dim_k) == 64 ? FN<float, 64>(__VA_ARGS__)                         \
-            : padded_dim_k(a->dim_k) == 96 ? FN<float, 96>(__VA_ARGS__)                         \
-                                           : FN<float, 128>(__VA_ARGS__))                       \
-         : (padded_dim_k(a->dim_k) == 32   ? FN<__nv_bfloat16, 32>(__VA_ARGS__)                 \
-            : padded_dim_k(a->dim_k) == 64 ? FN<__nv_bfloat16, 64>(__VA_ARGS__)                 \
-            : padded_dim_k(a->dim_k) == 96 ? FN<__nv_bfloat16, 96>(__VA_ARGS__)                 \
-                                           : FN<__nv_bfloat16, 128>(__VA_ARGS__)))
+#define DELTA_DISPATCH(FN, a, ...)                                                                             \
+    (a->dtype == VSCAN_F32 ? (padded_dim_k(a->dim_k) == 64 ? FN<float, 64>(__VA_ARGS__) : FN<float, 128>(__VA_ARGS__)) \
+                           : (padded_dim_k(a->dim_k) == 64 ? FN<__nv_bfloat16, 64>(__VA_ARGS__)                 \
+                                                           : FN<__nv_bfloat16, 128>(__VA_ARGS__)))
 
 }  // namespace
 

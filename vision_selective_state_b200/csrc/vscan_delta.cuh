@@ -34,6 +34,7 @@
 #include "vscan_common.cuh"
 #include "vscan_params.cuh"
 #include "vscan_route.cuh"
+#include "vscan_tc.cuh"
 
 namespace vscan {
 
@@ -68,18 +69,19 @@ struct DeltaParams {
     __nv_bfloat16* wP;   // [..][tplanes][64][64]
     float* wvec;         // [..][DL_VECS]
     float* wL;           // [..][64][64]: e^{G_i - G_j} k_i.k_j below the diagonal (backward, else null)
-    float* wS;           // [..][dv][DKP]: state entering the chunk (backward)
+    float* wS;           // [..][DKP][dv]: state entering the chunk (backward)
     float* wW;           // [..][64][dv]: W of the chunk (backward)
     // backward
     const void* dy;      // like y
     const float* ds_in;  // gradient of the final state or null
     float* ds_out;       // gradient of the initial state or null
-    float* wdS;          // [..][dv][DKP]: gradient of the state leaving the chunk
+    float* wdS;          // [..][DKP][dv]: gradient of the state leaving the chunk
     float* wdX;          // [..][64][dv]: gradient of X
     float* wpart;        // [..][2]: per-chunk sums for dA and dbias
     float *wdq, *wdk;    // [images][tokens][heads_v][dk]: per value head where key heads are shared, else null
     void *dq, *dkey, *dvalue, *da, *db;  // dense, in the I/O type
     float *dA, *dbias;
+    int* status;  // device word or null
 };
 
 // The steps of one image or packed sequence: its length, its first workspace
@@ -499,229 +501,380 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaParams p)
 }
 
 // ---- the walk over the chunks -----------------------------------------------------
-// One CTA per image (sequence), value head and slice of up to 128 value
-// channels; each warp owns 16 value channels and holds S^T[16][DKP] of them in
-// registers, so the walk needs no exchange between warps: S^T K^T, X^T, W^T and
-// y^T come out of one product in exactly the layout that the next one takes.
-// The next chunk's tiles are copied while this one computes (STAGES = 2).
+// One CTA of 256 threads per image (sequence), value head and slice of 128 value
+// channels. The products are formed transposed, with the value channel as the row of
+// the 128-row tensor-core tile, so that a thread holds half a row of everything in
+// registers: of S^T[128][DKP] (float32, for the whole walk), and in turn of
+// (K S)^T, X^T, W^T and y^T[128][64]. Between two products it rescales its values,
+// splits them into bf16 terms and stores them to tensor memory as the next left
+// operand; no value crosses threads. Per chunk:
+//
+//   1. KS = S K^T, QS = S Q^T                 B = K, Q    (K-major)
+//   2. X = beta (V - e^G KS);  W = X T^T      B = T       (K-major)
+//   3. O = W P^T, dS = (e^{G_C - G} W) K      B = P (K-major), K (MN-major: the same tile)
+//   4. y = scale e^G QS + O;  S = e^{G_C} S + dS   (float32, in registers)
+//
+// The chain of dependent products bounds the walk: the chunk's tiles are copied one
+// chunk ahead, and y leaves while the next chunk's first product runs.
+// Tensor-memory columns: S terms (over them dS, once step 1 is done), KS (W, then W's
+// terms for O), QS, X's terms (then those of e^{G_C - G} W), O.
+constexpr int DW_THREADS = 256;
+
 template <typename T, int DKP>
-struct ScanShape {
+struct WalkShape {
     static constexpr int NP = DeltaIo<T>::planes;
-    static constexpr int PP = NP == 1 ? 2 : 3;   // planes of P: y in bf16 needs two
+    static constexpr int PP = NP == 1 ? 2 : 3;   // terms of P and W in O: a bf16 y needs two
     static constexpr int STAGES = NP == 1 ? 2 : 1;
-    static constexpr int pitch = DKP + 8;
-    static constexpr int plane = DL_C * pitch;
-    static __host__ __device__ constexpr int vpitch(int warps) { return warps * 16 + 16 / (int)sizeof(T); }
-    static __host__ __device__ constexpr size_t stage_bytes(int warps)
+    static constexpr int KB = DKP / 64;          // 64-wide tiles of K
+    static constexpr int plane = KB * TC_TILE;   // bytes
+    static constexpr int vpitch = 128 + 16 / (int)sizeof(T);
+    static constexpr int oQ = NP * plane, oT = 2 * NP * plane, oP = oT + 3 * TC_TILE;
+    static __host__ __device__ constexpr int oV(int pplanes) { return oP + pplanes * TC_TILE; }
+    static __host__ __device__ constexpr int oVec(int pplanes) { return oV(pplanes) + DL_C * vpitch * (int)sizeof(T); }
+    static __host__ __device__ constexpr int stage(int pplanes) { return (oVec(pplanes) + DL_SCANVECS * 4 + 1023) / 1024 * 1024; }
+    // at least half of the SM's shared memory: one CTA an SM, which owns all tensor memory
+    static __host__ __device__ constexpr size_t smem(int pplanes)
     {
-        return (size_t)2 * NP * plane * 2 + (size_t)DL_C * vpitch(warps) * sizeof(T) +
-               (size_t)(3 + PP) * DL_C * DL_TPITCH * 2 + DL_SCANVECS * 4;
+        const size_t n = 1024 + 1024 + (size_t)STAGES * stage(pplanes);
+        return n < 120 * 1024 ? 120 * 1024 : n;
     }
+    // tensor-memory columns of half a row's terms: of S (DKP / 2 values), of a 64-wide operand (32)
+    static constexpr int SC = DKP / 4, XC = 16;
+};
+
+// Tile rows of a token array into swizzled shared memory, as load_tile.
+template <int NP>
+__device__ __forceinline__ void walk_load(unsigned char* dst, int plane, const __nv_bfloat16* src, long long tok, const int* rows,
+                                          int cols, int have, int tid)
+{
+    const int vecs = cols / 8;
+    for (int i = tid; i < DL_C * vecs; i += DW_THREADS) {
+        const int r = i / vecs, c = i - r * vecs;
+        const int row = rows[r];
+        const bool ok = row >= 0 && c * 8 < have;
+        cp_async16(dst + tc_swizzle(r, c), ok ? src + row * tok + c * 8 : src, ok);
+    }
+}
+template <int NP>
+__device__ __forceinline__ void walk_load(unsigned char* dst, int plane, const float* src, long long tok, const int* rows, int cols,
+                                          int have, int tid)
+{
+    const int vecs = cols / 8;
+    for (int i = tid; i < DL_C * vecs; i += DW_THREADS) {
+        const int r = i / vecs, c = i - r * vecs;
+        const int row = rows[r];
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), z = x;
+        if (row >= 0 && c * 8 < have) x = __ldg(reinterpret_cast<const float4*>(src + row * tok + c * 8));
+        if (row >= 0 && c * 8 + 4 < have) z = __ldg(reinterpret_cast<const float4*>(src + row * tok + c * 8 + 4));
+#pragma unroll
+        for (int n = 0; n < 3; ++n) {
+            uint4 u;
+            u.x = split_bf16(x.x, x.y);
+            u.y = split_bf16(x.z, x.w);
+            u.z = split_bf16(z.x, z.y);
+            u.w = split_bf16(z.z, z.w);
+            *reinterpret_cast<uint4*>(dst + n * plane + tc_swizzle(r, c)) = u;
+        }
+    }
+}
+
+// 64 x 64 planes of the workspace into swizzled shared memory.
+__device__ __forceinline__ void walk_load_planes(unsigned char* dst, const __nv_bfloat16* src, int planes, int tid)
+{
+    for (int i = tid; i < planes * (DL_C * 8); i += DW_THREADS) {
+        const int r = (i >> 3) & 63, c = i & 7, n = i >> 9;
+        cp_async16(dst + n * TC_TILE + tc_swizzle(r, c), src + (size_t)i * 8, true);
+    }
+}
+
+// NT bf16 terms of 32 values of a row, stored NT * 16 columns from `addr` on.
+template <int NT>
+__device__ __forceinline__ void put_terms(uint32_t addr, float (&v)[32])
+{
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        uint32_t u[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) u[i] = split_bf16(v[2 * i], v[2 * i + 1]);
+        tc_st16(addr + n * 16, u);
+    }
+}
+
+// All products of order up to ORD of an operand of NA terms in tensor memory with NB
+// planes in shared memory, small ones first: they add up before the large ones
+// truncate the accumulator at their own size. `a(x, k)` is the address of term x of
+// summed slice k, `b(y, k)` the descriptor of plane y's.
+template <int NA, int NB, int ORD, int KS, typename FA, typename FB>
+__device__ __forceinline__ void tc_product(uint32_t d, uint32_t idesc, bool add, FA a, FB b)
+{
+#pragma unroll
+    for (int o = ORD; o >= 0; --o)
+#pragma unroll
+        for (int y = 0; y < NB; ++y) {
+            const int x = o - y;
+            if (x >= 0 && x < NA) {
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    tc_mma(d, a(x, k), b(y, k), idesc, add);
+                    add = true;
+                }
+            }
+        }
+}
+
+// What a walk's CTA keeps in shared memory besides the stages.
+struct WalkShared {
+    unsigned long long mbar[4];
+    uint32_t tmem;
+    int dead;
+    int rows[3][DL_C];  // token rows of chunk c in slot c mod 3: the chunk that leaves, the present one, the next
 };
 
 template <typename T, int DKP, bool SAVE>
-__global__ void __launch_bounds__(256) delta_scan_kernel(const DeltaParams p)
+__global__ void __launch_bounds__(DW_THREADS, 1) delta_scan_kernel(const DeltaParams p)
 {
-    using Sh = ScanShape<T, DKP>;
-    constexpr int NP = Sh::NP, PP = Sh::PP, PITCH = Sh::pitch, PLANE = Sh::plane, NT = DKP / 8;
-    extern __shared__ __align__(16) unsigned char smem[];
-    const int tid = threadIdx.x, nthreads = blockDim.x, warps = nthreads >> 5, warp = tid >> 5, lane = tid & 31;
-    const int gr = lane >> 2, tc = (lane & 3) * 2;
+    using Sh = WalkShape<T, DKP>;
+    constexpr int NP = Sh::NP, PP = Sh::PP, HS = DKP / 2, KT = DKP / 16;
+    // tensor-memory columns
+    constexpr int cS = 0, cKS = cS + 6 * Sh::SC, cQS = cKS + 64, cX = cQS + 64, cO = cX + 96;
+    constexpr int cDS = DKP == 128 ? cS : cO + 64;
+    static_assert(cO + (DKP == 128 ? 64 : 128) <= 512, "tensor memory");
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = smem_raw + (1024 - (__cvta_generic_to_shared(smem_raw) & 1023)) % 1024;
+    WalkShared* ws = reinterpret_cast<WalkShared*>(smem);
+    unsigned char* stages = smem + 1024;
+    constexpr int STAGE = Sh::stage(PP);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = warp >> 2;
     const int head = blockIdx.y, b = blockIdx.z, hk = head / p.group;
-    const int slice = blockIdx.x * 128;            // first value channel of the CTA
-    const int v0 = slice + warp * 16;              // and of this warp
-    const int VP = Sh::vpitch(warps);
-    const size_t stage_bytes = Sh::stage_bytes(warps);
+    const int slice = blockIdx.x * 128, row = (warp & 3) * 32 + lane, vc = slice + row;  // this thread's value channel
+    const bool live = vc < p.dv;
     const DeltaSeq s = delta_seq(p, b);
     const int chunks = (s.len + DL_C - 1) / DL_C;
     const long long img = delta_img(p, b);
     const T* q = reinterpret_cast<const T*>(p.q) + img * p.q_img + (long long)hk * p.dk;
     const T* k = reinterpret_cast<const T*>(p.k) + img * p.k_img + (long long)hk * p.dk;
     const T* v = reinterpret_cast<const T*>(p.v) + img * p.v_img + (long long)head * p.dv + slice;
-    T* y = reinterpret_cast<T*>(p.y) + img * p.y_img + (long long)head * p.dv;
+    T* y = reinterpret_cast<T*>(p.y) + img * p.y_img + (long long)head * p.dv + slice;
+    const int dvs = min(128, p.dv - slice);
+    const size_t sbase = ((size_t)b * p.heads_v + head) * p.dk * p.dv;
 
-    auto stage_k = [&](int st) { return reinterpret_cast<__nv_bfloat16*>(smem + st * stage_bytes); };
+    float S[HS];  // S^T[row][half * HS + i]
+#pragma unroll
+    for (int i = 0; i < HS; ++i) {
+        const int kc = half * HS + i;
+        S[i] = p.s_in && live && kc < p.dk ? p.s_in[sbase + (size_t)kc * p.dv + vc] : 0.f;
+    }
+    if (chunks == 0) {
+        if (p.s_out && live)
+#pragma unroll
+            for (int i = 0; i < HS; ++i)
+                if (half * HS + i < p.dk) p.s_out[sbase + (size_t)(half * HS + i) * p.dv + vc] = S[i];
+        return;
+    }
+
+    uint32_t mbar[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) mbar[i] = static_cast<uint32_t>(__cvta_generic_to_shared(&ws->mbar[i]));
+    if (warp == 0) tc_alloc(static_cast<uint32_t>(__cvta_generic_to_shared(&ws->tmem)));
+    if (tid == 0) {
+        for (int i = 0; i < 3; ++i) mbar_init(mbar[i], 1);
+        ws->dead = 0;
+    }
+    auto rows_of = [&](int c) {
+        if (tid < DL_C) ws->rows[c % 3][tid] = delta_row(p, s, c * DL_C + tid);
+    };
     auto issue = [&](int c, int st) {
-        __nv_bfloat16* K = stage_k(st);
-        __nv_bfloat16* Q = K + NP * PLANE;
-        __nv_bfloat16* Tt = Q + NP * PLANE;
-        __nv_bfloat16* P = Tt + 3 * DL_C * DL_TPITCH;
-        T* V = reinterpret_cast<T*>(P + PP * DL_C * DL_TPITCH);
-        float* vec = reinterpret_cast<float*>(V + DL_C * VP);
+        unsigned char* base = stages + st * STAGE;
         const size_t rec = (size_t)(s.slot + c) * p.heads_v + head;
-        load_tile(K, PITCH, PLANE, k, p.k_tok, p, s, c * DL_C, DKP, p.dk, tid, nthreads);
-        if (!SAVE) load_tile(Q, PITCH, PLANE, q, p.q_tok, p, s, c * DL_C, DKP, p.dk, tid, nthreads);
-        load_planes(Tt, p.wT + rec * 3 * DL_PLANE, 3, tid, nthreads);
-        if (!SAVE) load_planes(P, p.wP + rec * p.tplanes * DL_PLANE, PP, tid, nthreads);
-        load_raw(V, VP, v, p.v_tok, p, s, c * DL_C, warps * 16, p.dv - slice, tid, nthreads);
-        for (int i = tid; i < DL_SCANVECS / 4; i += nthreads)
-            cp_async16(vec + 4 * i, p.wvec + rec * DL_VECS + 4 * i, true);
+        const int* rows = ws->rows[c % 3];
+        walk_load<NP>(base, Sh::plane, k, p.k_tok, rows, DKP, p.dk, tid);
+        if (!SAVE) walk_load<NP>(base + Sh::oQ, Sh::plane, q, p.q_tok, rows, DKP, p.dk, tid);
+        walk_load_planes(base + Sh::oT, p.wT + rec * 3 * DL_PLANE, 3, tid);
+        if (!SAVE) walk_load_planes(base + Sh::oP, p.wP + rec * p.tplanes * DL_PLANE, PP, tid);
+        constexpr int V = 16 / sizeof(T), vecs = 128 / V;
+        T* vd = reinterpret_cast<T*>(base + Sh::oV(PP));
+        for (int i = tid; i < DL_C * vecs; i += DW_THREADS) {
+            const int r = i / vecs, cc = (i - r * vecs) * V;
+            const bool ok = rows[r] >= 0 && cc < dvs;
+            cp_async16(vd + r * Sh::vpitch + cc, ok ? v + rows[r] * p.v_tok + cc : v, ok);
+        }
+        if (tid < DL_SCANVECS / 4)
+            cp_async16(base + Sh::oVec(PP) + 16 * tid, p.wvec + rec * DL_VECS + 4 * tid, true);
+    };
+    rows_of(0);
+    mbar_fence_init();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = ws->tmem, tl = tm + ((uint32_t)(warp & 3) << 21);  // this warp's 32 rows
+    issue(0, 0);
+    cp_async_commit();
+
+    auto put_state = [&]() {  // S's terms as the left operand of the next chunk
+#pragma unroll
+        for (int i = 0; i < HS; i += 32) {
+            float x[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = S[i + e];
+#pragma unroll
+            for (int n = 0; n < 3; ++n) {
+                uint32_t u[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) u[e] = split_bf16(x[2 * e], x[2 * e + 1]);
+                tc_st16(tl + cS + half * 3 * Sh::SC + n * Sh::SC + i / 2, u);
+            }
+        }
+    };
+    auto aS = [&](int x, int ks) { return tm + cS + (ks / (KT / 2)) * 3 * Sh::SC + x * Sh::SC + (ks % (KT / 2)) * 8; };
+    auto aX = [&](int x, int ks) { return tm + cX + (ks >> 1) * 48 + x * 16 + (ks & 1) * 8; };
+    // W's terms for O lie over W itself and QS, each half of a row over the columns that its own thread has read
+    auto aWO = [&](int x, int ks) { return tm + (x < 2 ? cKS + x * 16 : cQS) + (ks >> 1) * 32 + (ks & 1) * 8; };
+    auto put_out = [&](int c, int st) {  // y of chunk c, staged in V's place, to whole rows
+        constexpr int V = 16 / sizeof(T), vecs = 128 / V;
+        const T* vd = reinterpret_cast<const T*>(stages + st * STAGE + Sh::oV(PP));
+        for (int i = tid; i < DL_C * vecs; i += DW_THREADS) {
+            const int r = i / vecs, cc = (i - r * vecs) * V;
+            const int at = ws->rows[c % 3][r];
+            if (at >= 0 && cc < dvs)
+                *reinterpret_cast<uint4*>(y + at * p.y_tok + cc) = *reinterpret_cast<const uint4*>(vd + r * Sh::vpitch + cc);
+        }
     };
 
-    // S^T: rows are value channels, columns key channels
-    float S[NT][4];
-    const size_t sbase = ((size_t)b * p.heads_v + head) * p.dk * p.dv;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int vc = v0 + gr + (e >> 1) * 8, kc = nt * 8 + tc + (e & 1);
-            S[nt][e] = p.s_in && vc < p.dv && kc < p.dk ? p.s_in[sbase + (size_t)kc * p.dv + vc] : 0.f;
-        }
-
-    if (Sh::STAGES == 2 && chunks > 0) {
-        issue(0, 0);
-        cp_async_commit();
-    }
+    put_state();
     for (int c = 0; c < chunks; ++c) {
         const int st = Sh::STAGES == 2 ? c & 1 : 0;
+        const uint32_t par = c & 1;
+        unsigned char* base = stages + st * STAGE;
+        const uint32_t bK = static_cast<uint32_t>(__cvta_generic_to_shared(base)), bQ = bK + Sh::oQ, bT = bK + Sh::oT, bP = bK + Sh::oP;
+        T* vd = reinterpret_cast<T*>(base + Sh::oV(PP));
+        const float* vec = reinterpret_cast<const float*>(base + Sh::oVec(PP));
+        const size_t rec = (size_t)(s.slot + c) * p.heads_v + head;
+        if (Sh::STAGES == 1 && c > 0) {
+            // one stage: y leaves it, then it is filled again
+            __syncthreads();
+            if (!SAVE) put_out(c - 1, 0);
+            __syncthreads();
+            issue(c, 0);
+            cp_async_commit();
+        }
+        cp_async_wait<0>();
+        tc_fence_smem();
+        tc_wait_st();
+        tc_fence_before();
+        __syncthreads();
+        if (tid == 0) {  // 1: K S and Q S
+            tc_fence_after();
+            auto k_major = [&](uint32_t t) {
+                return [t](int n, int ks) { return tc_desc(t + n * Sh::plane + (ks >> 2) * TC_TILE + (ks & 3) * 32); };
+            };
+            tc_product<3, NP, 2, KT>(tm + cKS, tc_idesc(64, false), false, aS, k_major(bK));
+            // a bf16 y: two terms of the state (2^-17) are far below its rounding
+            if (!SAVE) tc_product<3, NP, NP == 1 ? 1 : 2, KT>(tm + cQS, tc_idesc(64, false), false, aS, k_major(bQ));
+            tc_commit(mbar[0]);
+        }
+        if (!SAVE && Sh::STAGES == 2 && c > 0) put_out(c - 1, st ^ 1);
+        if (c + 1 < chunks) rows_of(c + 1);
+        if (SAVE && live) {  // the state entering the chunk, for the gradients
+            float* o = p.wS + rec * p.dv * DKP + vc;
+#pragma unroll
+            for (int i = 0; i < HS; ++i) o[(size_t)(half * HS + i) * p.dv] = S[i];
+        }
+        float x[32];
+        mbar_wait(mbar[0], par, &ws->dead);
+        tc_fence_after();
+        tc_ld32(tl + cKS + half * 32, x);
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {  // X^T = beta (V - e^G K S)^T
+            const int r = half * 32 + i;
+            x[i] = vec[2 * DL_C + r] * (to_float(vd[r * Sh::vpitch + row]) - vec[r] * x[i]);
+        }
+        put_terms<3>(tl + cX + half * 48, x);
+        tc_wait_st();
+        tc_fence_before();
+        __syncthreads();
+        if (tid == 0) {  // 2: W
+            tc_fence_after();
+            tc_product<3, 3, 2, 4>(tm + cKS, tc_idesc(64, false), false, aX,
+                                   [bT](int n, int ks) { return tc_desc(bT + n * TC_TILE + ks * 32); });
+            tc_commit(mbar[1]);
+        }
+        // the next chunk's copies go where the last one was: its y has left before the barrier
         if (Sh::STAGES == 2) {
             if (c + 1 < chunks) issue(c + 1, st ^ 1);
             cp_async_commit();
-            cp_async_wait<1>();
-        } else {
-            issue(c, 0);
-            cp_async_commit();
-            cp_async_wait<0>();
         }
-        __syncthreads();
-        __nv_bfloat16* K = stage_k(st);
-        __nv_bfloat16* Q = K + NP * PLANE;
-        __nv_bfloat16* Tt = Q + NP * PLANE;
-        __nv_bfloat16* P = Tt + 3 * DL_C * DL_TPITCH;
-        T* V = reinterpret_cast<T*>(P + PP * DL_C * DL_TPITCH);
-        const float* vec = reinterpret_cast<const float*>(V + DL_C * VP);
-        const size_t rec = (size_t)(s.slot + c) * p.heads_v + head;
-
-        if (SAVE) {  // the state entering the chunk, for the gradients
-            float* o = p.wS + rec * p.dv * DKP;
+        float o[32];
+        if (!SAVE) {
+            tc_ld32(tl + cQS + half * 32, o);
+            tc_wait_ld();
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (v0 + gr + h * 8 < p.dv)
-                        *reinterpret_cast<float2*>(o + (size_t)(v0 + gr + h * 8) * DKP + nt * 8 + tc) =
-                            make_float2(S[nt][2 * h], S[nt][2 * h + 1]);
+            for (int i = 0; i < 32; ++i) o[i] *= p.scale * vec[half * 32 + i];
         }
-
-        // (K S)^T and (Q S)^T
-        float ks[8][4] = {}, o[8][4] = {};
-#pragma unroll
-        for (int kt = 0; kt < DKP / 16; ++kt) {
-            Frag4 sa[3];
-            split_tiles<3>(S[2 * kt], S[2 * kt + 1], sa);
-#pragma unroll
-            for (int nt = 0; nt < 8; nt += 2) {
-                Frag4 f[NP];
-#pragma unroll
-                for (int n = 0; n < NP; ++n) f[n] = load_b(K + n * PLANE, PITCH, nt * 8, kt * 16, lane);
-                mma_terms<3, NP>(ks[nt], ks[nt + 1], sa, f);
-                if (!SAVE) {
-#pragma unroll
-                    for (int n = 0; n < NP; ++n) f[n] = load_b(Q + n * PLANE, PITCH, nt * 8, kt * 16, lane);
-                    // y leaves in bf16: two terms of the state (2^-17) are far below its rounding
-                    mma_terms<3, NP, NP == 1 ? 1 : 2>(o[nt], o[nt + 1], sa, f);
-                }
-            }
-        }
-        // X^T = beta (V - e^G K S)^T
-#pragma unroll
-        for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int r = nt * 8 + tc + (e & 1);
-                const float x = to_float(V[r * VP + warp * 16 + gr + (e >> 1) * 8]);
-                ks[nt][e] = vec[2 * DL_C + r] * (x - vec[r] * ks[nt][e]);
-                if (!SAVE) o[nt][e] *= p.scale * vec[r];
-            }
-        // W^T = X^T T^T; T has nothing above the diagonal
-        float w[8][4] = {};
-#pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
-            Frag4 xa[3];
-            split_tiles<3>(ks[2 * kt], ks[2 * kt + 1], xa);
-#pragma unroll
-            for (int nt = 2 * kt; nt < 8; nt += 2) {
-                Frag4 f[3];
-#pragma unroll
-                for (int n = 0; n < 3; ++n) f[n] = load_b(Tt + n * DL_C * DL_TPITCH, DL_TPITCH, nt * 8, kt * 16, lane);
-                mma_terms<3, 3>(w[nt], w[nt + 1], xa, f);
-            }
-        }
+        mbar_wait(mbar[1], par, &ws->dead);
+        tc_fence_after();
+        tc_ld32(tl + cKS + half * 32, x);
+        tc_wait_ld();
         if (SAVE) {
-            float* ow = p.wW + rec * DL_C * p.dv;
+            if (live) {
+                float* ow = p.wW + rec * DL_C * p.dv + vc;
 #pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int vc = v0 + gr + (e >> 1) * 8;
-                    if (vc < p.dv) ow[(size_t)(nt * 8 + tc + (e & 1)) * p.dv + vc] = w[nt][e];
-                }
+                for (int i = 0; i < 32; ++i) ow[(size_t)(half * 32 + i) * p.dv] = x[i];
+            }
         } else {
-            // y^T = scale e^G (Q S)^T + W^T P^T
+            float w[32];
 #pragma unroll
-            for (int kt = 0; kt < 4; ++kt) {
-                Frag4 wa[PP];
-                split_tiles<PP>(w[2 * kt], w[2 * kt + 1], wa);
-#pragma unroll
-                for (int nt = 2 * kt; nt < 8; nt += 2) {
-                    Frag4 f[PP];
-#pragma unroll
-                    for (int n = 0; n < PP; ++n) f[n] = load_b(P + n * DL_C * DL_TPITCH, DL_TPITCH, nt * 8, kt * 16, lane);
-                    mma_terms<PP, PP, PP - 1>(o[nt], o[nt + 1], wa, f);
-                }
-            }
-            // through this warp's own columns of V, now read, to whole rows
-            __syncwarp();
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    store_elem(V + (nt * 8 + tc + (e & 1)) * VP + warp * 16 + gr + (e >> 1) * 8, o[nt][e]);
-            __syncwarp();
-            constexpr int VE = 16 / sizeof(T), VR = 16 / VE;
-#pragma unroll
-            for (int i = 0; i < DL_C * VR / 32; ++i) {
-                const int r = (i * 32 + lane) / VR, cc = ((i * 32 + lane) % VR) * VE;
-                const int row = delta_row(p, s, c * DL_C + r);
-                if (row >= 0 && v0 + cc < p.dv)
-                    *reinterpret_cast<uint4*>(y + row * p.y_tok + v0 + cc) =
-                        *reinterpret_cast<const uint4*>(V + r * VP + warp * 16 + cc);
-            }
+            for (int i = 0; i < 32; ++i) w[i] = x[i];
+            put_terms<2>(tl + cKS + half * 32, w);
+            if (PP == 3) put_terms<1>(tl + cQS + half * 32, w);
         }
-        // S^T = e^{G_C} S^T + (e^{G_C - G} W)^T K
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] *= vec[DL_C + half * 32 + i];
+        put_terms<3>(tl + cX + half * 48, x);
+        tc_wait_st();
+        tc_fence_before();
+        __syncthreads();
+        if (tid == 0) {  // 3: the change of the state, and O
+            tc_fence_after();
+#pragma unroll
+            for (int nb = 0; nb < Sh::KB; ++nb)
+                tc_product<3, NP, 2, 4>(tm + cDS + nb * (3 * Sh::SC), tc_idesc(64, true), false, aX, [bK, nb](int n, int ks) {
+                    return tc_desc(bK + n * Sh::plane + nb * TC_TILE + ks * 2048);
+                });
+            if (!SAVE)
+                tc_product<PP, PP, PP - 1, 4>(tm + cO, tc_idesc(64, false), false, aWO,
+                                              [bP](int n, int ks) { return tc_desc(bP + n * TC_TILE + ks * 32); });
+            tc_commit(mbar[2]);
+        }
         const float eC = vec[3 * DL_C];
+        mbar_wait(mbar[2], par, &ws->dead);
+        tc_fence_after();
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int i = 0; i < HS; i += 32) {
+            tc_ld32(tl + cDS + (DKP == 128 ? half * 3 * Sh::SC : half * 32) + i, x);
+            tc_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 4; ++e) S[nt][e] *= eC;
-#pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w[2 * kt + h][e] *= vec[DL_C + (2 * kt + h) * 8 + tc + (e & 1)];
-            Frag4 wa[3];
-            split_tiles<3>(w[2 * kt], w[2 * kt + 1], wa);
-#pragma unroll
-            for (int nt = 0; nt < NT; nt += 2) {
-                Frag4 f[NP];
-#pragma unroll
-                for (int n = 0; n < NP; ++n) f[n] = load_b_t(K + n * PLANE, PITCH, nt * 8, kt * 16, lane);
-                mma_terms<3, NP>(S[nt], S[nt + 1], wa, f);
-            }
+            for (int e = 0; e < 32; ++e) S[i + e] = eC * S[i + e] + x[e];
         }
-        __syncthreads();  // the stage is free for the copies of chunk c + 2
-    }
-    if (p.s_out) {
+        put_state();
+        if (!SAVE) {
+            tc_ld32(tl + cO + half * 32, x);
+            tc_wait_ld();
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int vc = v0 + gr + (e >> 1) * 8, kc = nt * 8 + tc + (e & 1);
-                if (vc < p.dv && kc < p.dk) p.s_out[sbase + (size_t)kc * p.dv + vc] = S[nt][e];
-            }
+            for (int i = 0; i < 32; ++i) store_elem(vd + (half * 32 + i) * Sh::vpitch + row, o[i] + x[i]);
+        }
     }
+    tc_wait_st();
+    cp_async_wait<0>();
+    tc_fence_before();
+    __syncthreads();
+    if (!SAVE) put_out(chunks - 1, Sh::STAGES == 2 ? (chunks - 1) & 1 : 0);
+    if (p.s_out && live)
+#pragma unroll
+        for (int i = 0; i < HS; ++i)
+            if (half * HS + i < p.dk) p.s_out[sbase + (size_t)(half * HS + i) * p.dv + vc] = S[i];
+    if (p.status && tid == 0 && ws->dead) atomicOr(p.status, DEV_STATUS_TIMEOUT);
+    if (warp == 0) tc_free(tm);
 }
 
 // ---- one token ----------------------------------------------------------------------

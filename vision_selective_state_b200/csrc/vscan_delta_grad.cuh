@@ -29,225 +29,252 @@
 namespace vscan {
 
 // ---- the walk backwards ---------------------------------------------------------------
+// As the walk forwards, with dS^T[128][DKP] in registers:
+//
+//   1. D1 = dS K^T, D2 = dO P                        B = K (K-major), P (MN-major)
+//   2. dW = e^{G_C - G} D1 + D2;  dX = dW T          B = T (MN-major)
+//   3. ddS = (scale e^G dO) Q - (e^G beta dX) K      B = Q, K (MN-major)
+//   4. dS = e^{G_C} dS + ddS
+//
+// Tensor-memory columns: dS's terms (over them ddS), D1 (then dX), D2 and dO's terms
+// (then those of scale e^G dO), dW's terms (then those of e^G dV).
 template <typename T, int DKP>
-struct RscanShape {
-    static constexpr int NP = DeltaIo<T>::planes;
-    static constexpr int STAGES = NP == 1 ? 2 : 1;
-    static constexpr int pitch = DKP + 8;
-    static constexpr int plane = DL_C * pitch;
-    static __host__ __device__ constexpr int vpitch(int warps) { return warps * 16 + 16 / (int)sizeof(T); }
-    static __host__ __device__ constexpr size_t stage_bytes(int warps)
-    {
-        return (size_t)2 * NP * plane * 2 + (size_t)DL_C * vpitch(warps) * sizeof(T) + (size_t)6 * DL_C * DL_TPITCH * 2 +
-               DL_SCANVECS * 4;
-    }
-};
-
-template <typename T, int DKP>
-__global__ void __launch_bounds__(256) delta_rscan_kernel(const DeltaParams p)
+__global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaParams p)
 {
-    using Sh = RscanShape<T, DKP>;
-    constexpr int NP = Sh::NP, PITCH = Sh::pitch, PLANE = Sh::plane, NT = DKP / 8;
-    extern __shared__ __align__(16) unsigned char smem[];
-    const int tid = threadIdx.x, nthreads = blockDim.x, warps = nthreads >> 5, warp = tid >> 5, lane = tid & 31;
-    const int gr = lane >> 2, tc = (lane & 3) * 2;
+    using Sh = WalkShape<T, DKP>;
+    constexpr int NP = Sh::NP, HS = DKP / 2, KT = DKP / 16, STAGE = Sh::stage(3);
+    constexpr int cS = 0, c1 = cS + 6 * Sh::SC, c2 = c1 + 64, cA = c2 + 64, cW = cA + NP * 32;
+    constexpr int cDS = DKP == 128 ? cS : cW + 96;
+    static_assert(cW + (DKP == 128 ? 96 : 160) <= 512, "tensor memory");
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = smem_raw + (1024 - (__cvta_generic_to_shared(smem_raw) & 1023)) % 1024;
+    WalkShared* ws = reinterpret_cast<WalkShared*>(smem);
+    unsigned char* stages = smem + 1024;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = warp >> 2;
     const int head = blockIdx.y, b = blockIdx.z, hk = head / p.group;
-    const int slice = blockIdx.x * 128, v0 = slice + warp * 16;
-    const int VP = Sh::vpitch(warps);
-    const size_t stage_bytes = Sh::stage_bytes(warps);
+    const int slice = blockIdx.x * 128, row = (warp & 3) * 32 + lane, vc = slice + row;
+    const bool live = vc < p.dv;
     const DeltaSeq s = delta_seq(p, b);
     const int chunks = (s.len + DL_C - 1) / DL_C;
     const long long img = delta_img(p, b);
     const T* q = reinterpret_cast<const T*>(p.q) + img * p.q_img + (long long)hk * p.dk;
     const T* k = reinterpret_cast<const T*>(p.k) + img * p.k_img + (long long)hk * p.dk;
     const T* dy = reinterpret_cast<const T*>(p.dy) + img * p.y_img + (long long)head * p.dv + slice;
+    T* dvalue = reinterpret_cast<T*>(p.dvalue);
+    if (dvalue) dvalue += (img * p.tokens * p.heads_v + head) * (long long)p.dv + slice;
+    const int dvs = min(128, p.dv - slice);
+    const size_t sbase = ((size_t)b * p.heads_v + head) * p.dk * p.dv;
 
-    auto stage_k = [&](int st) { return reinterpret_cast<__nv_bfloat16*>(smem + st * stage_bytes); };
-    auto issue = [&](int c, int st) {
-        __nv_bfloat16* K = stage_k(st);
-        __nv_bfloat16* Q = K + NP * PLANE;
-        __nv_bfloat16* Tt = Q + NP * PLANE;
-        T* O = reinterpret_cast<T*>(Tt + 6 * DL_C * DL_TPITCH);
-        float* vec = reinterpret_cast<float*>(O + DL_C * VP);
-        const size_t rec = (size_t)(s.slot + c) * p.heads_v + head;
-        load_tile(K, PITCH, PLANE, k, p.k_tok, p, s, c * DL_C, DKP, p.dk, tid, nthreads);
-        load_tile(Q, PITCH, PLANE, q, p.q_tok, p, s, c * DL_C, DKP, p.dk, tid, nthreads);
-        load_planes(Tt, p.wT + rec * 3 * DL_PLANE, 3, tid, nthreads);
-        load_planes(Tt + 3 * DL_C * DL_TPITCH, p.wP + rec * 3 * DL_PLANE, 3, tid, nthreads);
-        load_raw(O, VP, dy, p.y_tok, p, s, c * DL_C, warps * 16, p.dv - slice, tid, nthreads);
-        for (int i = tid; i < DL_SCANVECS / 4; i += nthreads)
-            cp_async16(vec + 4 * i, p.wvec + rec * DL_VECS + 4 * i, true);
+    float S[HS];  // dS^T[row][half * HS + i]
+#pragma unroll
+    for (int i = 0; i < HS; ++i) {
+        const int kc = half * HS + i;
+        S[i] = p.ds_in && live && kc < p.dk ? p.ds_in[sbase + (size_t)kc * p.dv + vc] : 0.f;
+    }
+    if (chunks == 0) {
+        if (p.ds_out && live)
+#pragma unroll
+            for (int i = 0; i < HS; ++i)
+                if (half * HS + i < p.dk) p.ds_out[sbase + (size_t)(half * HS + i) * p.dv + vc] = S[i];
+        return;
+    }
+
+    uint32_t mbar[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) mbar[i] = static_cast<uint32_t>(__cvta_generic_to_shared(&ws->mbar[i]));
+    if (warp == 0) tc_alloc(static_cast<uint32_t>(__cvta_generic_to_shared(&ws->tmem)));
+    if (tid == 0) {
+        for (int i = 0; i < 3; ++i) mbar_init(mbar[i], 1);
+        ws->dead = 0;
+    }
+    // n counts the chunks in the order of the walk, from the last to the first
+    auto rows_of = [&](int n) {
+        if (tid < DL_C) ws->rows[n % 3][tid] = delta_row(p, s, (chunks - 1 - n) * DL_C + tid);
+    };
+    auto issue = [&](int n, int st) {
+        unsigned char* base = stages + st * STAGE;
+        const size_t rec = (size_t)(s.slot + chunks - 1 - n) * p.heads_v + head;
+        const int* rows = ws->rows[n % 3];
+        walk_load<NP>(base, Sh::plane, k, p.k_tok, rows, DKP, p.dk, tid);
+        walk_load<NP>(base + Sh::oQ, Sh::plane, q, p.q_tok, rows, DKP, p.dk, tid);
+        walk_load_planes(base + Sh::oT, p.wT + rec * 3 * DL_PLANE, 3, tid);
+        walk_load_planes(base + Sh::oP, p.wP + rec * 3 * DL_PLANE, 3, tid);
+        constexpr int V = 16 / sizeof(T), vecs = 128 / V;
+        T* vd = reinterpret_cast<T*>(base + Sh::oV(3));
+        for (int i = tid; i < DL_C * vecs; i += DW_THREADS) {
+            const int r = i / vecs, cc = (i - r * vecs) * V;
+            const bool ok = rows[r] >= 0 && cc < dvs;
+            cp_async16(vd + r * Sh::vpitch + cc, ok ? dy + rows[r] * p.y_tok + cc : dy, ok);
+        }
+        if (tid < DL_SCANVECS / 4)
+            cp_async16(base + Sh::oVec(3) + 16 * tid, p.wvec + rec * DL_VECS + 4 * tid, true);
+    };
+    rows_of(0);
+    mbar_fence_init();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = ws->tmem, tl = tm + ((uint32_t)(warp & 3) << 21);
+    issue(0, 0);
+    cp_async_commit();
+
+    auto put_state = [&]() {
+#pragma unroll
+        for (int i = 0; i < HS; i += 32) {
+            float x[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = S[i + e];
+#pragma unroll
+            for (int n = 0; n < 3; ++n) {
+                uint32_t u[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) u[e] = split_bf16(x[2 * e], x[2 * e + 1]);
+                tc_st16(tl + cS + half * 3 * Sh::SC + n * Sh::SC + i / 2, u);
+            }
+        }
+    };
+    auto aS = [&](int x, int ks) { return tm + cS + (ks / (KT / 2)) * 3 * Sh::SC + x * Sh::SC + (ks % (KT / 2)) * 8; };
+    auto aO = [&](int x, int ks) { return tm + cA + (ks >> 1) * (NP * 16) + x * 16 + (ks & 1) * 8; };
+    auto aQ = [&](int x, int ks) { return tm + c2 + (ks >> 1) * 48 + x * 16 + (ks & 1) * 8; };
+    auto aW = [&](int x, int ks) { return tm + cW + (ks >> 1) * 48 + x * 16 + (ks & 1) * 8; };
+    auto put_out = [&](int n, int st) {  // dV, staged in dO's place, to whole rows
+        if (!dvalue) return;
+        constexpr int V = 16 / sizeof(T), vecs = 128 / V;
+        const T* vd = reinterpret_cast<const T*>(stages + st * STAGE + Sh::oV(3));
+        for (int i = tid; i < DL_C * vecs; i += DW_THREADS) {
+            const int r = i / vecs, cc = (i - r * vecs) * V;
+            const int at = ws->rows[n % 3][r];
+            if (at >= 0 && cc < dvs)
+                *reinterpret_cast<uint4*>(dvalue + (long long)at * p.heads_v * p.dv + cc) =
+                    *reinterpret_cast<const uint4*>(vd + r * Sh::vpitch + cc);
+        }
     };
 
-    float S[NT][4];  // dS^T
-    const size_t sbase = ((size_t)b * p.heads_v + head) * p.dk * p.dv;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int vc = v0 + gr + (e >> 1) * 8, kc = nt * 8 + tc + (e & 1);
-            S[nt][e] = p.ds_in && vc < p.dv && kc < p.dk ? p.ds_in[sbase + (size_t)kc * p.dv + vc] : 0.f;
-        }
-
-    if (Sh::STAGES == 2 && chunks > 0) {
-        issue(chunks - 1, 0);
-        cp_async_commit();
-    }
+    put_state();
     for (int n = 0; n < chunks; ++n) {
-        const int c = chunks - 1 - n, st = Sh::STAGES == 2 ? n & 1 : 0;
-        if (Sh::STAGES == 2) {
-            if (c > 0) issue(c - 1, st ^ 1);
+        const int st = Sh::STAGES == 2 ? n & 1 : 0;
+        const uint32_t par = n & 1;
+        unsigned char* base = stages + st * STAGE;
+        const uint32_t bK = static_cast<uint32_t>(__cvta_generic_to_shared(base)), bQ = bK + Sh::oQ, bT = bK + Sh::oT, bP = bK + Sh::oP;
+        T* vd = reinterpret_cast<T*>(base + Sh::oV(3));
+        const float* vec = reinterpret_cast<const float*>(base + Sh::oVec(3));
+        const size_t rec = (size_t)(s.slot + chunks - 1 - n) * p.heads_v + head;
+        if (Sh::STAGES == 1 && n > 0) {
+            __syncthreads();
+            put_out(n - 1, 0);
+            __syncthreads();
+            issue(n, 0);
             cp_async_commit();
-            cp_async_wait<1>();
-        } else {
-            issue(c, 0);
-            cp_async_commit();
-            cp_async_wait<0>();
         }
+        cp_async_wait<0>();
+        tc_fence_smem();
         __syncthreads();
-        __nv_bfloat16* K = stage_k(st);
-        __nv_bfloat16* Q = K + NP * PLANE;
-        __nv_bfloat16* Tt = Q + NP * PLANE;
-        __nv_bfloat16* P = Tt + 3 * DL_C * DL_TPITCH;
-        T* O = reinterpret_cast<T*>(P + 3 * DL_C * DL_TPITCH);
-        const float* vec = reinterpret_cast<const float*>(O + DL_C * VP);
-        const size_t rec = (size_t)(s.slot + c) * p.heads_v + head;
-
+        float o[32], x[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = o[i] = to_float(vd[(half * 32 + i) * Sh::vpitch + row]);
+        put_terms<NP>(tl + cA + half * (NP * 16), x);
+        tc_wait_st();
+        tc_fence_before();
+        __syncthreads();
+        if (tid == 0) {  // 1
+            tc_fence_after();
+            tc_product<3, NP, 2, KT>(tm + c1, tc_idesc(64, false), false, aS, [bK](int i, int ks) {
+                return tc_desc(bK + i * Sh::plane + (ks >> 2) * TC_TILE + (ks & 3) * 32);
+            });
+            tc_product<NP, 3, 2, 4>(tm + c2, tc_idesc(64, true), false, aO,
+                                    [bP](int i, int ks) { return tc_desc(bP + i * TC_TILE + ks * 2048); });
+            tc_commit(mbar[0]);
+        }
+        if (Sh::STAGES == 2 && n > 0) put_out(n - 1, st ^ 1);
+        if (n + 1 < chunks) rows_of(n + 1);
+        if (live) {  // the gradient of the state leaving the chunk
+            float* g = p.wdS + rec * p.dv * DKP + vc;
+#pragma unroll
+            for (int i = 0; i < HS; ++i) g[(size_t)(half * HS + i) * p.dv] = S[i];
+        }
+        mbar_wait(mbar[0], par, &ws->dead);
+        tc_fence_after();
         {
-            float* o = p.wdS + rec * p.dv * DKP;
+            float z[32];
+            tc_ld32(tl + c1 + half * 32, x);
+            tc_ld32(tl + c2 + half * 32, z);
+            tc_wait_ld();
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (v0 + gr + h * 8 < p.dv)
-                        *reinterpret_cast<float2*>(o + (size_t)(v0 + gr + h * 8) * DKP + nt * 8 + tc) =
-                            make_float2(S[nt][2 * h], S[nt][2 * h + 1]);
+            for (int i = 0; i < 32; ++i) x[i] = vec[DL_C + half * 32 + i] * x[i] + z[i];
         }
-        // dW^T = e^{G_C - G} (dS^T K^T) + dO^T P
-        float dw[8][4] = {};
-#pragma unroll
-        for (int kt = 0; kt < DKP / 16; ++kt) {
-            Frag4 sa[3];
-            split_tiles<3>(S[2 * kt], S[2 * kt + 1], sa);
-#pragma unroll
-            for (int nt = 0; nt < 8; nt += 2) {
-                Frag4 f[NP];
-#pragma unroll
-                for (int i = 0; i < NP; ++i) f[i] = load_b(K + i * PLANE, PITCH, nt * 8, kt * 16, lane);
-                mma_terms<3, NP>(dw[nt], dw[nt + 1], sa, f);
-            }
-        }
-#pragma unroll
-        for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) dw[nt][e] *= vec[DL_C + nt * 8 + tc + (e & 1)];
-        // a pair of 8-step tiles of dO^T
-        auto tile = [&](int kt, float (&lo)[4], float (&hi)[4]) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int col = warp * 16 + gr + (e >> 1) * 8;
-                lo[e] = to_float(O[(kt * 16 + tc + (e & 1)) * VP + col]);
-                hi[e] = to_float(O[(kt * 16 + 8 + tc + (e & 1)) * VP + col]);
-            }
-        };
-#pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
-            float lo[4], hi[4];
-            tile(kt, lo, hi);
-            Frag4 oa[NP];
-            split_tiles<NP>(lo, hi, oa);
-#pragma unroll
-            for (int nt = 0; nt <= 2 * kt; nt += 2) {
-                Frag4 f[3];
-#pragma unroll
-                for (int i = 0; i < 3; ++i) f[i] = load_b_t(P + i * DL_C * DL_TPITCH, DL_TPITCH, nt * 8, kt * 16, lane);
-                mma_terms<NP, 3>(dw[nt], dw[nt + 1], oa, f);
-            }
-        }
-        // dX^T = dW^T T
-        float dx[8][4] = {};
-#pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
-            Frag4 wa[3];
-            split_tiles<3>(dw[2 * kt], dw[2 * kt + 1], wa);
-#pragma unroll
-            for (int nt = 0; nt <= 2 * kt; nt += 2) {
-                Frag4 f[3];
-#pragma unroll
-                for (int i = 0; i < 3; ++i) f[i] = load_b_t(Tt + i * DL_C * DL_TPITCH, DL_TPITCH, nt * 8, kt * 16, lane);
-                mma_terms<3, 3>(dx[nt], dx[nt + 1], wa, f);
-            }
-        }
-        // dS^T = e^{G_C} dS^T + (scale e^G dO)^T Q - (e^G dV)^T K
-        const float eC = vec[3 * DL_C];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) S[nt][e] *= eC;
-        float* ox = p.wdX + rec * DL_C * p.dv;
-#pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
-            float lo[4], hi[4];
-            tile(kt, lo, hi);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                lo[e] *= p.scale * vec[kt * 16 + tc + (e & 1)];
-                hi[e] *= p.scale * vec[kt * 16 + 8 + tc + (e & 1)];
-            }
-            Frag4 oa[3], va[3];
-            split_tiles<3>(lo, hi, oa);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int r = (2 * kt + h) * 8 + tc + (e & 1), vc = v0 + gr + (e >> 1) * 8;
-                    float& x = dx[2 * kt + h][e];
-                    if (vc < p.dv) ox[(size_t)r * p.dv + vc] = x;
-                    x *= vec[2 * DL_C + r];  // dV from here on
-                    (h ? hi : lo)[e] = -vec[r] * x;
-                }
-            split_tiles<3>(lo, hi, va);
-#pragma unroll
-            for (int nt = 0; nt < NT; nt += 2) {
-                Frag4 f[NP];
-#pragma unroll
-                for (int i = 0; i < NP; ++i) f[i] = load_b_t(Q + i * PLANE, PITCH, nt * 8, kt * 16, lane);
-                mma_terms<3, NP>(S[nt], S[nt + 1], oa, f);
-#pragma unroll
-                for (int i = 0; i < NP; ++i) f[i] = load_b_t(K + i * PLANE, PITCH, nt * 8, kt * 16, lane);
-                mma_terms<3, NP>(S[nt], S[nt + 1], va, f);
-            }
-        }
-        if (p.dvalue) {  // through this warp's own columns of dO, now read, to whole rows
-            T* o = reinterpret_cast<T*>(p.dvalue) + (img * p.tokens * p.heads_v + head) * (long long)p.dv;
-            __syncwarp();
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    store_elem(O + (nt * 8 + tc + (e & 1)) * VP + warp * 16 + gr + (e >> 1) * 8, dx[nt][e]);
-            __syncwarp();
-            constexpr int VE = 16 / sizeof(T), VR = 16 / VE;
-#pragma unroll
-            for (int i = 0; i < DL_C * VR / 32; ++i) {
-                const int r = (i * 32 + lane) / VR, cc = ((i * 32 + lane) % VR) * VE;
-                const int row = delta_row(p, s, c * DL_C + r);
-                if (row >= 0 && v0 + cc < p.dv)
-                    *reinterpret_cast<uint4*>(o + (long long)row * p.heads_v * p.dv + v0 + cc) =
-                        *reinterpret_cast<const uint4*>(O + r * VP + warp * 16 + cc);
-            }
-        }
+        put_terms<3>(tl + cW + half * 48, x);
+        tc_wait_st();
+        tc_fence_before();
         __syncthreads();
-    }
-    if (p.ds_out) {
+        if (tid == 0) {  // 2
+            tc_fence_after();
+            tc_product<3, 3, 2, 4>(tm + c1, tc_idesc(64, true), false, aW,
+                                   [bT](int i, int ks) { return tc_desc(bT + i * TC_TILE + ks * 2048); });
+            tc_commit(mbar[1]);
+        }
+        if (Sh::STAGES == 2) {
+            if (n + 1 < chunks) issue(n + 1, st ^ 1);
+            cp_async_commit();
+        }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int i = 0; i < 32; ++i) o[i] *= p.scale * vec[half * 32 + i];
+        put_terms<3>(tl + c2 + half * 48, o);
+        mbar_wait(mbar[1], par, &ws->dead);
+        tc_fence_after();
+        tc_ld32(tl + c1 + half * 32, x);
+        tc_wait_ld();
+        if (live) {
+            float* ox = p.wdX + rec * DL_C * p.dv + vc;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int vc = v0 + gr + (e >> 1) * 8, kc = nt * 8 + tc + (e & 1);
-                if (vc < p.dv && kc < p.dk) p.ds_out[sbase + (size_t)kc * p.dv + vc] = S[nt][e];
+            for (int i = 0; i < 32; ++i) ox[(size_t)(half * 32 + i) * p.dv] = x[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const int r = half * 32 + i;
+            x[i] *= vec[2 * DL_C + r];  // dV
+            store_elem(vd + r * Sh::vpitch + row, x[i]);
+            x[i] *= -vec[r];
+        }
+        put_terms<3>(tl + cW + half * 48, x);
+        tc_wait_st();
+        tc_fence_before();
+        __syncthreads();
+        if (tid == 0) {  // 3
+            tc_fence_after();
+#pragma unroll
+            for (int nb = 0; nb < Sh::KB; ++nb) {
+                auto mn = [nb](uint32_t t) {
+                    return [t, nb](int i, int ks) { return tc_desc(t + i * Sh::plane + nb * TC_TILE + ks * 2048); };
+                };
+                const uint32_t d = tm + cDS + nb * (3 * Sh::SC);
+                tc_product<3, NP, 2, 4>(d, tc_idesc(64, true), false, aQ, mn(bQ));
+                tc_product<3, NP, 2, 4>(d, tc_idesc(64, true), true, aW, mn(bK));
             }
+            tc_commit(mbar[2]);
+        }
+        const float eC = vec[3 * DL_C];
+        mbar_wait(mbar[2], par, &ws->dead);
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < HS; i += 32) {
+            tc_ld32(tl + cDS + (DKP == 128 ? half * 3 * Sh::SC : half * 32) + i, x);
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) S[i + e] = eC * S[i + e] + x[e];
+        }
+        put_state();
     }
+    tc_wait_st();
+    cp_async_wait<0>();
+    tc_fence_before();
+    __syncthreads();
+    put_out(chunks - 1, Sh::STAGES == 2 ? (chunks - 1) & 1 : 0);
+    if (p.ds_out && live)
+#pragma unroll
+        for (int i = 0; i < HS; ++i)
+            if (half * HS + i < p.dk) p.ds_out[sbase + (size_t)(half * HS + i) * p.dv + vc] = S[i];
+    if (p.status && tid == 0 && ws->dead) atomicOr(p.status, DEV_STATUS_TIMEOUT);
+    if (warp == 0) tc_free(tm);
 }
 
 // ---- per-chunk gradients -------------------------------------------------------------
@@ -260,8 +287,9 @@ struct GradShape {
     static constexpr int NP = DeltaIo<T>::planes;
     static constexpr int pitch = DKP + 8;
     static constexpr int plane = DL_C * pitch;
-    // K, Q, a slab of a state in three planes; E and M in three planes each; row sums
-    static constexpr size_t smem = (size_t)(2 * NP + 3) * plane * 2 + (size_t)6 * DL_C * DL_TPITCH * 2 +
+    static constexpr int splane = DKP * DL_TPITCH;  // a slab of a state: [DKP][64 value channels]
+    // K, Q; a slab of a state, E and M in three planes each; row sums
+    static constexpr size_t smem = (size_t)2 * NP * plane * 2 + (size_t)3 * splane * 2 + (size_t)6 * DL_C * DL_TPITCH * 2 +
                                    6 * DL_C * 8 + (5 * DL_C + 16) * 4;
 };
 
@@ -291,7 +319,7 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaParams p)
     __nv_bfloat16* K = reinterpret_cast<__nv_bfloat16*>(red + 16);
     __nv_bfloat16* Q = K + NP * PLANE;
     __nv_bfloat16* St = Q + NP * PLANE;
-    __nv_bfloat16* E = St + 3 * PLANE;
+    __nv_bfloat16* E = St + 3 * Sh::splane;
     __nv_bfloat16* M = E + 3 * DL_C * DL_TPITCH;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tc = (lane & 3) * 2;
     const int head = blockIdx.y, hk = head / p.group;
@@ -338,13 +366,13 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaParams p)
     for (int slab = 0; slab < p.dv; slab += DL_C) {
         const int cols = min(DL_C, p.dv - slab);
         auto load_state = [&](const float* src, const float* other) {
-            for (int i = tid; i < DL_C * (DKP / 4); i += 256) {
-                const int r = i / (DKP / 4), cc = (i - r * (DKP / 4)) * 4;
+            for (int i = tid; i < DKP * (DL_C / 4); i += 256) {
+                const int r = i / (DL_C / 4), cc = (i - r * (DL_C / 4)) * 4;
                 float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (r < cols) {
-                    x = __ldg(reinterpret_cast<const float4*>(src + (size_t)(slab + r) * DKP + cc));
+                if (cc < cols) {
+                    x = __ldg(reinterpret_cast<const float4*>(src + (size_t)r * p.dv + slab + cc));
                     if (other) {
-                        const float4 z = __ldg(reinterpret_cast<const float4*>(other + (size_t)(slab + r) * DKP + cc));
+                        const float4 z = __ldg(reinterpret_cast<const float4*>(other + (size_t)r * p.dv + slab + cc));
                         dots += x.x * z.x + x.y * z.y + x.z * z.z + x.w * z.w;
                     }
                 }
@@ -353,7 +381,7 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaParams p)
                     uint2 u;
                     u.x = split_bf16(x.x, x.y);
                     u.y = split_bf16(x.z, x.w);
-                    *reinterpret_cast<uint2*>(St + n * PLANE + r * PITCH + cc) = u;
+                    *reinterpret_cast<uint2*>(St + n * Sh::splane + r * DL_TPITCH + cc) = u;
                 }
             }
         };
@@ -399,7 +427,7 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaParams p)
             for (int nt = 0; nt < NH; nt += 2) {
                 Frag4 f[3];
 #pragma unroll
-                for (int n = 0; n < 3; ++n) f[n] = load_b_t(St + n * PLANE, PITCH, n0 + nt * 8, kt * 16, lane);
+                for (int n = 0; n < 3; ++n) f[n] = load_b(St + n * Sh::splane, DL_TPITCH, n0 + nt * 8, kt * 16, lane);
                 mma_terms<NP, 3>(dq[nt], dq[nt + 1], oa, f);
                 mma_terms<3, 3>(dkr[nt], dkr[nt + 1], va, f);
             }
@@ -435,7 +463,7 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaParams p)
             for (int nt = 0; nt < NH; nt += 2) {
                 Frag4 f[3];
 #pragma unroll
-                for (int n = 0; n < 3; ++n) f[n] = load_b_t(St + n * PLANE, PITCH, n0 + nt * 8, kt * 16, lane);
+                for (int n = 0; n < 3; ++n) f[n] = load_b(St + n * Sh::splane, DL_TPITCH, n0 + nt * 8, kt * 16, lane);
                 mma_terms<3, 3>(dkc[nt], dkc[nt + 1], wa, f);
             }
         }
