@@ -123,7 +123,7 @@ long long slots_of(const vscan_route* r, const vscan_delta_args* a)
 bool empty(const vscan_delta_args* a) { return a->batch == 0; }
 
 struct Layout {
-    size_t T, P, vec, total;
+    size_t total;  // the records
     size_t L, S, dS, W, dX, part, dq, dk, grad_total;  // backward
 };
 
@@ -131,10 +131,7 @@ Layout forward_layout(const vscan_route* r, const vscan_delta_args* a, int pplan
 {
     const size_t n = (size_t)slots_of(r, a) * a->heads_v;
     Layout l;
-    l.T = 0;
-    l.P = l.T + round256(n * 3 * vscan::DL_PLANE * 2);
-    l.vec = l.P + round256(n * pplanes * vscan::DL_PLANE * 2);
-    l.total = l.vec + round256(n * vscan::DL_VECS * 4);
+    l.total = round256(n * vscan::delta_record_bytes(pplanes));
     return l;
 }
 
@@ -294,9 +291,7 @@ vscan_status vscan_delta_forward(const vscan_route* route, const vscan_delta_arg
     DeltaParams p = make_params(route, args);
     char* ws = static_cast<char*>(args->workspace);
     p.tplanes = forward_planes(args);
-    p.wT = reinterpret_cast<__nv_bfloat16*>(ws + l.T);
-    p.wP = reinterpret_cast<__nv_bfloat16*>(ws + l.P);
-    p.wvec = reinterpret_cast<float*>(ws + l.vec);
+    p.wrec = reinterpret_cast<unsigned char*>(ws);
     const cudaError_t e = DELTA_DISPATCH(run_forward, args, p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? VSCAN_OK : cuda_fail(e, "vscan_delta_forward");
 }
@@ -353,9 +348,7 @@ vscan_status vscan_delta_backward(const vscan_route* route, const vscan_delta_ar
     char* ws = static_cast<char*>(grads->workspace);
     p.s_out = nullptr;
     p.tplanes = 3;
-    p.wT = reinterpret_cast<__nv_bfloat16*>(ws + l.T);
-    p.wP = reinterpret_cast<__nv_bfloat16*>(ws + l.P);
-    p.wvec = reinterpret_cast<float*>(ws + l.vec);
+    p.wrec = reinterpret_cast<unsigned char*>(ws);
     p.wL = reinterpret_cast<float*>(ws + l.L);
     p.wS = reinterpret_cast<float*>(ws + l.S);
     p.wdS = reinterpret_cast<float*>(ws + l.dS);

@@ -42,8 +42,7 @@ constexpr int DL_C = 64;          // steps per chunk
 constexpr int DL_TPITCH = 72;     // shared-memory row pitch of a 64-wide bf16 tile: 144 bytes, an odd
                                   // multiple of 16, so ldmatrix rows fall into different banks
 // Floats per chunk in the workspace: e^{G_i}, e^{G_C - G_i}, beta_i, {e^{G_C}}, and G_i in float64.
-constexpr int DL_VECS = 6 * DL_C;
-constexpr int DL_SCANVECS = 4 * DL_C;  // those that the walks read
+constexpr int DL_VECS = 8 * DL_C;  // 2048 bytes, so that the planes behind them keep their alignment
 constexpr int DL_PLANE = DL_C * DL_C;
 
 struct DeltaParams {
@@ -65,9 +64,8 @@ struct DeltaParams {
     float scale, beta_scale;
     long long q_tok, q_img, k_tok, k_img, v_tok, v_img, a_tok, a_img, b_tok, b_img, y_tok, y_img;
     // workspace, indexed by slot * heads_v + head
-    __nv_bfloat16* wT;   // [..][3][64][64]
-    __nv_bfloat16* wP;   // [..][tplanes][64][64]
-    float* wvec;         // [..][DL_VECS]
+    unsigned char* wrec; // records: DL_VECS floats, three planes of T, tplanes planes of P; each plane [64][64]
+                         // the image of a swizzled tile, so that a walk copies a record as it is
     float* wL;           // [..][64][64]: e^{G_i - G_j} k_i.k_j below the diagonal (backward, else null)
     float* wS;           // [..][DKP][dv]: state entering the chunk (backward)
     float* wW;           // [..][64][dv]: W of the chunk (backward)
@@ -119,6 +117,18 @@ __device__ __forceinline__ int delta_row(const DeltaParams& p, const DeltaSeq& s
 }
 
 __device__ __forceinline__ long long delta_img(const DeltaParams& p, int b) { return p.offsets ? 0 : b; }
+
+// Parts of a record.
+__host__ __device__ __forceinline__ size_t delta_record_bytes(int tplanes) { return DL_VECS * 4 + (size_t)(3 + tplanes) * DL_PLANE * 2; }
+__device__ __forceinline__ float* record_vec(const DeltaParams& p, size_t rec)
+{
+    return reinterpret_cast<float*>(p.wrec + rec * delta_record_bytes(p.tplanes));
+}
+__device__ __forceinline__ __nv_bfloat16* record_T(const DeltaParams& p, size_t rec)
+{
+    return reinterpret_cast<__nv_bfloat16*>(record_vec(p, rec) + DL_VECS);
+}
+__device__ __forceinline__ __nv_bfloat16* record_P(const DeltaParams& p, size_t rec) { return record_T(p, rec) + 3 * DL_PLANE; }
 
 // ---- tensor-core fragments ------------------------------------------------------
 // m16n8k16: lane (g, t) = (lane / 4, lane % 4) holds of A the pairs of columns
@@ -173,14 +183,24 @@ __device__ __forceinline__ Frag4 load_b_t(const __nv_bfloat16* t, int pitch, int
     return ldsm4t(t + (k0 + (lane & 7) + ((lane >> 3) & 1) * 8) * pitch + n0 + (lane >> 4) * 8);
 }
 
-// x = h + r for a pair: h rounded to bf16 (packed, x in the low half), r exact.
+// x = h + r for a pair: h the upper 16 bits (packed, x in the low half), r exact. Cutting
+// instead of rounding, three terms hold the 24 bits of a float32 exactly, and the integer
+// pipe, which bounds the walks, does a byte permutation where the conversion to bf16 takes it
+// four times as long (56x56 cross-scan walk, batch 16: 197 against 150 us).
 __device__ __forceinline__ uint32_t split_bf16(float& x, float& y)
 {
+    const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+    const float2 r = __fadd2_rn(make_float2(x, y), make_float2(-__uint_as_float(a & 0xffff0000u), -__uint_as_float(b & 0xffff0000u)));
+    x = r.x;
+    y = r.y;
+    return __byte_perm(a, b, 0x7632);
+}
+
+// The rounded pair, for fewer than three terms.
+__device__ __forceinline__ uint32_t round_bf16(float x, float y)
+{
     const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-    const uint32_t u = *reinterpret_cast<const uint32_t*>(&h);
-    x -= __uint_as_float(u << 16);
-    y -= __uint_as_float(u & 0xffff0000u);
-    return u;
+    return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // NT bf16 terms of a pair of C tiles as A fragments.
@@ -307,6 +327,9 @@ __device__ __forceinline__ float exp_diff(double d)
     return e + e * (float)(d - (double)h);
 }
 
+// Element (i, j) of a 64 x 64 plane of the workspace: the image of a swizzled tile.
+__device__ __forceinline__ int plane_at(int i, int j) { return tc_swizzle(i, j >> 3) / 2 + (j & 7); }
+
 // ---- per-chunk triangle: T, P, decays -----------------------------------------------
 // One CTA of four warps per chunk and value head. Bound by latency: two
 // 64 x 64 x dk products, 4 x 16 dependent rows of forward substitution and three
@@ -388,7 +411,7 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaParams p)
         G[2 * lane] = sum - g[1];
         G[2 * lane + 1] = sum;
         __syncwarp();
-        float* vec = p.wvec + rec * DL_VECS;
+        float* vec = record_vec(p, rec);
         const double last = G[DL_C - 1];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -425,7 +448,7 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaParams p)
                 }
             }
         }
-        __nv_bfloat16* wP = p.wP + rec * p.tplanes * DL_PLANE;
+        __nv_bfloat16* wP = record_P(p, rec);
         const int gr = lane >> 2, tc = (lane & 3) * 2;
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)
@@ -443,8 +466,15 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaParams p)
                     Ti[i * DL_LP + j + e] = 0.f;
                 }
                 if (p.wL) *reinterpret_cast<float2*>(p.wL + rec * DL_PLANE + i * DL_C + j) = make_float2(lv[0], lv[1]);
-                for (int n = 0; n < p.tplanes; ++n)
-                    *reinterpret_cast<uint32_t*>(wP + n * DL_PLANE + i * DL_C + j) = split_bf16(pv[0], pv[1]);
+                if (p.tplanes == 2) {  // rounded, both: what the product of the second terms would add is left out
+                    const uint32_t u = round_bf16(pv[0], pv[1]);
+                    *reinterpret_cast<uint32_t*>(wP + plane_at(i, j)) = u;
+                    *reinterpret_cast<uint32_t*>(wP + DL_PLANE + plane_at(i, j)) =
+                        round_bf16(pv[0] - __uint_as_float(u << 16), pv[1] - __uint_as_float(u & 0xffff0000u));
+                } else {
+                    for (int n = 0; n < 3; ++n)
+                        *reinterpret_cast<uint32_t*>(wP + n * DL_PLANE + plane_at(i, j)) = split_bf16(pv[0], pv[1]);
+                }
             }
     }
     __syncthreads();
@@ -491,34 +521,40 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaParams p)
         }
         __syncthreads();
     }
-    __nv_bfloat16* wT = p.wT + rec * 3 * DL_PLANE;
+    __nv_bfloat16* wT = record_T(p, rec);
     for (int i = tid; i < DL_PLANE / 2; i += 128) {
         const int r = i >> 5, j = (i & 31) * 2;
         float x = Ti[r * DL_LP + j], y = Ti[r * DL_LP + j + 1];
 #pragma unroll
-        for (int n = 0; n < 3; ++n) *reinterpret_cast<uint32_t*>(wT + n * DL_PLANE + r * DL_C + j) = split_bf16(x, y);
+        for (int n = 0; n < 3; ++n) *reinterpret_cast<uint32_t*>(wT + n * DL_PLANE + plane_at(r, j)) = split_bf16(x, y);
     }
 }
 
 // ---- the walk over the chunks -----------------------------------------------------
-// One CTA of 256 threads per image (sequence), value head and slice of 128 value
-// channels. The products are formed transposed, with the value channel as the row of
-// the 128-row tensor-core tile, so that a thread holds half a row of everything in
-// registers: of S^T[128][DKP] (float32, for the whole walk), and in turn of
-// (K S)^T, X^T, W^T and y^T[128][64]. Between two products it rescales its values,
-// splits them into bf16 terms and stores them to tensor memory as the next left
-// operand; no value crosses threads. Per chunk:
+// One CTA per image (sequence), value head and slice of 128 value channels. The
+// products are formed transposed, with the value channel as the row of the 128-row
+// tensor-core tile, so that a thread holds half a row of everything in registers: of
+// S^T[128][DKP] (float32, for the whole walk), and in turn of (K S)^T, X^T, W^T and
+// y^T[128][64]. Between two products it rescales its values, splits them into bf16
+// terms and stores them to tensor memory as the next left operand; no value crosses
+// threads. Per chunk:
 //
 //   1. KS = S K^T, QS = S Q^T                 B = K, Q    (K-major)
 //   2. X = beta (V - e^G KS);  W = X T^T      B = T       (K-major)
-//   3. O = W P^T, dS = (e^{G_C - G} W) K      B = P (K-major), K (MN-major: the same tile)
-//   4. y = scale e^G QS + O;  S = e^{G_C} S + dS   (float32, in registers)
+//   3. dS = (e^{G_C - G} W) K, O = W P^T      B = K (MN-major: the same tile), P (K-major)
+//   4. S = e^{G_C} S + dS (float32, in registers);  y = scale e^G QS + O
 //
-// The chain of dependent products bounds the walk: the chunk's tiles are copied one
-// chunk ahead, and y leaves while the next chunk's first product runs.
+// The chain KS -> W -> dS -> S bounds the walk, so everything else is off it: eight
+// warps compute, one thread issues the products (the ones of the chain first), three
+// warps copy the next chunk's tiles in and the last one's y out, and a computing
+// thread never waits for another one, only for products. y of a chunk is finished
+// while the next one's KS runs. T and P are lower triangles: slice ks of their summed
+// index touches the columns from 16 ks on only.
 // Tensor-memory columns: S terms (over them dS, once step 1 is done), KS (W, then W's
 // terms for O), QS, X's terms (then those of e^{G_C - G} W), O.
-constexpr int DW_THREADS = 256;
+constexpr int DW_COMPUTE = 256, DW_HELP = 96, DW_THREADS = 384;  // warps 0-7, 9-11, all (warp 8 issues)
+// Registers a thread: 384 x 168 at launch, split 200 / 96: 256 x 200 + 128 x 96 = 63488 of 64512.
+constexpr int DW_REGS_COMPUTE = 200, DW_REGS_HELP = 96;
 
 template <typename T, int DKP>
 struct WalkShape {
@@ -528,44 +564,67 @@ struct WalkShape {
     static constexpr int KB = DKP / 64;          // 64-wide tiles of K
     static constexpr int plane = KB * TC_TILE;   // bytes
     static constexpr int vpitch = 128 + 16 / (int)sizeof(T);
-    static constexpr int oQ = NP * plane, oT = 2 * NP * plane, oP = oT + 3 * TC_TILE;
+    // a stage: K, Q, the chunk's record, V
+    static constexpr int oQ = NP * plane, oVec = 2 * NP * plane, oT = oVec + DL_VECS * 4, oP = oT + 3 * TC_TILE;
     static __host__ __device__ constexpr int oV(int pplanes) { return oP + pplanes * TC_TILE; }
-    static __host__ __device__ constexpr int oVec(int pplanes) { return oV(pplanes) + DL_C * vpitch * (int)sizeof(T); }
-    static __host__ __device__ constexpr int stage(int pplanes) { return (oVec(pplanes) + DL_SCANVECS * 4 + 1023) / 1024 * 1024; }
+    static __host__ __device__ constexpr int stage(int pplanes)
+    {
+        return (oV(pplanes) + DL_C * vpitch * (int)sizeof(T) + 1023) / 1024 * 1024;
+    }
     // at least half of the SM's shared memory: one CTA an SM, which owns all tensor memory
     static __host__ __device__ constexpr size_t smem(int pplanes)
     {
         const size_t n = 1024 + 1024 + (size_t)STAGES * stage(pplanes);
         return n < 120 * 1024 ? 120 * 1024 : n;
     }
-    // tensor-memory columns of half a row's terms: of S (DKP / 2 values), of a 64-wide operand (32)
-    static constexpr int SC = DKP / 4, XC = 16;
+    // tensor-memory columns of one term of half a row of S (DKP / 2 values)
+    static constexpr int SC = DKP / 4;
 };
 
-// Tile rows of a token array into swizzled shared memory, as load_tile.
-template <int NP>
-__device__ __forceinline__ void walk_load(unsigned char* dst, int plane, const __nv_bfloat16* src, long long tok, const int* rows,
-                                          int cols, int have, int tid)
+// The copying warps move rows of VECS 16-byte pieces; a thread keeps to one piece and to every
+// (DW_HELP / VECS)-th row, four rows at a time: their token rows are read before the first of
+// the four copies, which those reads could not pass. Not unrolled further: this code runs once
+// a chunk between the computing warps' long one, and unrolled it spent its time on
+// instruction-cache misses (70 to 140 cycles a piece).
+template <int VECS, typename F>
+__device__ __forceinline__ void copy_rows(const int* rows, int tid, F copy)
 {
-    const int vecs = cols / 8;
-    for (int i = tid; i < DL_C * vecs; i += DW_THREADS) {
-        const int r = i / vecs, c = i - r * vecs;
-        const int row = rows[r];
-        const bool ok = row >= 0 && c * 8 < have;
-        cp_async16(dst + tc_swizzle(r, c), ok ? src + row * tok + c * 8 : src, ok);
+    constexpr int step = DW_HELP / VECS, B = 4;
+#pragma unroll 1
+    for (int r = tid / VECS; r < DL_C; r += B * step) {
+        int row[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i) row[i] = rows[min(r + i * step, DL_C - 1)];
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+            if (r + i * step < DL_C) copy(r + i * step, row[i]);
     }
 }
-template <int NP>
-__device__ __forceinline__ void walk_load(unsigned char* dst, int plane, const float* src, long long tok, const int* rows, int cols,
-                                          int have, int tid)
+
+// The 64 rows of a token array into swizzled shared memory in bf16 planes, zero where there is
+// no token and from column `have` on.
+template <int COLS>
+__device__ __forceinline__ void walk_load(unsigned char* dst, const __nv_bfloat16* src, long long tok, const int* rows, int have,
+                                          int tid)
 {
-    const int vecs = cols / 8;
-    for (int i = tid; i < DL_C * vecs; i += DW_THREADS) {
-        const int r = i / vecs, c = i - r * vecs;
-        const int row = rows[r];
+    constexpr int vecs = COLS / 8;
+    const int c = tid % vecs;
+    const bool in = c * 8 < have;
+    const __nv_bfloat16* at = in ? src + c * 8 : src;
+    copy_rows<vecs>(rows, tid, [&](int r, int row) {
+        const bool ok = in && row >= 0;
+        copy16(dst + tc_swizzle(r, c), at + (ok ? row * tok : 0), ok);
+    });
+}
+template <int COLS>
+__device__ __forceinline__ void walk_load(unsigned char* dst, const float* src, long long tok, const int* rows, int have, int tid)
+{
+    constexpr int vecs = COLS / 8, plane = COLS / 64 * TC_TILE;
+    const int c = tid % vecs;
+    copy_rows<vecs>(rows, tid, [&](int r, int row) {
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f), z = x;
-        if (row >= 0 && c * 8 < have) x = __ldg(reinterpret_cast<const float4*>(src + row * tok + c * 8));
-        if (row >= 0 && c * 8 + 4 < have) z = __ldg(reinterpret_cast<const float4*>(src + row * tok + c * 8 + 4));
+        if (row >= 0 && c * 8 < have) x = __ldg(reinterpret_cast<const float4*>(src + c * 8 + row * tok));
+        if (row >= 0 && c * 8 + 4 < have) z = __ldg(reinterpret_cast<const float4*>(src + c * 8 + 4 + row * tok));
 #pragma unroll
         for (int n = 0; n < 3; ++n) {
             uint4 u;
@@ -575,66 +634,204 @@ __device__ __forceinline__ void walk_load(unsigned char* dst, int plane, const f
             u.w = split_bf16(z.z, z.w);
             *reinterpret_cast<uint4*>(dst + n * plane + tc_swizzle(r, c)) = u;
         }
-    }
+    });
 }
 
-// 64 x 64 planes of the workspace into swizzled shared memory.
-__device__ __forceinline__ void walk_load_planes(unsigned char* dst, const __nv_bfloat16* src, int planes, int tid)
+// The rows of a value-shaped token array (up to 128 channels of them), unsplit, in and out. A
+// bulk copy a row would be fewer instructions, but they issue one after the other: 64 of them
+// took 2600 cycles.
+template <typename T>
+__device__ __forceinline__ void walk_load_values(T* dst, int pitch, const T* src, long long tok, const int* rows, int have, int tid)
 {
-    for (int i = tid; i < planes * (DL_C * 8); i += DW_THREADS) {
-        const int r = (i >> 3) & 63, c = i & 7, n = i >> 9;
-        cp_async16(dst + n * TC_TILE + tc_swizzle(r, c), src + (size_t)i * 8, true);
+    constexpr int V = 16 / sizeof(T), vecs = 128 / V;
+    const int c = tid % vecs * V;
+    const bool in = c < have;
+    const T* at = in ? src + c : src;
+    copy_rows<vecs>(rows, tid, [&](int r, int row) {
+        const bool ok = in && row >= 0;
+        copy16(dst + r * pitch + c, at + (ok ? row * tok : 0), ok);
+    });
+}
+template <typename T>
+__device__ __forceinline__ void walk_store_values(T* dst, long long tok, const T* src, int pitch, const int* rows, int have, int tid)
+{
+    constexpr int V = 16 / sizeof(T), vecs = 128 / V, step = DW_HELP / vecs;
+    const int c = tid % vecs * V;
+    if (c >= have) return;
+    constexpr int B = 4;
+#pragma unroll 1
+    for (int r = tid / vecs; r < DL_C; r += B * step) {
+        int row[B];
+        uint4 x[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            const int rs = min(r + i * step, DL_C - 1);
+            row[i] = rows[rs];
+            x[i] = *reinterpret_cast<const uint4*>(src + rs * pitch + c);
+        }
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+            if (r + i * step < DL_C && row[i] >= 0) *reinterpret_cast<uint4*>(dst + row[i] * tok + c) = x[i];
     }
 }
 
-// NT bf16 terms of 32 values of a row, stored NT * 16 columns from `addr` on.
-template <int NT>
-__device__ __forceinline__ void put_terms(uint32_t addr, float (&v)[32])
+// NT bf16 terms of 32 values of a row, term n in the 16 columns from addr + n * step on. Three
+// are cut (exact); one or two are rounded (2^-18 for two, cut ones would leave 2^-16), unless
+// CUT says that more follow elsewhere.
+template <int NT, bool CUT = NT == 3>
+__device__ __forceinline__ void put_terms(uint32_t addr, int step, float (&v)[32])
 {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         uint32_t u[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) u[i] = split_bf16(v[2 * i], v[2 * i + 1]);
-        tc_st16(addr + n * 16, u);
+        for (int i = 0; i < 16; ++i) {
+            if (CUT) {
+                u[i] = split_bf16(v[2 * i], v[2 * i + 1]);
+            } else {
+                u[i] = round_bf16(v[2 * i], v[2 * i + 1]);
+                v[2 * i] -= __uint_as_float(u[i] << 16);
+                v[2 * i + 1] -= __uint_as_float(u[i] & 0xffff0000u);
+            }
+        }
+        tc_st16(addr + n * step, u);
+    }
+}
+
+// What the first two of three terms hold.
+__device__ __forceinline__ float upper_terms(float x)
+{
+    const float h = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+    return h + __uint_as_float(__float_as_uint(x - h) & 0xffff0000u);
+}
+
+// S's (dS's) terms: half a row's lie side by side, three of SC columns.
+template <int HS, int SC>
+__device__ __forceinline__ void put_state(uint32_t addr, const float (&S)[HS])
+{
+#pragma unroll
+    for (int i = 0; i < HS; i += 32) {
+        float x[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) x[e] = S[i + e];
+        put_terms<3>(addr + i / 2, SC, x);
     }
 }
 
 // All products of order up to ORD of an operand of NA terms in tensor memory with NB
 // planes in shared memory, small ones first: they add up before the large ones
-// truncate the accumulator at their own size. `a(x, k)` is the address of term x of
-// summed slice k, `b(y, k)` the descriptor of plane y's.
-template <int NA, int NB, int ORD, int KS, typename FA, typename FB>
-__device__ __forceinline__ void tc_product(uint32_t d, uint32_t idesc, bool add, FA a, FB b)
+// truncate the accumulator at their own size. mma(x, y, k, add) issues slice k (from
+// FIRST on, cyclically) of term x with plane y.
+template <int NA, int NB, int ORD, int KS, int FIRST, typename F>
+__device__ __forceinline__ void tc_product(bool add, F mma)
 {
+    // unrolled, constants and all: a product issues in its 32 cycles or less; rolled it took 70
 #pragma unroll
     for (int o = ORD; o >= 0; --o)
+#pragma unroll(NB == 1 ? 1 : 1)
+        for (int y = o < NA ? 0 : o - NA + 1; y <= o && y < NB; ++y) {
 #pragma unroll
-        for (int y = 0; y < NB; ++y) {
-            const int x = o - y;
-            if (x >= 0 && x < NA) {
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    tc_mma(d, a(x, k), b(y, k), idesc, add);
-                    add = true;
-                }
+            for (int k = 0; k < KS; ++k) {
+                mma(o - y, y, (k + FIRST) % KS, add);
+                add = true;
             }
         }
 }
 
+// Two values `pitch` elements apart: one conversion for both.
+__device__ __forceinline__ void store_two(float* p, int pitch, float x, float y)
+{
+    p[0] = x;
+    p[pitch] = y;
+}
+__device__ __forceinline__ void store_two(__nv_bfloat16* p, int pitch, float x, float y)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    p[0] = __low2bfloat16(h);
+    p[pitch] = __high2bfloat16(h);
+}
+
 // What a walk's CTA keeps in shared memory besides the stages.
 struct WalkShared {
-    unsigned long long mbar[4];
+    unsigned long long full[2], empty[2], done[5];
     uint32_t tmem;
     int dead;
-    int rows[3][DL_C];  // token rows of chunk c in slot c mod 3: the chunk that leaves, the present one, the next
+    int rows[3][DL_C];  // token rows of chunk c in slot c mod 3
 };
+
+struct WalkBars {
+    uint32_t full, empty, done;  // shared addresses; 8 bytes apart
+    __device__ __forceinline__ explicit WalkBars(WalkShared* w)
+    {
+        full = static_cast<uint32_t>(__cvta_generic_to_shared(w->full));
+        empty = static_cast<uint32_t>(__cvta_generic_to_shared(w->empty));
+        done = static_cast<uint32_t>(__cvta_generic_to_shared(w->done));
+    }
+};
+
+// Tensor memory and barriers of a walk; all threads.
+__device__ __forceinline__ uint32_t walk_begin(WalkShared* w, const WalkBars& bar)
+{
+    if (threadIdx.x < 32) tc_alloc(static_cast<uint32_t>(__cvta_generic_to_shared(&w->tmem)));
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar.full + 8 * i, DW_HELP);  // the copying threads, each with the bytes of its bulk copies
+            mbar_init(bar.empty + 8 * i, DW_COMPUTE);
+        }
+        for (int i = 0; i < 5; ++i) mbar_init(bar.done + 8 * i, 1);
+        w->dead = 0;
+        mbar_fence_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    return w->tmem;
+}
+
+__device__ __forceinline__ void walk_end(WalkShared* w, uint32_t tm, int* status)
+{
+    tc_wait_st();
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && status && w->dead) atomicOr(status, DEV_STATUS_TIMEOUT);
+    if (threadIdx.x < 32) tc_free(tm);
+}
+
+// The copying warps' part: chunk n of `chunks` into stage n mod STAGES, after `out` has taken
+// what the stage's last chunk left in it. `in` returns the bytes of its thread's bulk copies.
+template <int STAGES, typename ROWS, typename IN, typename OUT>
+__device__ __forceinline__ void walk_copy(WalkShared* w, const WalkBars& bar, int chunks, int tid, ROWS row_of, IN in, OUT out)
+{
+    for (int n = 0; n < chunks + STAGES; ++n) {
+        const int st = STAGES == 2 ? n & 1 : 0, before = n - STAGES;
+        if (before >= 0 && before < chunks) {
+            mbar_wait(bar.empty + 8 * st, (before / STAGES) & 1, &w->dead);
+            out(st, w->rows[before % 3]);
+        }
+        if (n < chunks) {
+            if (tid < DL_C) w->rows[n % 3][tid] = row_of(n, tid);
+            bar_sync(7, DW_HELP);  // rows are in, and all have taken what they copy out of the stage
+            const uint32_t bytes = in(n, st, w->rows[n % 3]);
+            cp_async_commit();
+            cp_async_wait<0>();
+            tc_fence_smem();
+            mbar_expect(bar.full + 8 * st, bytes);
+        }
+    }
+}
+
+__device__ __forceinline__ void walk_ready(int id)  // this thread's part of an operand is in tensor memory
+{
+    tc_wait_st();
+    tc_fence_before();
+    bar_arrive(id, DW_COMPUTE + 32);
+}
 
 template <typename T, int DKP, bool SAVE>
 __global__ void __launch_bounds__(DW_THREADS, 1) delta_scan_kernel(const DeltaParams p)
 {
     using Sh = WalkShape<T, DKP>;
-    constexpr int NP = Sh::NP, PP = Sh::PP, HS = DKP / 2, KT = DKP / 16;
+    constexpr int NP = Sh::NP, PP = Sh::PP, HS = DKP / 2, KT = DKP / 16, STAGES = Sh::STAGES;
     // tensor-memory columns
     constexpr int cS = 0, cKS = cS + 6 * Sh::SC, cQS = cKS + 64, cX = cQS + 64, cO = cX + 96;
     constexpr int cDS = DKP == 128 ? cS : cO + 64;
@@ -644,237 +841,220 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_scan_kernel(const DeltaPa
     WalkShared* ws = reinterpret_cast<WalkShared*>(smem);
     unsigned char* stages = smem + 1024;
     constexpr int STAGE = Sh::stage(PP);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = warp >> 2;
-    const int head = blockIdx.y, b = blockIdx.z, hk = head / p.group;
-    const int slice = blockIdx.x * 128, row = (warp & 3) * 32 + lane, vc = slice + row;  // this thread's value channel
-    const bool live = vc < p.dv;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int head = blockIdx.y, b = blockIdx.z;
+    const int slice = blockIdx.x * 128;
     const DeltaSeq s = delta_seq(p, b);
     const int chunks = (s.len + DL_C - 1) / DL_C;
-    const long long img = delta_img(p, b);
-    const T* q = reinterpret_cast<const T*>(p.q) + img * p.q_img + (long long)hk * p.dk;
-    const T* k = reinterpret_cast<const T*>(p.k) + img * p.k_img + (long long)hk * p.dk;
-    const T* v = reinterpret_cast<const T*>(p.v) + img * p.v_img + (long long)head * p.dv + slice;
-    T* y = reinterpret_cast<T*>(p.y) + img * p.y_img + (long long)head * p.dv + slice;
-    const int dvs = min(128, p.dv - slice);
     const size_t sbase = ((size_t)b * p.heads_v + head) * p.dk * p.dv;
+    const WalkBars bar(ws);
+    const uint32_t tm = walk_begin(ws, bar);
 
-    float S[HS];  // S^T[row][half * HS + i]
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(DW_REGS_HELP));
+        if (warp == 8) {
+            auto aS = [&](int x, int ks) { return tm + cS + (ks / (KT / 2)) * 3 * Sh::SC + x * Sh::SC + (ks % (KT / 2)) * 8; };
+            auto aX = [&](int x, int ks) { return tm + cX + (ks >> 1) * 48 + x * 16 + (ks & 1) * 8; };
+            // W's terms for O lie over W itself and QS, each half of a row over the columns that its own thread has read
+            auto aW = [&](int x, int ks) { return tm + (x < 2 ? cKS + x * 16 : cQS) + (ks >> 1) * 32 + (ks & 1) * 8; };
+            for (int c = 0; c < chunks; ++c) {
+                const int st = STAGES == 2 ? c & 1 : 0;
+                const uint32_t par = c & 1;
+                const uint32_t bK = static_cast<uint32_t>(__cvta_generic_to_shared(stages + st * STAGE));
+                const uint64_t dK = tc_desc(bK), dQ = tc_desc(bK + Sh::oQ), dT = tc_desc(bK + Sh::oT), dP = tc_desc(bK + Sh::oP);
+                mbar_wait(bar.full + 8 * st, (c / STAGES) & 1, &ws->dead);
+                bar_sync(1, DW_COMPUTE + 32);
+                tc_fence_after();
+                if (tc_elect()) {  // 1
+                    auto rows_of = [&](uint32_t d, uint64_t t) {
+                        return [=](int x, int y, int ks, bool add) {
+                            tc_mma(tm + d, aS(x, ks), t + (y * Sh::plane + (ks >> 2) * TC_TILE + (ks & 3) * 32) / 16,
+                                   tc_idesc(64, false), add);
+                        };
+                    };
+                    tc_product<3, NP, 2, KT, 0>(false, rows_of(cKS, dK));
+                    tc_commit(bar.done);
+                    if (!SAVE) {
+                        tc_product<3, NP, 2, KT, 0>(false, rows_of(cQS, dQ));
+                        tc_commit(bar.done + 8);
+                    }
+                }
+                __syncwarp();
+                bar_sync(2, DW_COMPUTE + 32);
+                tc_fence_after();
+                if (tc_elect()) {  // 2
+                    tc_product<3, 3, 2, 4, 0>(false, [&](int x, int y, int ks, bool add) {
+                        tc_mma(tm + cKS + 16 * ks, aX(x, ks), dT + (y * TC_TILE + ks * (2048 + 32)) / 16,
+                               tc_idesc(64 - 16 * ks, false), add);
+                    });
+                    tc_commit(bar.done + 16);
+                }
+                __syncwarp();
+                bar_sync(3, DW_COMPUTE + 32);
+                tc_fence_after();
+                if (tc_elect()) {  // 3
 #pragma unroll
-    for (int i = 0; i < HS; ++i) {
-        const int kc = half * HS + i;
-        S[i] = p.s_in && live && kc < p.dk ? p.s_in[sbase + (size_t)kc * p.dv + vc] : 0.f;
-    }
-    if (chunks == 0) {
+                    for (int nb = 0; nb < Sh::KB; ++nb)
+                        tc_product<3, NP, 2, 4, 0>(false, [&](int x, int y, int ks, bool add) {
+                            tc_mma(tm + cDS + nb * (3 * Sh::SC), aX(x, ks),
+                                   dK + (y * Sh::plane + nb * TC_TILE + ks * 2048) / 16, tc_idesc(64, true), add);
+                        });
+                    tc_commit(bar.done + 24);
+                }
+                __syncwarp();
+                if (!SAVE) {
+                    bar_sync(4, DW_COMPUTE + 32);
+                    tc_fence_after();
+                    if (tc_elect()) {
+                        tc_product<PP, PP, PP - 1, 4, 0>(false, [&](int x, int y, int ks, bool add) {
+                            tc_mma(tm + cO + 16 * ks, aW(x, ks), dP + (y * TC_TILE + ks * (2048 + 32)) / 16,
+                                   tc_idesc(64 - 16 * ks, false), add);
+                        });
+                        tc_commit(bar.done + 32);
+                    }
+                    __syncwarp();
+                    // the next KS lies over W's terms: O has read them
+                    mbar_wait(bar.done + 32, par, &ws->dead);
+                }
+            }
+        } else {
+            const int ht = tid - 288, hk = head / p.group;
+            const long long img = delta_img(p, b);
+            const T* q = reinterpret_cast<const T*>(p.q) + img * p.q_img + (long long)hk * p.dk;
+            const T* k = reinterpret_cast<const T*>(p.k) + img * p.k_img + (long long)hk * p.dk;
+            const T* v = reinterpret_cast<const T*>(p.v) + img * p.v_img + (long long)head * p.dv + slice;
+            T* y = reinterpret_cast<T*>(p.y) + img * p.y_img + (long long)head * p.dv + slice;
+            const int dvs = min(128, p.dv - slice);
+            walk_copy<STAGES>(
+                ws, bar, chunks, ht, [&](int c, int r) { return delta_row(p, s, c * DL_C + r); },
+                [&](int c, int st, const int* rows) {
+                    unsigned char* base = stages + st * STAGE;
+                    const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(base)), full = bar.full + 8 * st;
+                    const size_t rec = (size_t)(s.slot + c) * p.heads_v + head;
+                    walk_load<DKP>(base, k, p.k_tok, rows, p.dk, ht);
+                    if (!SAVE) walk_load<DKP>(base + Sh::oQ, q, p.q_tok, rows, p.dk, ht);
+                    walk_load_values(reinterpret_cast<T*>(base + Sh::oV(PP)), Sh::vpitch, v, p.v_tok, rows, dvs, ht);
+                    uint32_t bytes = 0;
+                    if (ht == 0) {
+                        bytes = DL_VECS * 4 + (3 + (SAVE ? 0 : PP)) * TC_TILE;
+                        bulk_in(at + Sh::oVec, record_vec(p, rec), bytes, full);
+                    }
+                    return bytes;
+                },
+                [&](int st, const int* rows) {
+                    if (!SAVE)
+                        walk_store_values(y, p.y_tok, reinterpret_cast<const T*>(stages + st * STAGE + Sh::oV(PP)), Sh::vpitch, rows,
+                                          dvs, ht);
+                });
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(DW_REGS_COMPUTE));
+        const int half = warp >> 2, row = (warp & 3) * 32 + lane, vc = slice + row;  // this thread's value channel
+        const bool live = vc < p.dv;
+        const uint32_t tl = tm + ((uint32_t)(warp & 3) << 21);  // this warp's 32 rows
+        float S[HS];  // S^T[row][half * HS + i]
+#pragma unroll
+        for (int i = 0; i < HS; ++i) {
+            const int kc = half * HS + i;
+            S[i] = p.s_in && live && kc < p.dk ? p.s_in[sbase + (size_t)kc * p.dv + vc] : 0.f;
+        }
+        if (chunks > 0) {
+            put_state<HS, Sh::SC>(tl + cS + half * 3 * Sh::SC, S);
+            walk_ready(1);
+        }
+        for (int c = 0; c < chunks; ++c) {
+            const int st = STAGES == 2 ? c & 1 : 0;
+            const uint32_t par = c & 1;
+            T* vd = reinterpret_cast<T*>(stages + st * STAGE + Sh::oV(PP)) + half * 32 * Sh::vpitch + row;
+            const float* vec = reinterpret_cast<const float*>(stages + st * STAGE + Sh::oVec) + half * 32;
+            const size_t rec = (size_t)(s.slot + c) * p.heads_v + head;
+            if (SAVE && live) {  // the state entering the chunk, for the gradients
+                float* o = p.wS + rec * p.dv * DKP + vc;
+#pragma unroll
+                for (int i = 0; i < HS; ++i) o[(size_t)(half * HS + i) * p.dv] = S[i];
+            }
+            float x[32], o[SAVE ? 1 : 32];
+            mbar_wait(bar.full + 8 * st, (c / STAGES) & 1, &ws->dead);
+            {
+                float u[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) u[i] = to_float(vd[i * Sh::vpitch]);
+                mbar_wait(bar.done, par, &ws->dead);
+                tc_fence_after();
+                tc_ld32(tl + cKS + half * 32, x);
+                tc_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = vec[2 * DL_C + i] * (u[i] - vec[i] * x[i]);  // X^T = beta (V - e^G K S)^T
+            }
+            put_terms<3>(tl + cX + half * 48, 16, x);
+            walk_ready(2);
+            if constexpr (!SAVE) {
+                mbar_wait(bar.done + 8, par, &ws->dead);
+                tc_fence_after();
+                tc_ld32(tl + cQS + half * 32, o);
+                tc_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] *= p.scale * vec[i];
+            }
+            mbar_wait(bar.done + 16, par, &ws->dead);
+            tc_fence_after();
+            tc_ld32(tl + cKS + half * 32, x);
+            tc_wait_ld();
+            {
+                float w[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) w[i] = x[i] * vec[DL_C + i];
+                put_terms<3>(tl + cX + half * 48, 16, w);
+                walk_ready(3);
+            }
+            if constexpr (SAVE) {
+                if (live) {
+                    float* ow = p.wW + (rec * DL_C + half * 32) * p.dv + vc;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) ow[(size_t)i * p.dv] = x[i];
+                }
+            } else {
+                if constexpr (PP == 2) {
+                    put_terms<2>(tl + cKS + half * 32, 16, x);
+                } else {  // the third term lies apart
+                    float w[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) w[i] = x[i] - upper_terms(x[i]);
+                    put_terms<1>(tl + cQS + half * 32, 16, w);
+                    put_terms<2, true>(tl + cKS + half * 32, 16, x);
+                }
+                walk_ready(4);
+            }
+            const float eC = vec[3 * DL_C - half * 32];
+            mbar_wait(bar.done + 24, par, &ws->dead);
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < HS; i += 32) {
+                tc_ld32(tl + cDS + (DKP == 128 ? half * 3 * Sh::SC : half * 32) + i, x);
+                tc_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) S[i + e] = eC * S[i + e] + x[e];
+            }
+            if (c + 1 < chunks) {
+                put_state<HS, Sh::SC>(tl + cS + half * 3 * Sh::SC, S);
+                walk_ready(1);
+            }
+            if constexpr (!SAVE) {
+                mbar_wait(bar.done + 32, par, &ws->dead);
+                tc_fence_after();
+                tc_ld32(tl + cO + half * 32, x);
+                tc_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) store_two(vd + i * Sh::vpitch, Sh::vpitch, o[i] + x[i], o[i + 1] + x[i + 1]);
+            }
+            mbar_arrive(bar.empty + 8 * st);
+        }
         if (p.s_out && live)
 #pragma unroll
             for (int i = 0; i < HS; ++i)
                 if (half * HS + i < p.dk) p.s_out[sbase + (size_t)(half * HS + i) * p.dv + vc] = S[i];
-        return;
     }
-
-    uint32_t mbar[3];
-#pragma unroll
-    for (int i = 0; i < 3; ++i) mbar[i] = static_cast<uint32_t>(__cvta_generic_to_shared(&ws->mbar[i]));
-    if (warp == 0) tc_alloc(static_cast<uint32_t>(__cvta_generic_to_shared(&ws->tmem)));
-    if (tid == 0) {
-        for (int i = 0; i < 3; ++i) mbar_init(mbar[i], 1);
-        ws->dead = 0;
-    }
-    auto rows_of = [&](int c) {
-        if (tid < DL_C) ws->rows[c % 3][tid] = delta_row(p, s, c * DL_C + tid);
-    };
-    auto issue = [&](int c, int st) {
-        unsigned char* base = stages + st * STAGE;
-        const size_t rec = (size_t)(s.slot + c) * p.heads_v + head;
-        const int* rows = ws->rows[c % 3];
-        walk_load<NP>(base, Sh::plane, k, p.k_tok, rows, DKP, p.dk, tid);
-        if (!SAVE) walk_load<NP>(base + Sh::oQ, Sh::plane, q, p.q_tok, rows, DKP, p.dk, tid);
-        walk_load_planes(base + Sh::oT, p.wT + rec * 3 * DL_PLANE, 3, tid);
-        if (!SAVE) walk_load_planes(base + Sh::oP, p.wP + rec * p.tplanes * DL_PLANE, PP, tid);
-        constexpr int V = 16 / sizeof(T), vecs = 128 / V;
-        T* vd = reinterpret_cast<T*>(base + Sh::oV(PP));
-        for (int i = tid; i < DL_C * vecs; i += DW_THREADS) {
-            const int r = i / vecs, cc = (i - r * vecs) * V;
-            const bool ok = rows[r] >= 0 && cc < dvs;
-            cp_async16(vd + r * Sh::vpitch + cc, ok ? v + rows[r] * p.v_tok + cc : v, ok);
-        }
-        if (tid < DL_SCANVECS / 4)
-            cp_async16(base + Sh::oVec(PP) + 16 * tid, p.wvec + rec * DL_VECS + 4 * tid, true);
-    };
-    rows_of(0);
-    mbar_fence_init();
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tm = ws->tmem, tl = tm + ((uint32_t)(warp & 3) << 21);  // this warp's 32 rows
-    issue(0, 0);
-    cp_async_commit();
-
-    auto put_state = [&]() {  // S's terms as the left operand of the next chunk
-#pragma unroll
-        for (int i = 0; i < HS; i += 32) {
-            float x[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = S[i + e];
-#pragma unroll
-            for (int n = 0; n < 3; ++n) {
-                uint32_t u[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) u[e] = split_bf16(x[2 * e], x[2 * e + 1]);
-                tc_st16(tl + cS + half * 3 * Sh::SC + n * Sh::SC + i / 2, u);
-            }
-        }
-    };
-    auto aS = [&](int x, int ks) { return tm + cS + (ks / (KT / 2)) * 3 * Sh::SC + x * Sh::SC + (ks % (KT / 2)) * 8; };
-    auto aX = [&](int x, int ks) { return tm + cX + (ks >> 1) * 48 + x * 16 + (ks & 1) * 8; };
-    // W's terms for O lie over W itself and QS, each half of a row over the columns that its own thread has read
-    auto aWO = [&](int x, int ks) { return tm + (x < 2 ? cKS + x * 16 : cQS) + (ks >> 1) * 32 + (ks & 1) * 8; };
-    auto put_out = [&](int c, int st) {  // y of chunk c, staged in V's place, to whole rows
-        constexpr int V = 16 / sizeof(T), vecs = 128 / V;
-        const T* vd = reinterpret_cast<const T*>(stages + st * STAGE + Sh::oV(PP));
-        for (int i = tid; i < DL_C * vecs; i += DW_THREADS) {
-            const int r = i / vecs, cc = (i - r * vecs) * V;
-            const int at = ws->rows[c % 3][r];
-            if (at >= 0 && cc < dvs)
-                *reinterpret_cast<uint4*>(y + at * p.y_tok + cc) = *reinterpret_cast<const uint4*>(vd + r * Sh::vpitch + cc);
-        }
-    };
-
-    put_state();
-    for (int c = 0; c < chunks; ++c) {
-        const int st = Sh::STAGES == 2 ? c & 1 : 0;
-        const uint32_t par = c & 1;
-        unsigned char* base = stages + st * STAGE;
-        const uint32_t bK = static_cast<uint32_t>(__cvta_generic_to_shared(base)), bQ = bK + Sh::oQ, bT = bK + Sh::oT, bP = bK + Sh::oP;
-        T* vd = reinterpret_cast<T*>(base + Sh::oV(PP));
-        const float* vec = reinterpret_cast<const float*>(base + Sh::oVec(PP));
-        const size_t rec = (size_t)(s.slot + c) * p.heads_v + head;
-        if (Sh::STAGES == 1 && c > 0) {
-            // one stage: y leaves it, then it is filled again
-            __syncthreads();
-            if (!SAVE) put_out(c - 1, 0);
-            __syncthreads();
-            issue(c, 0);
-            cp_async_commit();
-        }
-        cp_async_wait<0>();
-        tc_fence_smem();
-        tc_wait_st();
-        tc_fence_before();
-        __syncthreads();
-        if (tid == 0) {  // 1: K S and Q S
-            tc_fence_after();
-            auto k_major = [&](uint32_t t) {
-                return [t](int n, int ks) { return tc_desc(t + n * Sh::plane + (ks >> 2) * TC_TILE + (ks & 3) * 32); };
-            };
-            tc_product<3, NP, 2, KT>(tm + cKS, tc_idesc(64, false), false, aS, k_major(bK));
-            // a bf16 y: two terms of the state (2^-17) are far below its rounding
-            if (!SAVE) tc_product<3, NP, NP == 1 ? 1 : 2, KT>(tm + cQS, tc_idesc(64, false), false, aS, k_major(bQ));
-            tc_commit(mbar[0]);
-        }
-        if (!SAVE && Sh::STAGES == 2 && c > 0) put_out(c - 1, st ^ 1);
-        if (c + 1 < chunks) rows_of(c + 1);
-        if (SAVE && live) {  // the state entering the chunk, for the gradients
-            float* o = p.wS + rec * p.dv * DKP + vc;
-#pragma unroll
-            for (int i = 0; i < HS; ++i) o[(size_t)(half * HS + i) * p.dv] = S[i];
-        }
-        float x[32];
-        mbar_wait(mbar[0], par, &ws->dead);
-        tc_fence_after();
-        tc_ld32(tl + cKS + half * 32, x);
-        tc_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {  // X^T = beta (V - e^G K S)^T
-            const int r = half * 32 + i;
-            x[i] = vec[2 * DL_C + r] * (to_float(vd[r * Sh::vpitch + row]) - vec[r] * x[i]);
-        }
-        put_terms<3>(tl + cX + half * 48, x);
-        tc_wait_st();
-        tc_fence_before();
-        __syncthreads();
-        if (tid == 0) {  // 2: W
-            tc_fence_after();
-            tc_product<3, 3, 2, 4>(tm + cKS, tc_idesc(64, false), false, aX,
-                                   [bT](int n, int ks) { return tc_desc(bT + n * TC_TILE + ks * 32); });
-            tc_commit(mbar[1]);
-        }
-        // the next chunk's copies go where the last one was: its y has left before the barrier
-        if (Sh::STAGES == 2) {
-            if (c + 1 < chunks) issue(c + 1, st ^ 1);
-            cp_async_commit();
-        }
-        float o[32];
-        if (!SAVE) {
-            tc_ld32(tl + cQS + half * 32, o);
-            tc_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= p.scale * vec[half * 32 + i];
-        }
-        mbar_wait(mbar[1], par, &ws->dead);
-        tc_fence_after();
-        tc_ld32(tl + cKS + half * 32, x);
-        tc_wait_ld();
-        if (SAVE) {
-            if (live) {
-                float* ow = p.wW + rec * DL_C * p.dv + vc;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) ow[(size_t)(half * 32 + i) * p.dv] = x[i];
-            }
-        } else {
-            float w[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] = x[i];
-            put_terms<2>(tl + cKS + half * 32, w);
-            if (PP == 3) put_terms<1>(tl + cQS + half * 32, w);
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] *= vec[DL_C + half * 32 + i];
-        put_terms<3>(tl + cX + half * 48, x);
-        tc_wait_st();
-        tc_fence_before();
-        __syncthreads();
-        if (tid == 0) {  // 3: the change of the state, and O
-            tc_fence_after();
-#pragma unroll
-            for (int nb = 0; nb < Sh::KB; ++nb)
-                tc_product<3, NP, 2, 4>(tm + cDS + nb * (3 * Sh::SC), tc_idesc(64, true), false, aX, [bK, nb](int n, int ks) {
-                    return tc_desc(bK + n * Sh::plane + nb * TC_TILE + ks * 2048);
-                });
-            if (!SAVE)
-                tc_product<PP, PP, PP - 1, 4>(tm + cO, tc_idesc(64, false), false, aWO,
-                                              [bP](int n, int ks) { return tc_desc(bP + n * TC_TILE + ks * 32); });
-            tc_commit(mbar[2]);
-        }
-        const float eC = vec[3 * DL_C];
-        mbar_wait(mbar[2], par, &ws->dead);
-        tc_fence_after();
-#pragma unroll
-        for (int i = 0; i < HS; i += 32) {
-            tc_ld32(tl + cDS + (DKP == 128 ? half * 3 * Sh::SC : half * 32) + i, x);
-            tc_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) S[i + e] = eC * S[i + e] + x[e];
-        }
-        put_state();
-        if (!SAVE) {
-            tc_ld32(tl + cO + half * 32, x);
-            tc_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) store_elem(vd + (half * 32 + i) * Sh::vpitch + row, o[i] + x[i]);
-        }
-    }
-    tc_wait_st();
-    cp_async_wait<0>();
-    tc_fence_before();
-    __syncthreads();
-    if (!SAVE) put_out(chunks - 1, Sh::STAGES == 2 ? (chunks - 1) & 1 : 0);
-    if (p.s_out && live)
-#pragma unroll
-        for (int i = 0; i < HS; ++i)
-            if (half * HS + i < p.dk) p.s_out[sbase + (size_t)(half * HS + i) * p.dv + vc] = S[i];
-    if (p.status && tid == 0 && ws->dead) atomicOr(p.status, DEV_STATUS_TIMEOUT);
-    if (warp == 0) tc_free(tm);
+    walk_end(ws, tm, p.status);
 }
 
 // ---- one token ----------------------------------------------------------------------

@@ -42,7 +42,7 @@ template <typename T, int DKP>
 __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaParams p)
 {
     using Sh = WalkShape<T, DKP>;
-    constexpr int NP = Sh::NP, HS = DKP / 2, KT = DKP / 16, STAGE = Sh::stage(3);
+    constexpr int NP = Sh::NP, HS = DKP / 2, KT = DKP / 16, STAGE = Sh::stage(3), STAGES = Sh::STAGES;
     constexpr int cS = 0, c1 = cS + 6 * Sh::SC, c2 = c1 + 64, cA = c2 + 64, cW = cA + NP * 32;
     constexpr int cDS = DKP == 128 ? cS : cW + 96;
     static_assert(cW + (DKP == 128 ? 96 : 160) <= 512, "tensor memory");
@@ -50,231 +50,195 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaP
     unsigned char* smem = smem_raw + (1024 - (__cvta_generic_to_shared(smem_raw) & 1023)) % 1024;
     WalkShared* ws = reinterpret_cast<WalkShared*>(smem);
     unsigned char* stages = smem + 1024;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = warp >> 2;
-    const int head = blockIdx.y, b = blockIdx.z, hk = head / p.group;
-    const int slice = blockIdx.x * 128, row = (warp & 3) * 32 + lane, vc = slice + row;
-    const bool live = vc < p.dv;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int head = blockIdx.y, b = blockIdx.z;
+    const int slice = blockIdx.x * 128;
     const DeltaSeq s = delta_seq(p, b);
     const int chunks = (s.len + DL_C - 1) / DL_C;
-    const long long img = delta_img(p, b);
-    const T* q = reinterpret_cast<const T*>(p.q) + img * p.q_img + (long long)hk * p.dk;
-    const T* k = reinterpret_cast<const T*>(p.k) + img * p.k_img + (long long)hk * p.dk;
-    const T* dy = reinterpret_cast<const T*>(p.dy) + img * p.y_img + (long long)head * p.dv + slice;
-    T* dvalue = reinterpret_cast<T*>(p.dvalue);
-    if (dvalue) dvalue += (img * p.tokens * p.heads_v + head) * (long long)p.dv + slice;
-    const int dvs = min(128, p.dv - slice);
     const size_t sbase = ((size_t)b * p.heads_v + head) * p.dk * p.dv;
+    const WalkBars bar(ws);
+    const uint32_t tm = walk_begin(ws, bar);
+    // n counts the chunks in the order of the walk, from the last to the first
 
-    float S[HS];  // dS^T[row][half * HS + i]
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(DW_REGS_HELP));
+        if (warp == 8) {
+            auto aS = [&](int x, int ks) { return tm + cS + (ks / (KT / 2)) * 3 * Sh::SC + x * Sh::SC + (ks % (KT / 2)) * 8; };
+            auto aO = [&](int x, int ks) { return tm + cA + (ks >> 1) * (NP * 16) + x * 16 + (ks & 1) * 8; };
+            auto aQ = [&](int x, int ks) { return tm + c2 + (ks >> 1) * 48 + x * 16 + (ks & 1) * 8; };
+            auto aW = [&](int x, int ks) { return tm + cW + (ks >> 1) * 48 + x * 16 + (ks & 1) * 8; };
+            for (int n = 0; n < chunks; ++n) {
+                const int st = STAGES == 2 ? n & 1 : 0;
+                const uint32_t bK = static_cast<uint32_t>(__cvta_generic_to_shared(stages + st * STAGE));
+                const uint64_t dK = tc_desc(bK), dQ = tc_desc(bK + Sh::oQ), dT = tc_desc(bK + Sh::oT), dP = tc_desc(bK + Sh::oP);
+                mbar_wait(bar.full + 8 * st, (n / STAGES) & 1, &ws->dead);
+                bar_sync(1, DW_COMPUTE + 32);
+                tc_fence_after();
+                if (tc_elect())  // 1
+                    tc_product<3, NP, 2, KT, 0>(false, [&](int x, int y, int ks, bool add) {
+                        tc_mma(tm + c1, aS(x, ks), dK + (y * Sh::plane + (ks >> 2) * TC_TILE + (ks & 3) * 32) / 16,
+                               tc_idesc(64, false), add);
+                    });
+                __syncwarp();
+                bar_sync(2, DW_COMPUTE + 32);
+                tc_fence_after();
+                if (tc_elect()) {  // slice ks of the rows i reaches the columns j up to 16 ks + 15: the last one covers all
+                    tc_product<NP, 3, 2, 4, 3>(false, [&](int x, int y, int ks, bool add) {
+                        tc_mma(tm + c2, aO(x, ks), dP + (y * TC_TILE + ks * 2048) / 16, tc_idesc(16 * ks + 16, true), add);
+                    });
+                    tc_commit(bar.done);
+                }
+                __syncwarp();
+                bar_sync(3, DW_COMPUTE + 32);
+                tc_fence_after();
+                if (tc_elect()) {  // 2
+                    tc_product<3, 3, 2, 4, 3>(false, [&](int x, int y, int ks, bool add) {
+                        tc_mma(tm + c1, aW(x, ks), dT + (y * TC_TILE + ks * 2048) / 16, tc_idesc(16 * ks + 16, true), add);
+                    });
+                    tc_commit(bar.done + 8);
+                }
+                __syncwarp();
+                auto state = [&](auto a, uint64_t t, bool more) {
 #pragma unroll
-    for (int i = 0; i < HS; ++i) {
-        const int kc = half * HS + i;
-        S[i] = p.ds_in && live && kc < p.dk ? p.ds_in[sbase + (size_t)kc * p.dv + vc] : 0.f;
-    }
-    if (chunks == 0) {
+                    for (int nb = 0; nb < Sh::KB; ++nb)
+                        tc_product<3, NP, 2, 4, 0>(more, [&](int x, int y, int ks, bool add) {
+                            tc_mma(tm + cDS + nb * (3 * Sh::SC), a(x, ks),
+                                   t + (y * Sh::plane + nb * TC_TILE + ks * 2048) / 16, tc_idesc(64, true), add);
+                        });
+                };
+                bar_sync(4, DW_COMPUTE + 32);
+                tc_fence_after();
+                if (tc_elect()) state(aQ, dQ, false);  // 3
+                __syncwarp();
+                bar_sync(5, DW_COMPUTE + 32);
+                tc_fence_after();
+                if (tc_elect()) {
+                    state(aW, dK, true);
+                    tc_commit(bar.done + 16);
+                }
+                __syncwarp();
+            }
+        } else {
+            const int ht = tid - 288, hk = head / p.group;
+            const long long img = delta_img(p, b);
+            const T* q = reinterpret_cast<const T*>(p.q) + img * p.q_img + (long long)hk * p.dk;
+            const T* k = reinterpret_cast<const T*>(p.k) + img * p.k_img + (long long)hk * p.dk;
+            const T* dy = reinterpret_cast<const T*>(p.dy) + img * p.y_img + (long long)head * p.dv + slice;
+            T* dvalue = reinterpret_cast<T*>(p.dvalue);
+            if (dvalue) dvalue += (img * p.tokens * p.heads_v + head) * (long long)p.dv + slice;
+            const int dvs = min(128, p.dv - slice);
+            walk_copy<STAGES>(
+                ws, bar, chunks, ht, [&](int n, int r) { return delta_row(p, s, (chunks - 1 - n) * DL_C + r); },
+                [&](int n, int st, const int* rows) {
+                    unsigned char* base = stages + st * STAGE;
+                    const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(base)), full = bar.full + 8 * st;
+                    const size_t rec = (size_t)(s.slot + chunks - 1 - n) * p.heads_v + head;
+                    walk_load<DKP>(base, k, p.k_tok, rows, p.dk, ht);
+                    walk_load<DKP>(base + Sh::oQ, q, p.q_tok, rows, p.dk, ht);
+                    walk_load_values(reinterpret_cast<T*>(base + Sh::oV(3)), Sh::vpitch, dy, p.y_tok, rows, dvs, ht);
+                    uint32_t bytes = 0;
+                    if (ht == 0) {
+                        bytes = DL_VECS * 4 + 6 * TC_TILE;
+                        bulk_in(at + Sh::oVec, record_vec(p, rec), bytes, full);
+                    }
+                    return bytes;
+                },
+                [&](int st, const int* rows) {  // dV, left in dO's place
+                    if (dvalue)
+                        walk_store_values(dvalue, (long long)p.heads_v * p.dv,
+                                          reinterpret_cast<const T*>(stages + st * STAGE + Sh::oV(3)), Sh::vpitch, rows, dvs, ht);
+                });
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(DW_REGS_COMPUTE));
+        const int half = warp >> 2, row = (warp & 3) * 32 + lane, vc = slice + row;
+        const bool live = vc < p.dv;
+        const uint32_t tl = tm + ((uint32_t)(warp & 3) << 21);
+        float S[HS];  // dS^T[row][half * HS + i]
+#pragma unroll
+        for (int i = 0; i < HS; ++i) {
+            const int kc = half * HS + i;
+            S[i] = p.ds_in && live && kc < p.dk ? p.ds_in[sbase + (size_t)kc * p.dv + vc] : 0.f;
+        }
+        if (chunks > 0) {
+            put_state<HS, Sh::SC>(tl + cS + half * 3 * Sh::SC, S);
+            walk_ready(1);
+        }
+        for (int n = 0; n < chunks; ++n) {
+            const int st = STAGES == 2 ? n & 1 : 0;
+            const uint32_t par = n & 1;
+            T* vd = reinterpret_cast<T*>(stages + st * STAGE + Sh::oV(3)) + half * 32 * Sh::vpitch + row;
+            const float* vec = reinterpret_cast<const float*>(stages + st * STAGE + Sh::oVec) + half * 32;
+            const size_t rec = (size_t)(s.slot + chunks - 1 - n) * p.heads_v + head;
+            float o[32], x[32];
+            mbar_wait(bar.full + 8 * st, (n / STAGES) & 1, &ws->dead);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = o[i] = to_float(vd[i * Sh::vpitch]);
+            put_terms<NP>(tl + cA + half * (NP * 16), 16, x);
+            walk_ready(2);
+            if (live) {  // the gradient of the state leaving the chunk
+                float* g = p.wdS + rec * p.dv * DKP + vc;
+#pragma unroll
+                for (int i = 0; i < HS; ++i) g[(size_t)(half * HS + i) * p.dv] = S[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= p.scale * vec[i];
+            mbar_wait(bar.done, par, &ws->dead);
+            tc_fence_after();
+            {
+                float z[32];
+                tc_ld32(tl + c1 + half * 32, x);
+                tc_ld32(tl + c2 + half * 32, z);
+                tc_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = vec[DL_C + i] * x[i] + z[i];
+            }
+            put_terms<3>(tl + cW + half * 48, 16, x);
+            walk_ready(3);
+            // over D2, which both halves of a row have to have read
+            mbar_wait(bar.done + 8, par, &ws->dead);
+            put_terms<3>(tl + c2 + half * 48, 16, o);
+            walk_ready(4);
+            tc_fence_after();
+            tc_ld32(tl + c1 + half * 32, x);
+            tc_wait_ld();
+            if (live) {
+                float* ox = p.wdX + (rec * DL_C + half * 32) * p.dv + vc;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) ox[(size_t)i * p.dv] = x[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                x[i] *= vec[2 * DL_C + i];  // dV
+                x[i + 1] *= vec[2 * DL_C + i + 1];
+                store_two(vd + i * Sh::vpitch, Sh::vpitch, x[i], x[i + 1]);
+                x[i] *= -vec[i];
+                x[i + 1] *= -vec[i + 1];
+            }
+            put_terms<3>(tl + cW + half * 48, 16, x);
+            walk_ready(5);
+            const float eC = vec[3 * DL_C - half * 32];
+            mbar_wait(bar.done + 16, par, &ws->dead);
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < HS; i += 32) {
+                tc_ld32(tl + cDS + (DKP == 128 ? half * 3 * Sh::SC : half * 32) + i, x);
+                tc_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) S[i + e] = eC * S[i + e] + x[e];
+            }
+            mbar_arrive(bar.empty + 8 * st);
+            if (n + 1 < chunks) {
+                put_state<HS, Sh::SC>(tl + cS + half * 3 * Sh::SC, S);
+                walk_ready(1);
+            }
+        }
         if (p.ds_out && live)
 #pragma unroll
             for (int i = 0; i < HS; ++i)
                 if (half * HS + i < p.dk) p.ds_out[sbase + (size_t)(half * HS + i) * p.dv + vc] = S[i];
-        return;
     }
-
-    uint32_t mbar[3];
-#pragma unroll
-    for (int i = 0; i < 3; ++i) mbar[i] = static_cast<uint32_t>(__cvta_generic_to_shared(&ws->mbar[i]));
-    if (warp == 0) tc_alloc(static_cast<uint32_t>(__cvta_generic_to_shared(&ws->tmem)));
-    if (tid == 0) {
-        for (int i = 0; i < 3; ++i) mbar_init(mbar[i], 1);
-        ws->dead = 0;
-    }
-    // n counts the chunks in the order of the walk, from the last to the first
-    auto rows_of = [&](int n) {
-        if (tid < DL_C) ws->rows[n % 3][tid] = delta_row(p, s, (chunks - 1 - n) * DL_C + tid);
-    };
-    auto issue = [&](int n, int st) {
-        unsigned char* base = stages + st * STAGE;
-        const size_t rec = (size_t)(s.slot + chunks - 1 - n) * p.heads_v + head;
-        const int* rows = ws->rows[n % 3];
-        walk_load<NP>(base, Sh::plane, k, p.k_tok, rows, DKP, p.dk, tid);
-        walk_load<NP>(base + Sh::oQ, Sh::plane, q, p.q_tok, rows, DKP, p.dk, tid);
-        walk_load_planes(base + Sh::oT, p.wT + rec * 3 * DL_PLANE, 3, tid);
-        walk_load_planes(base + Sh::oP, p.wP + rec * 3 * DL_PLANE, 3, tid);
-        constexpr int V = 16 / sizeof(T), vecs = 128 / V;
-        T* vd = reinterpret_cast<T*>(base + Sh::oV(3));
-        for (int i = tid; i < DL_C * vecs; i += DW_THREADS) {
-            const int r = i / vecs, cc = (i - r * vecs) * V;
-            const bool ok = rows[r] >= 0 && cc < dvs;
-            cp_async16(vd + r * Sh::vpitch + cc, ok ? dy + rows[r] * p.y_tok + cc : dy, ok);
-        }
-        if (tid < DL_SCANVECS / 4)
-            cp_async16(base + Sh::oVec(3) + 16 * tid, p.wvec + rec * DL_VECS + 4 * tid, true);
-    };
-    rows_of(0);
-    mbar_fence_init();
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tm = ws->tmem, tl = tm + ((uint32_t)(warp & 3) << 21);
-    issue(0, 0);
-    cp_async_commit();
-
-    auto put_state = [&]() {
-#pragma unroll
-        for (int i = 0; i < HS; i += 32) {
-            float x[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = S[i + e];
-#pragma unroll
-            for (int n = 0; n < 3; ++n) {
-                uint32_t u[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) u[e] = split_bf16(x[2 * e], x[2 * e + 1]);
-                tc_st16(tl + cS + half * 3 * Sh::SC + n * Sh::SC + i / 2, u);
-            }
-        }
-    };
-    auto aS = [&](int x, int ks) { return tm + cS + (ks / (KT / 2)) * 3 * Sh::SC + x * Sh::SC + (ks % (KT / 2)) * 8; };
-    auto aO = [&](int x, int ks) { return tm + cA + (ks >> 1) * (NP * 16) + x * 16 + (ks & 1) * 8; };
-    auto aQ = [&](int x, int ks) { return tm + c2 + (ks >> 1) * 48 + x * 16 + (ks & 1) * 8; };
-    auto aW = [&](int x, int ks) { return tm + cW + (ks >> 1) * 48 + x * 16 + (ks & 1) * 8; };
-    auto put_out = [&](int n, int st) {  // dV, staged in dO's place, to whole rows
-        if (!dvalue) return;
-        constexpr int V = 16 / sizeof(T), vecs = 128 / V;
-        const T* vd = reinterpret_cast<const T*>(stages + st * STAGE + Sh::oV(3));
-        for (int i = tid; i < DL_C * vecs; i += DW_THREADS) {
-            const int r = i / vecs, cc = (i - r * vecs) * V;
-            const int at = ws->rows[n % 3][r];
-            if (at >= 0 && cc < dvs)
-                *reinterpret_cast<uint4*>(dvalue + (long long)at * p.heads_v * p.dv + cc) =
-                    *reinterpret_cast<const uint4*>(vd + r * Sh::vpitch + cc);
-        }
-    };
-
-    put_state();
-    for (int n = 0; n < chunks; ++n) {
-        const int st = Sh::STAGES == 2 ? n & 1 : 0;
-        const uint32_t par = n & 1;
-        unsigned char* base = stages + st * STAGE;
-        const uint32_t bK = static_cast<uint32_t>(__cvta_generic_to_shared(base)), bQ = bK + Sh::oQ, bT = bK + Sh::oT, bP = bK + Sh::oP;
-        T* vd = reinterpret_cast<T*>(base + Sh::oV(3));
-        const float* vec = reinterpret_cast<const float*>(base + Sh::oVec(3));
-        const size_t rec = (size_t)(s.slot + chunks - 1 - n) * p.heads_v + head;
-        if (Sh::STAGES == 1 && n > 0) {
-            __syncthreads();
-            put_out(n - 1, 0);
-            __syncthreads();
-            issue(n, 0);
-            cp_async_commit();
-        }
-        cp_async_wait<0>();
-        tc_fence_smem();
-        __syncthreads();
-        float o[32], x[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = o[i] = to_float(vd[(half * 32 + i) * Sh::vpitch + row]);
-        put_terms<NP>(tl + cA + half * (NP * 16), x);
-        tc_wait_st();
-        tc_fence_before();
-        __syncthreads();
-        if (tid == 0) {  // 1
-            tc_fence_after();
-            tc_product<3, NP, 2, KT>(tm + c1, tc_idesc(64, false), false, aS, [bK](int i, int ks) {
-                return tc_desc(bK + i * Sh::plane + (ks >> 2) * TC_TILE + (ks & 3) * 32);
-            });
-            tc_product<NP, 3, 2, 4>(tm + c2, tc_idesc(64, true), false, aO,
-                                    [bP](int i, int ks) { return tc_desc(bP + i * TC_TILE + ks * 2048); });
-            tc_commit(mbar[0]);
-        }
-        if (Sh::STAGES == 2 && n > 0) put_out(n - 1, st ^ 1);
-        if (n + 1 < chunks) rows_of(n + 1);
-        if (live) {  // the gradient of the state leaving the chunk
-            float* g = p.wdS + rec * p.dv * DKP + vc;
-#pragma unroll
-            for (int i = 0; i < HS; ++i) g[(size_t)(half * HS + i) * p.dv] = S[i];
-        }
-        mbar_wait(mbar[0], par, &ws->dead);
-        tc_fence_after();
-        {
-            float z[32];
-            tc_ld32(tl + c1 + half * 32, x);
-            tc_ld32(tl + c2 + half * 32, z);
-            tc_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = vec[DL_C + half * 32 + i] * x[i] + z[i];
-        }
-        put_terms<3>(tl + cW + half * 48, x);
-        tc_wait_st();
-        tc_fence_before();
-        __syncthreads();
-        if (tid == 0) {  // 2
-            tc_fence_after();
-            tc_product<3, 3, 2, 4>(tm + c1, tc_idesc(64, true), false, aW,
-                                   [bT](int i, int ks) { return tc_desc(bT + i * TC_TILE + ks * 2048); });
-            tc_commit(mbar[1]);
-        }
-        if (Sh::STAGES == 2) {
-            if (n + 1 < chunks) issue(n + 1, st ^ 1);
-            cp_async_commit();
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] *= p.scale * vec[half * 32 + i];
-        put_terms<3>(tl + c2 + half * 48, o);
-        mbar_wait(mbar[1], par, &ws->dead);
-        tc_fence_after();
-        tc_ld32(tl + c1 + half * 32, x);
-        tc_wait_ld();
-        if (live) {
-            float* ox = p.wdX + rec * DL_C * p.dv + vc;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) ox[(size_t)(half * 32 + i) * p.dv] = x[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const int r = half * 32 + i;
-            x[i] *= vec[2 * DL_C + r];  // dV
-            store_elem(vd + r * Sh::vpitch + row, x[i]);
-            x[i] *= -vec[r];
-        }
-        put_terms<3>(tl + cW + half * 48, x);
-        tc_wait_st();
-        tc_fence_before();
-        __syncthreads();
-        if (tid == 0) {  // 3
-            tc_fence_after();
-#pragma unroll
-            for (int nb = 0; nb < Sh::KB; ++nb) {
-                auto mn = [nb](uint32_t t) {
-                    return [t, nb](int i, int ks) { return tc_desc(t + i * Sh::plane + nb * TC_TILE + ks * 2048); };
-                };
-                const uint32_t d = tm + cDS + nb * (3 * Sh::SC);
-                tc_product<3, NP, 2, 4>(d, tc_idesc(64, true), false, aQ, mn(bQ));
-                tc_product<3, NP, 2, 4>(d, tc_idesc(64, true), true, aW, mn(bK));
-            }
-            tc_commit(mbar[2]);
-        }
-        const float eC = vec[3 * DL_C];
-        mbar_wait(mbar[2], par, &ws->dead);
-        tc_fence_after();
-#pragma unroll
-        for (int i = 0; i < HS; i += 32) {
-            tc_ld32(tl + cDS + (DKP == 128 ? half * 3 * Sh::SC : half * 32) + i, x);
-            tc_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) S[i + e] = eC * S[i + e] + x[e];
-        }
-        put_state();
-    }
-    tc_wait_st();
-    cp_async_wait<0>();
-    tc_fence_before();
-    __syncthreads();
-    put_out(chunks - 1, Sh::STAGES == 2 ? (chunks - 1) & 1 : 0);
-    if (p.ds_out && live)
-#pragma unroll
-        for (int i = 0; i < HS; ++i)
-            if (half * HS + i < p.dk) p.ds_out[sbase + (size_t)(half * HS + i) * p.dv + vc] = S[i];
-    if (p.status && tid == 0 && ws->dead) atomicOr(p.status, DEV_STATUS_TIMEOUT);
-    if (warp == 0) tc_free(tm);
+    walk_end(ws, tm, p.status);
 }
 
 // ---- per-chunk gradients -------------------------------------------------------------
@@ -342,7 +306,7 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaParams p)
     const int t0 = (int)c * DL_C;
     const long long img = delta_img(p, b);
     const size_t rec = (size_t)blockIdx.x * p.heads_v + head;
-    const float* vec = p.wvec + rec * DL_VECS;
+    const float* vec = record_vec(p, rec);
     const float* wS = p.wS + rec * p.dv * DKP;
     const float* wdS = p.wdS + rec * p.dv * DKP;
     const float* wW = p.wW + rec * DL_C * p.dv;
@@ -500,7 +464,7 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaParams p)
     {
         const double* G = reinterpret_cast<const double*>(vec + 4 * DL_C);
         const double g0 = G[r0], g1 = G[r1];
-        const __nv_bfloat16* wP = p.wP + rec * 3 * DL_PLANE;
+        const __nv_bfloat16* wP = record_P(p, rec);
         const float* wL = p.wL + rec * DL_PLANE;
         double hr0 = 0.0, hr1 = 0.0;
 #pragma unroll
@@ -512,8 +476,8 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaParams p)
                 float pv[4] = {}, lv[4];
 #pragma unroll
                 for (int n = 2; n >= 0; --n) {
-                    const float2 x = load_pair(wP + n * DL_PLANE + r0 * DL_C + j);
-                    const float2 z = load_pair(wP + n * DL_PLANE + r1 * DL_C + j);
+                    const float2 x = load_pair(wP + n * DL_PLANE + plane_at(r0, j));
+                    const float2 z = load_pair(wP + n * DL_PLANE + plane_at(r1, j));
                     pv[0] += x.x; pv[1] += x.y; pv[2] += z.x; pv[3] += z.y;
                 }
                 const float2 l0 = load_pair(wL + r0 * DL_C + j), l1 = load_pair(wL + r1 * DL_C + j);

@@ -34,6 +34,16 @@ __host__ __device__ constexpr uint32_t tc_idesc(int n, bool b_mn_major)
     return 1u << 4 | 1u << 7 | 1u << 10 | (b_mn_major ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (128u >> 4) << 24;
 }
 
+// One lane of a converged warp. A branch on this predicate keeps the operands of the
+// products in uniform registers: a 64-column product then issues in its 32 cycles, behind a
+// branch on the thread index it took 47.
+__device__ __forceinline__ bool tc_elect()
+{
+    uint32_t p;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.b32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+
 // d[128][n] (+)= a[128][16] b[16][n]; d and a are tensor-memory addresses. One thread.
 __device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
 {
@@ -95,14 +105,39 @@ __device__ __forceinline__ void mbar_fence_init() { asm volatile("fence.mbarrier
 __device__ __forceinline__ bool mbar_test(uint32_t mbar, uint32_t parity)
 {
     uint32_t done;
-    asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.b32 %0, 1, 0, p;\n}\n"
+    asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\nselp.b32 %0, 1, 0, p;\n}\n"
                  : "=r"(done) : "r"(mbar), "r"(parity) : "memory");
     return done != 0;
 }
-// Wait for a phase, at most about a second in all: after that `dead` is set, this and
+// 16 bytes into shared memory, or zeros. (The copy with a source size in a register has to be
+// ready for any size.)
+__device__ __forceinline__ void copy16(void* smem, const void* gmem, bool valid)
+{
+    asm volatile("{\n.reg .pred p;\nsetp.eq.b32 p, %2, 0;\ncp.async.cg.shared.global [%0], [%1], 16, p;\n}\n" ::"r"(
+                     static_cast<unsigned>(__cvta_generic_to_shared(smem))), "l"(gmem), "r"((int)valid));
+}
+
+// Copies by the bulk engine: 16-byte aligned, a multiple of 16 bytes, counted by a barrier.
+__device__ __forceinline__ void mbar_expect(uint32_t mbar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(mbar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_in(uint32_t smem, const void* gmem, uint32_t bytes, uint32_t mbar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(smem), "l"(gmem),
+                 "r"(bytes), "r"(mbar) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t mbar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(mbar) : "memory");
+}
+// Named barriers: some threads only arrive, the others wait for them.
+__device__ __forceinline__ void bar_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;\n" ::"r"(id), "r"(threads) : "memory"); }
+__device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory"); }
+// Wait for a phase, at most about a second in all (each try sleeps for up to 1000 ns): after that `dead` is set, this and
 // every later wait of the CTA returns at once, and the kernel runs to its end with
 // invalid results instead of hanging.
-constexpr int TC_WAIT_TRIES = 1 << 21;
+constexpr int TC_WAIT_TRIES = 1 << 20;
 __device__ __forceinline__ void mbar_wait(uint32_t mbar, uint32_t parity, volatile int* dead)
 {
     int i = 0;
