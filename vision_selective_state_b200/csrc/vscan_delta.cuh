@@ -546,9 +546,8 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaParams p)
 //
 // The chain KS -> W -> dS -> S bounds the walk, so everything else is off it: eight
 // warps compute, one thread issues the products (the ones of the chain first), three
-// warps copy the next chunk's tiles in and the last one's y out, and a computing
-// thread never waits for another one, only for products. y of a chunk is finished
-// while the next one's KS runs. T and P are lower triangles: slice ks of their summed
+// warps copy the next chunks' tiles in, and a computing thread never waits for
+// another one, only for products. y of a chunk is finished while the next one's KS runs. T and P are lower triangles: slice ks of their summed
 // index touches the columns from 16 ks on only.
 // Tensor-memory columns: S terms (over them dS, once step 1 is done), KS (W, then W's
 // terms for O), QS, X's terms (then those of e^{G_C - G} W), O.
@@ -652,27 +651,37 @@ __device__ __forceinline__ void walk_load_values(T* dst, int pitch, const T* src
         copy16(dst + r * pitch + c, at + (ok ? row * tok : 0), ok);
     });
 }
-template <typename T>
-__device__ __forceinline__ void walk_store_values(T* dst, long long tok, const T* src, int pitch, const int* rows, int have, int tid)
+// 32 steps of a warp's 32 value channels to their token rows, through the warp's own corner of the
+// stage's value tile (whose values it alone has read): one value at a time from the registers,
+// 32 stores a lane took 2100 cycles a chunk, this takes 500. `mine` is this thread's value of
+// step 0 in the tile, `dst` the channel of lane 0.
+__device__ __forceinline__ void stage_two(float* p, int pitch, float x, float y)
 {
-    constexpr int V = 16 / sizeof(T), vecs = 128 / V, step = DW_HELP / vecs;
-    const int c = tid % vecs * V;
-    if (c >= have) return;
-    constexpr int B = 4;
-#pragma unroll 1
-    for (int r = tid / vecs; r < DL_C; r += B * step) {
-        int row[B];
-        uint4 x[B];
+    p[0] = x;
+    p[pitch] = y;
+}
+__device__ __forceinline__ void stage_two(__nv_bfloat16* p, int pitch, float x, float y)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);  // one conversion for both
+    p[0] = __low2bfloat16(h);
+    p[pitch] = __high2bfloat16(h);
+}
+template <typename T>
+__device__ __forceinline__ void walk_store(T* dst, long long tok, const int* rows, T* mine, int pitch, int have, int lane,
+                                           const float (&x)[32])
+{
 #pragma unroll
-        for (int i = 0; i < B; ++i) {
-            const int rs = min(r + i * step, DL_C - 1);
-            row[i] = rows[rs];
-            x[i] = *reinterpret_cast<const uint4*>(src + rs * pitch + c);
+    for (int i = 0; i < 32; i += 2) stage_two(mine + i * pitch, pitch, x[i], x[i + 1]);
+    __syncwarp();
+    constexpr int V = 16 / sizeof(T), vecs = 32 / V, per = 32 / vecs;  // pieces of a row, rows at a time
+    const int c = lane % vecs * V;
+    const T* src = mine - lane + c;
+    if (c < have)
+#pragma unroll
+        for (int i = 0; i < 32; i += per) {
+            const int r = i + lane / vecs, row = rows[r];
+            if (row >= 0) *reinterpret_cast<uint4*>(dst + row * tok + c) = *reinterpret_cast<const uint4*>(src + r * pitch);
         }
-#pragma unroll
-        for (int i = 0; i < B; ++i)
-            if (r + i * step < DL_C && row[i] >= 0) *reinterpret_cast<uint4*>(dst + row[i] * tok + c) = x[i];
-    }
 }
 
 // NT bf16 terms of 32 values of a row, term n in the 16 columns from addr + n * step on. Three
@@ -738,25 +747,12 @@ __device__ __forceinline__ void tc_product(bool add, F mma)
         }
 }
 
-// Two values `pitch` elements apart: one conversion for both.
-__device__ __forceinline__ void store_two(float* p, int pitch, float x, float y)
-{
-    p[0] = x;
-    p[pitch] = y;
-}
-__device__ __forceinline__ void store_two(__nv_bfloat16* p, int pitch, float x, float y)
-{
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-    p[0] = __low2bfloat16(h);
-    p[pitch] = __high2bfloat16(h);
-}
-
 // What a walk's CTA keeps in shared memory besides the stages.
 struct WalkShared {
     unsigned long long full[2], empty[2], done[5];
     uint32_t tmem;
     int dead;
-    int rows[3][DL_C];  // token rows of chunk c in slot c mod 3
+    alignas(16) int rows[3][DL_C];  // token rows of chunk c in slot c mod 3
 };
 
 struct WalkBars {
@@ -797,26 +793,22 @@ __device__ __forceinline__ void walk_end(WalkShared* w, uint32_t tm, int* status
     if (threadIdx.x < 32) tc_free(tm);
 }
 
-// The copying warps' part: chunk n of `chunks` into stage n mod STAGES, after `out` has taken
-// what the stage's last chunk left in it. `in` returns the bytes of its thread's bulk copies.
-template <int STAGES, typename ROWS, typename IN, typename OUT>
-__device__ __forceinline__ void walk_copy(WalkShared* w, const WalkBars& bar, int chunks, int tid, ROWS row_of, IN in, OUT out)
+// The copying warps' part: chunk n of `chunks` into stage n mod STAGES. `in` returns the bytes of
+// its thread's bulk copies.
+template <int STAGES, typename ROWS, typename IN>
+__device__ __forceinline__ void walk_copy(WalkShared* w, const WalkBars& bar, int chunks, int tid, ROWS row_of, IN in)
 {
-    for (int n = 0; n < chunks + STAGES; ++n) {
-        const int st = STAGES == 2 ? n & 1 : 0, before = n - STAGES;
-        if (before >= 0 && before < chunks) {
-            mbar_wait(bar.empty + 8 * st, (before / STAGES) & 1, &w->dead);
-            out(st, w->rows[before % 3]);
-        }
-        if (n < chunks) {
-            if (tid < DL_C) w->rows[n % 3][tid] = row_of(n, tid);
-            bar_sync(7, DW_HELP);  // rows are in, and all have taken what they copy out of the stage
-            const uint32_t bytes = in(n, st, w->rows[n % 3]);
-            cp_async_commit();
-            cp_async_wait<0>();
-            tc_fence_smem();
-            mbar_expect(bar.full + 8 * st, bytes);
-        }
+    for (int n = 0; n < chunks; ++n) {
+        const int st = STAGES == 2 ? n & 1 : 0;
+        // chunk n - 3, the last user of this slot, is done: the wait for chunk n - 1 - STAGES saw to it
+        if (tid < DL_C) w->rows[n % 3][tid] = row_of(n, tid);
+        bar_sync(7, DW_HELP);
+        if (n >= STAGES) mbar_wait(bar.empty + 8 * st, ((n - STAGES) / STAGES) & 1, &w->dead);
+        const uint32_t bytes = in(n, st, w->rows[n % 3]);
+        cp_async_commit();
+        cp_async_wait<0>();
+        tc_fence_smem();
+        mbar_expect(bar.full + 8 * st, bytes);
     }
 }
 
@@ -923,7 +915,6 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_scan_kernel(const DeltaPa
             const T* q = reinterpret_cast<const T*>(p.q) + img * p.q_img + (long long)hk * p.dk;
             const T* k = reinterpret_cast<const T*>(p.k) + img * p.k_img + (long long)hk * p.dk;
             const T* v = reinterpret_cast<const T*>(p.v) + img * p.v_img + (long long)head * p.dv + slice;
-            T* y = reinterpret_cast<T*>(p.y) + img * p.y_img + (long long)head * p.dv + slice;
             const int dvs = min(128, p.dv - slice);
             walk_copy<STAGES>(
                 ws, bar, chunks, ht, [&](int c, int r) { return delta_row(p, s, c * DL_C + r); },
@@ -940,11 +931,6 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_scan_kernel(const DeltaPa
                         bulk_in(at + Sh::oVec, record_vec(p, rec), bytes, full);
                     }
                     return bytes;
-                },
-                [&](int st, const int* rows) {
-                    if (!SAVE)
-                        walk_store_values(y, p.y_tok, reinterpret_cast<const T*>(stages + st * STAGE + Sh::oV(PP)), Sh::vpitch, rows,
-                                          dvs, ht);
                 });
         }
     } else {
@@ -952,6 +938,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_scan_kernel(const DeltaPa
         const int half = warp >> 2, row = (warp & 3) * 32 + lane, vc = slice + row;  // this thread's value channel
         const bool live = vc < p.dv;
         const uint32_t tl = tm + ((uint32_t)(warp & 3) << 21);  // this warp's 32 rows
+        T* y = reinterpret_cast<T*>(p.y) + delta_img(p, b) * p.y_img + (long long)head * p.dv + vc - lane;
         float S[HS];  // S^T[row][half * HS + i]
 #pragma unroll
         for (int i = 0; i < HS; ++i) {
@@ -1045,7 +1032,8 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_scan_kernel(const DeltaPa
                 tc_ld32(tl + cO + half * 32, x);
                 tc_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) store_two(vd + i * Sh::vpitch, Sh::vpitch, o[i] + x[i], o[i + 1] + x[i + 1]);
+                for (int i = 0; i < 32; ++i) x[i] += o[i];
+                walk_store(y, p.y_tok, ws->rows[c % 3] + half * 32, vd, Sh::vpitch, p.dv - vc + lane, lane, x);
             }
             mbar_arrive(bar.empty + 8 * st);
         }

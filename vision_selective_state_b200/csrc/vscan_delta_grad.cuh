@@ -124,8 +124,6 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaP
             const T* q = reinterpret_cast<const T*>(p.q) + img * p.q_img + (long long)hk * p.dk;
             const T* k = reinterpret_cast<const T*>(p.k) + img * p.k_img + (long long)hk * p.dk;
             const T* dy = reinterpret_cast<const T*>(p.dy) + img * p.y_img + (long long)head * p.dv + slice;
-            T* dvalue = reinterpret_cast<T*>(p.dvalue);
-            if (dvalue) dvalue += (img * p.tokens * p.heads_v + head) * (long long)p.dv + slice;
             const int dvs = min(128, p.dv - slice);
             walk_copy<STAGES>(
                 ws, bar, chunks, ht, [&](int n, int r) { return delta_row(p, s, (chunks - 1 - n) * DL_C + r); },
@@ -142,11 +140,6 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaP
                         bulk_in(at + Sh::oVec, record_vec(p, rec), bytes, full);
                     }
                     return bytes;
-                },
-                [&](int st, const int* rows) {  // dV, left in dO's place
-                    if (dvalue)
-                        walk_store_values(dvalue, (long long)p.heads_v * p.dv,
-                                          reinterpret_cast<const T*>(stages + st * STAGE + Sh::oV(3)), Sh::vpitch, rows, dvs, ht);
                 });
         }
     } else {
@@ -154,6 +147,8 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaP
         const int half = warp >> 2, row = (warp & 3) * 32 + lane, vc = slice + row;
         const bool live = vc < p.dv;
         const uint32_t tl = tm + ((uint32_t)(warp & 3) << 21);
+        T* dvalue = reinterpret_cast<T*>(p.dvalue);
+        if (dvalue) dvalue += (delta_img(p, b) * p.tokens * p.heads_v + head) * (long long)p.dv + vc - lane;
         float S[HS];  // dS^T[row][half * HS + i]
 #pragma unroll
         for (int i = 0; i < HS; ++i) {
@@ -208,15 +203,16 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaP
                 for (int i = 0; i < 32; ++i) ox[(size_t)i * p.dv] = x[i];
             }
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-                x[i] *= vec[2 * DL_C + i];  // dV
-                x[i + 1] *= vec[2 * DL_C + i + 1];
-                store_two(vd + i * Sh::vpitch, Sh::vpitch, x[i], x[i + 1]);
-                x[i] *= -vec[i];
-                x[i + 1] *= -vec[i + 1];
+            for (int i = 0; i < 32; ++i) x[i] *= vec[2 * DL_C + i];  // dV
+            {
+                float u[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) u[i] = x[i] * -vec[i];
+                put_terms<3>(tl + cW + half * 48, 16, u);
             }
-            put_terms<3>(tl + cW + half * 48, 16, x);
             walk_ready(5);
+            if (dvalue)
+                walk_store(dvalue, (long long)p.heads_v * p.dv, ws->rows[n % 3] + half * 32, vd, Sh::vpitch, p.dv - vc + lane, lane, x);
             const float eC = vec[3 * DL_C - half * 32];
             mbar_wait(bar.done + 16, par, &ws->dead);
             tc_fence_after();
