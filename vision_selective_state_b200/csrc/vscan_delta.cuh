@@ -330,39 +330,124 @@ __device__ __forceinline__ float exp_diff(double d)
 // Element (i, j) of a 64 x 64 plane of the workspace: the image of a swizzled tile.
 __device__ __forceinline__ int plane_at(int i, int j) { return tc_swizzle(i, j >> 3) / 2 + (j & 7); }
 
-// ---- per-chunk triangle: T, P, decays -----------------------------------------------
-// One CTA of four warps per chunk and value head. Bound by latency: two
-// 64 x 64 x dk products, 4 x 16 dependent rows of forward substitution and three
-// rounds of 16 x 16 block products.
-template <int DKP>
-struct PrepShape {
-    static constexpr int pitch = DKP + 8;  // an odd multiple of 16 bytes
-    static constexpr int plane = DL_C * pitch;
-};
+// THREADS threads move the 64 rows of VECS 16-byte pieces of a chunk; a thread keeps to one piece
+// and to every (THREADS / VECS)-th row, four rows at a time: their token rows are read before the
+// first of the four copies, which those reads could not pass. Not unrolled further: in the walks
+// this code runs once a chunk between the computing warps' long one, and unrolled it spent its
+// time on instruction-cache misses (70 to 140 cycles a piece).
+template <int VECS, int THREADS, typename F>
+__device__ __forceinline__ void copy_rows(const int* rows, int tid, F copy)
+{
+    constexpr int step = THREADS / VECS, B = 4;
+    if (THREADS % VECS != 0 && tid >= step * VECS) return;
+#pragma unroll 1
+    for (int r = tid / VECS; r < DL_C; r += B * step) {
+        int row[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i) row[i] = rows[min(r + i * step, DL_C - 1)];
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+            if (r + i * step < DL_C) copy(r + i * step, row[i]);
+    }
+}
 
-constexpr int DL_LP = DL_C + 1;  // pitch of the float32 triangle
+// ---- per-chunk triangle: T, P, decays -----------------------------------------------
+// One CTA of eight warps per chunk and value head, bound by the latency of its chain, so
+// the chain is kept short and several CTAs share an SM: warps 0-3 form K K^T, L and T,
+// warps 4-7 Q K^T and P at the same time, row block by row block of 16. T comes from
+// the inverses of the four diagonal 16 x 16 blocks (one column a lane, each known
+// entry subtracted from all later ones at once), merged twice:
+//   [A 0; C B]^-1 = [A^-1 0; -B^-1 C A^-1 B^-1].
+// L and T's blocks lie transposed as well, so that four rows of a left factor are one
+// 16-byte read. The record is assembled in shared memory, in the walks' swizzled
+// layout, and leaves in two bulk copies; blocks above the diagonal hold nothing, and
+// nothing reads them.
+constexpr int DP_THREADS = 256;
+constexpr int DP_LP = 68, DP_TP = 36;  // row pitches of L^T and of the 32 x 32 blocks of T
 
 template <typename T, int DKP>
-constexpr size_t delta_prep_smem()
+struct PrepShape {
+    static constexpr int NP = DeltaIo<T>::planes;
+    static constexpr int pitch = DKP + 8;  // an odd multiple of 16 bytes
+    static constexpr int plane = DL_C * pitch;
+    static constexpr int tiles = 2 * NP * plane * 2;                      // bytes of K and Q, until the products are done:
+    static constexpr int image = DL_VECS * 4 + 3 * DL_PLANE * 2;          // then decays and T's planes,
+    static constexpr int later = image + DL_C * DP_TP * 4;                // and T by rows
+    static constexpr int front = (tiles > later ? tiles : later);
+    static __host__ __device__ constexpr int oP() { return front; }
+    static __host__ __device__ constexpr int oL(int pplanes) { return front + pplanes * DL_PLANE * 2; }
+    static __host__ __device__ constexpr int oTt(int pplanes) { return oL(pplanes) + DL_C * DP_LP * 4; }
+    static __host__ __device__ constexpr int oM(int pplanes) { return oTt(pplanes) + DL_C * DP_TP * 4; }
+    static __host__ __device__ constexpr int oGates(int pplanes) { return oM(pplanes) + 32 * DP_TP * 4; }
+    static __host__ __device__ constexpr size_t smem(int pplanes) { return oGates(pplanes) + DL_C * (8 + 4 * 7); }
+};
+
+// A value's three bf16 terms, one in each plane of T's image; `at` is its plane_at.
+__device__ __forceinline__ void image_put(__nv_bfloat16* img, int at, float x)
 {
-    const size_t tiles = 2 * (size_t)DeltaIo<T>::planes * PrepShape<DKP>::plane * 2;
-    const size_t tri = 2 * (size_t)DL_C * DL_LP * 4 + 4 * 16 * 17 * 4;
-    return tiles + tri + DL_C * 8 + 4 * DL_C * 4;
+    uint16_t* o = reinterpret_cast<uint16_t*>(img) + at;
+#pragma unroll
+    for (int n = 0; n < 3; ++n) {
+        const uint32_t u = __float_as_uint(x);
+        o[n * DL_PLANE] = (uint16_t)(u >> 16);
+        x -= __uint_as_float(u & 0xffff0000u);
+    }
+}
+
+// The rows of K or Q to padded rows in bf16 planes, by all warps but the first.
+template <int DKP>
+__device__ __forceinline__ void prep_load(__nv_bfloat16* dst, const __nv_bfloat16* src, long long tok, const int* rows, int have, int tid)
+{
+    constexpr int vecs = DKP / 8;
+    const int c = tid % vecs * 8;
+    const __nv_bfloat16* at = c < have ? src + c : src;
+    copy_rows<vecs, DP_THREADS - 32>(rows, tid, [&](int r, int row) {
+        const bool ok = c < have && row >= 0;
+        copy16(dst + r * (DKP + 8) + c, at + (ok ? row * tok : 0), ok);
+    });
+}
+template <int DKP>
+__device__ __forceinline__ void prep_load(__nv_bfloat16* dst, const float* src, long long tok, const int* rows, int have, int tid)
+{
+    constexpr int vecs = DKP / 8;
+    const int c = tid % vecs * 8;
+    copy_rows<vecs, DP_THREADS - 32>(rows, tid, [&](int r, int row) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), z = x;
+        if (row >= 0 && c < have) x = __ldg(reinterpret_cast<const float4*>(src + c + row * tok));
+        if (row >= 0 && c + 4 < have) z = __ldg(reinterpret_cast<const float4*>(src + c + 4 + row * tok));
+#pragma unroll
+        for (int n = 0; n < 3; ++n) {
+            uint4 u;
+            u.x = split_bf16(x.x, x.y);
+            u.y = split_bf16(x.z, x.w);
+            u.z = split_bf16(z.x, z.y);
+            u.w = split_bf16(z.z, z.w);
+            *reinterpret_cast<uint4*>(dst + n * (DL_C * (DKP + 8)) + r * (DKP + 8) + c) = u;
+        }
+    });
 }
 
 template <typename T, int DKP>
-__global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaParams p)
+__global__ void __launch_bounds__(DP_THREADS) delta_prep_kernel(const DeltaParams p)
 {
-    constexpr int NP = DeltaIo<T>::planes, PITCH = PrepShape<DKP>::pitch, PLANE = PrepShape<DKP>::plane;
-    extern __shared__ __align__(16) unsigned char smem[];
-    double* G = reinterpret_cast<double*>(smem);
-    float* beta = reinterpret_cast<float*>(G + DL_C);
-    float* L = beta + 4 * DL_C;                 // [64][65]
-    float* Ti = L + DL_C * DL_LP;               // [64][65]
-    float* tmp = Ti + DL_C * DL_LP;             // [4 warps][16][17]
-    __nv_bfloat16* K = reinterpret_cast<__nv_bfloat16*>(tmp + 4 * 16 * 17);
+    using Sh = PrepShape<T, DKP>;
+    constexpr int NP = Sh::NP, PITCH = Sh::pitch, PLANE = Sh::plane;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __nv_bfloat16* K = reinterpret_cast<__nv_bfloat16*>(smem);
     __nv_bfloat16* Q = K + NP * PLANE;
+    float* vec = reinterpret_cast<float*>(smem);
+    __nv_bfloat16* imgT = reinterpret_cast<__nv_bfloat16*>(vec + DL_VECS);
+    float* Tr = reinterpret_cast<float*>(smem + Sh::image);                 // T_ij at [i][j mod 32]
+    __nv_bfloat16* imgP = reinterpret_cast<__nv_bfloat16*>(smem + Sh::oP());
+    float* Lt = reinterpret_cast<float*>(smem + Sh::oL(p.tplanes));         // L_ij at [j][i]
+    float* Tt = reinterpret_cast<float*>(smem + Sh::oTt(p.tplanes));        // T_ij at [j][i mod 32]
+    float* M = reinterpret_cast<float*>(smem + Sh::oM(p.tplanes));
+    float2* G = reinterpret_cast<float2*>(smem + Sh::oGates(p.tplanes));    // running sum, rounded and rest
+    float* beta = reinterpret_cast<float*>(G + DL_C);
+    float *onward = beta + DL_C, *upto = onward + DL_C;                     // [64]; [4][64], row block 0 unused
+    int* rows = reinterpret_cast<int*>(upto + 4 * DL_C);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, head = blockIdx.y;
+    const int group = warp >> 2, m0 = (warp & 3) * 16;
 
     // the sequence of this slot
     int b;
@@ -384,23 +469,21 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaParams p)
     const int hk = head / p.group;
     const size_t rec = (size_t)blockIdx.x * p.heads_v + head;
 
-    load_tile(K, PITCH, PLANE, reinterpret_cast<const T*>(p.k) + img * p.k_img + (long long)hk * p.dk, p.k_tok, p, s, t0,
-              DKP, p.dk, tid, 128);
-    load_tile(Q, PITCH, PLANE, reinterpret_cast<const T*>(p.q) + img * p.q_img + (long long)hk * p.dk, p.q_tok, p, s, t0,
-              DKP, p.dk, tid, 128);
-    cp_async_commit();
-
+    double g[2];
     if (warp == 0) {  // running sum of the log decay: two steps a lane, then a scan over the lanes
-        double g[2];
         const float A = p.A[head], bias = p.bias ? p.bias[head] : 0.f;
+        float a[2], bb[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int t = t0 + 2 * lane + i;
-            const int row = delta_row(p, s, t);
-            const float a = row >= 0 ? to_float(reinterpret_cast<const T*>(p.a)[img * p.a_img + row * p.a_tok + head]) : 0.f;
-            const float bb = row >= 0 ? to_float(reinterpret_cast<const T*>(p.b)[img * p.b_img + row * p.b_tok + head]) : 0.f;
-            g[i] = t < s.len ? (double)delta_decay(A, a + bias) : 0.0;
-            beta[2 * lane + i] = t < s.len ? p.beta_scale * delta_sigmoid(bb) : 0.f;
+            const int row = delta_row(p, s, t0 + 2 * lane + i);
+            a[i] = row >= 0 ? to_float(reinterpret_cast<const T*>(p.a)[img * p.a_img + row * p.a_tok + head]) : 0.f;
+            bb[i] = row >= 0 ? to_float(reinterpret_cast<const T*>(p.b)[img * p.b_img + row * p.b_tok + head]) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const bool in = t0 + 2 * lane + i < s.len;
+            g[i] = in ? (double)delta_decay(A, a[i] + bias) : 0.0;
+            beta[2 * lane + i] = in ? p.beta_scale * delta_sigmoid(bb[i]) : 0.f;
         }
         double sum = g[0] + g[1];
 #pragma unroll
@@ -408,125 +491,205 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaParams p)
             const double other = __shfl_up_sync(0xffffffffu, sum, o);
             if (lane >= o) sum += other;
         }
-        G[2 * lane] = sum - g[1];
-        G[2 * lane + 1] = sum;
-        __syncwarp();
-        float* vec = record_vec(p, rec);
-        const double last = G[DL_C - 1];
+        g[0] = sum - g[1];
+        g[1] = sum;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = 2 * lane + i;
-            vec[r] = exp_diff(G[r]);
-            vec[DL_C + r] = exp_diff(last - G[r]);
-            vec[2 * DL_C + r] = beta[r];
-        }
-        if (lane == 0) vec[3 * DL_C] = exp_diff(last);
-        *reinterpret_cast<double2*>(vec + 4 * DL_C + 4 * lane) = make_double2(G[2 * lane], G[2 * lane + 1]);
+        for (int i = 0; i < 2; ++i) G[2 * lane + i] = make_float2((float)g[i], (float)(g[i] - (double)(float)g[i]));
+    } else {  // the other warps fetch K and Q
+        const int ht = tid - 32;
+        if (ht < DL_C) rows[ht] = delta_row(p, s, t0 + ht);
+        bar_sync(3, DP_THREADS - 32);
+        prep_load<DKP>(K, reinterpret_cast<const T*>(p.k) + img * p.k_img + (long long)hk * p.dk, p.k_tok, rows, p.dk, ht);
+        prep_load<DKP>(Q, reinterpret_cast<const T*>(p.q) + img * p.q_img + (long long)hk * p.dk, p.q_tok, rows, p.dk, ht);
+        cp_async_commit();
+        cp_async_wait<0>();
     }
-    cp_async_wait<0>();
     __syncthreads();
+    // Decays between blocks of 16 steps, in two factors of at most 1: from step j to the first of
+    // row block B, and on from there to step i. Inside a block each pair has its own.
+    if (tid < DL_C) {
+        const float2 x = G[tid], r = G[tid & ~15];
+        onward[tid] = expf((x.x - r.x) + (x.y - r.y));
+    } else {
+        const int bi = tid >> 6, j = tid & 63;  // 1 .. 3
+        const float2 x = G[j], r = G[bi * 16];
+        if (j < bi * 16) upto[bi * DL_C + j] = expf((r.x - x.x) + (r.y - x.y));
+    }
 
-    // K K^T and Q K^T, rows 16 warp .. of the lower triangle
+    // K K^T (warps 0-3) and Q K^T, the lower triangle of a row block
+    float acc[8][4] = {};
     {
-        float kk[8][4] = {}, qk[8][4] = {};
-        const int m0 = warp * 16;
+        const __nv_bfloat16* left = group ? Q : K;
+#pragma unroll 2
         for (int k0 = 0; k0 < DKP; k0 += 16) {
-            Frag4 ak[NP], aq[NP];
+            Frag4 a[NP];
 #pragma unroll
-            for (int n = 0; n < NP; ++n) {
-                ak[n] = load_a(K + n * PLANE, PITCH, m0, k0, lane);
-                aq[n] = load_a(Q + n * PLANE, PITCH, m0, k0, lane);
-            }
+            for (int n = 0; n < NP; ++n) a[n] = load_a(left + n * PLANE, PITCH, m0, k0, lane);
 #pragma unroll
             for (int nt = 0; nt < 8; nt += 2) {
                 if (nt * 8 <= m0) {
                     Frag4 bk[NP];
 #pragma unroll
                     for (int n = 0; n < NP; ++n) bk[n] = load_b(K + n * PLANE, PITCH, nt * 8, k0, lane);
-                    mma_terms<NP, NP>(kk[nt], kk[nt + 1], ak, bk);
-                    mma_terms<NP, NP>(qk[nt], qk[nt + 1], aq, bk);
+                    mma_terms<NP, NP>(acc[nt], acc[nt + 1], a, bk);
                 }
             }
         }
-        __nv_bfloat16* wP = record_P(p, rec);
-        const int gr = lane >> 2, tc = (lane & 3) * 2;
+    }
+    __syncthreads();  // K and Q are read: their place is the record's now
+    {
+        const int r0 = m0 + (lane >> 2), tc = (lane & 3) * 2;
 #pragma unroll
-        for (int nt = 0; nt < 8; ++nt)
+        for (int nt = 0; nt < 8; ++nt) {
+            if (nt * 8 > m0 + 15) continue;
+            const bool within = nt * 8 >= m0;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const int i = m0 + gr + half * 8, j = nt * 8 + tc;
-                float pv[2], lv[2];
+                const int i = r0 + half * 8, j = nt * 8 + tc;
+                float v[2];
+                if (within) {
+                    const float2 gi = G[i];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    // selected, not multiplied by zero: what lies above the diagonal is not looked at
-                    const float d = j + e <= i ? exp_diff(G[i] - G[j + e]) : 0.f;
-                    pv[e] = j + e <= i ? p.scale * (d * qk[nt][half * 2 + e]) : 0.f;
-                    lv[e] = j + e < i ? d * kk[nt][half * 2 + e] : 0.f;
-                    L[i * DL_LP + j + e] = beta[i] * lv[e];
-                    Ti[i * DL_LP + j + e] = 0.f;
-                }
-                if (p.wL) *reinterpret_cast<float2*>(p.wL + rec * DL_PLANE + i * DL_C + j) = make_float2(lv[0], lv[1]);
-                if (p.tplanes == 2) {  // rounded, both: what the product of the second terms would add is left out
-                    const uint32_t u = round_bf16(pv[0], pv[1]);
-                    *reinterpret_cast<uint32_t*>(wP + plane_at(i, j)) = u;
-                    *reinterpret_cast<uint32_t*>(wP + DL_PLANE + plane_at(i, j)) =
-                        round_bf16(pv[0] - __uint_as_float(u << 16), pv[1] - __uint_as_float(u & 0xffff0000u));
+                    for (int e = 0; e < 2; ++e) {
+                        const float2 gj = G[j + e];
+                        // selected, not multiplied by zero: what lies above the diagonal is not looked at
+                        const float d = expf((gi.x - gj.x) + (gi.y - gj.y));
+                        v[e] = j + e < i + group ? d * acc[nt][half * 2 + e] : 0.f;
+                    }
                 } else {
-                    for (int n = 0; n < 3; ++n)
-                        *reinterpret_cast<uint32_t*>(wP + n * DL_PLANE + plane_at(i, j)) = split_bf16(pv[0], pv[1]);
+                    const float f = onward[i];
+                    const float2 h = *reinterpret_cast<const float2*>(upto + (m0 / 16) * DL_C + j);
+                    v[0] = f * h.x * acc[nt][half * 2];
+                    v[1] = f * h.y * acc[nt][half * 2 + 1];
+                }
+                if (group) {
+                    v[0] *= p.scale;
+                    v[1] *= p.scale;
+                    const int at = i * 64 + ((nt ^ (lane >> 2)) << 3) + tc;  // plane_at(i, j)
+                    if (p.tplanes == 2) {  // rounded, both: what the product of the second terms would add is left out
+                        const uint32_t u = round_bf16(v[0], v[1]);
+                        *reinterpret_cast<uint32_t*>(imgP + at) = u;
+                        *reinterpret_cast<uint32_t*>(imgP + DL_PLANE + at) =
+                            round_bf16(v[0] - __uint_as_float(u << 16), v[1] - __uint_as_float(u & 0xffff0000u));
+                    } else {
+                        for (int n = 0; n < 3; ++n)
+                            *reinterpret_cast<uint32_t*>(imgP + n * DL_PLANE + at) = split_bf16(v[0], v[1]);
+                    }
+                } else {
+                    if (p.wL) *reinterpret_cast<float2*>(p.wL + rec * DL_PLANE + i * DL_C + j) = make_float2(v[0], v[1]);
+                    Lt[j * DP_LP + i] = beta[i] * v[0];
+                    Lt[(j + 1) * DP_LP + i] = beta[i] * v[1];
                 }
             }
+        }
     }
-    __syncthreads();
-
-    // T = (I + L)^-1. Diagonal 16 x 16 blocks by forward substitution, one
-    // column a lane, one block a warp.
-    if (lane < 16) {
+    unsigned char* out = p.wrec + rec * delta_record_bytes(p.tplanes);
+    if (group) {
+        tc_fence_smem();
+        bar_sync(2, 128);
+        if (tid == 128) {
+            bulk_out(out + Sh::image, imgP, p.tplanes * DL_PLANE * 2);
+            bulk_out_read();
+        }
+        return;
+    }
+    if (warp == 0) {
+        const double last = __shfl_sync(0xffffffffu, g[1], 31);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = 2 * lane + i;
+            vec[r] = exp_diff(g[i]);
+            vec[DL_C + r] = exp_diff(last - g[i]);
+            vec[2 * DL_C + r] = beta[r];
+        }
+        if (lane == 0) vec[3 * DL_C] = exp_diff(last);
+        *reinterpret_cast<double2*>(vec + 4 * DL_C + 4 * lane) = make_double2(g[0], g[1]);
+    }
+    bar_sync(1, 128);
+    if (lane < 16) {  // inverse of diagonal block m0, column `lane`
         float x[16];
-        const float* Lb = L + (warp * 16) * DL_LP + warp * 16;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = i == lane ? 1.f : 0.f;
+        const float* L = Lt + m0 * DP_LP + m0;
+#pragma unroll
+        for (int j = 0; j < 15; ++j) {
+            float l[16];
+#pragma unroll
+            for (int q = (j + 1) / 4; q < 4; ++q) *reinterpret_cast<float4*>(l + 4 * q) = *reinterpret_cast<const float4*>(L + j * DP_LP + 4 * q);
+#pragma unroll
+            for (int i = j + 1; i < 16; ++i) x[i] -= l[i] * x[j];
+        }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            float v = i == lane ? 1.f : 0.f;
-#pragma unroll
-            for (int j = 0; j < i; ++j) v -= Lb[i * DL_LP + j] * x[j];
-            x[i] = v;
-            Ti[(warp * 16 + i) * DL_LP + warp * 16 + lane] = v;
+            Tr[(m0 + i) * DP_TP + (m0 & 31) + lane] = x[i];
+            Tt[(m0 + lane) * DP_TP + (m0 & 31) + i] = x[i];
+            image_put(imgT, (m0 + i) * 64 + ((((m0 + lane) >> 3) ^ (i & 7)) << 3) + (lane & 7), x[i]);
         }
     }
-    __syncthreads();
-    // Blocks at distance d below the diagonal: T_rs = -T_rr sum_m L_rm T_ms.
-    for (int d = 1; d < 4; ++d) {
-        const int r = warp + d;
-        if (r < 4) {
-            float* t = tmp + warp * 16 * 17;
-            const int col = lane & 15, half = (lane >> 4) * 8;
-            float m[8] = {};
-            for (int kk = warp * 16; kk < r * 16; ++kk) {
-                const float x = Ti[kk * DL_LP + warp * 16 + col];
+    bar_sync(1, 128);
+    {  // 16 x 16 blocks below the diagonal of both 32 x 32 ones: four rows of a column a thread
+        const int b0 = (tid >> 6) * 32, col = tid & 15, r = (tid >> 4 & 3) * 4;
+        float m[4] = {}, o[4] = {};
+        float* Mb = M + (tid >> 6) * 16 * DP_TP;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) m[i] += L[(r * 16 + half + i) * DL_LP + kk] * x;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) t[(half + i) * 17 + col] = m[i];
-            __syncwarp();
-            float o[8] = {};
-#pragma unroll 4
-            for (int kk = 0; kk < 16; ++kk) {
-                const float x = t[kk * 17 + col];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] -= Ti[(r * 16 + half + i) * DL_LP + r * 16 + kk] * x;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) Ti[(r * 16 + half + i) * DL_LP + warp * 16 + col] = o[i];
+        for (int k = 0; k < 16; ++k) {
+            const float4 l = *reinterpret_cast<const float4*>(Lt + (b0 + k) * DP_LP + b0 + 16 + r);
+            const float x = Tr[(b0 + k) * DP_TP + col];
+            m[0] += l.x * x; m[1] += l.y * x; m[2] += l.z * x; m[3] += l.w * x;
         }
-        __syncthreads();
-    }
-    __nv_bfloat16* wT = record_T(p, rec);
-    for (int i = tid; i < DL_PLANE / 2; i += 128) {
-        const int r = i >> 5, j = (i & 31) * 2;
-        float x = Ti[r * DL_LP + j], y = Ti[r * DL_LP + j + 1];
 #pragma unroll
-        for (int n = 0; n < 3; ++n) *reinterpret_cast<uint32_t*>(wT + n * DL_PLANE + plane_at(r, j)) = split_bf16(x, y);
+        for (int i = 0; i < 4; ++i) Mb[(r + i) * DP_TP + col] = m[i];
+        bar_sync(1, 128);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const float4 l = *reinterpret_cast<const float4*>(Tt + (b0 + 16 + k) * DP_TP + 16 + r);
+            const float x = Mb[k * DP_TP + col];
+            o[0] -= l.x * x; o[1] -= l.y * x; o[2] -= l.z * x; o[3] -= l.w * x;
+        }
+        bar_sync(1, 128);
+        *reinterpret_cast<float4*>(Tt + (b0 + col) * DP_TP + 16 + r) = make_float4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            Tr[(b0 + 16 + r + i) * DP_TP + col] = o[i];
+            image_put(imgT, plane_at(b0 + 16 + r + i, b0 + col), o[i]);
+        }
+        // above the diagonal of the 32 x 32 blocks, which the next products read
+#pragma unroll
+        for (int i = 0; i < 4; ++i) Tr[(b0 + r + i) * DP_TP + 16 + col] = 0.f;
+        *reinterpret_cast<float4*>(Tt + (b0 + 16 + col) * DP_TP + r) = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    bar_sync(1, 128);
+    {  // the 32 x 32 block below the diagonal: four rows of two columns a thread
+        const int col = (tid & 15) * 2, r = (tid >> 4) * 4;
+        float m[4][2] = {}, o[4][2] = {};
+#pragma unroll 8
+        for (int k = 0; k < 32; ++k) {
+            const float4 l = *reinterpret_cast<const float4*>(Lt + k * DP_LP + 32 + r);
+            const float2 x = *reinterpret_cast<const float2*>(Tr + k * DP_TP + col);
+            m[0][0] += l.x * x.x; m[1][0] += l.y * x.x; m[2][0] += l.z * x.x; m[3][0] += l.w * x.x;
+            m[0][1] += l.x * x.y; m[1][1] += l.y * x.y; m[2][1] += l.z * x.y; m[3][1] += l.w * x.y;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<float2*>(M + (r + i) * DP_TP + col) = make_float2(m[i][0], m[i][1]);
+        bar_sync(1, 128);
+#pragma unroll 8
+        for (int k = 0; k < 32; ++k) {
+            const float4 l = *reinterpret_cast<const float4*>(Tt + (32 + k) * DP_TP + r);
+            const float2 x = *reinterpret_cast<const float2*>(M + k * DP_TP + col);
+            o[0][0] -= l.x * x.x; o[1][0] -= l.y * x.x; o[2][0] -= l.z * x.x; o[3][0] -= l.w * x.x;
+            o[0][1] -= l.x * x.y; o[1][1] -= l.y * x.y; o[2][1] -= l.z * x.y; o[3][1] -= l.w * x.y;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int n = 0; n < 3; ++n)
+                *reinterpret_cast<uint32_t*>(imgT + n * DL_PLANE + plane_at(32 + r + i, col)) = split_bf16(o[i][0], o[i][1]);
+    }
+    tc_fence_smem();
+    bar_sync(1, 128);
+    if (tid == 0) {
+        bulk_out(out, vec, Sh::image);
+        bulk_out_read();
     }
 }
 
@@ -580,26 +743,6 @@ struct WalkShape {
     static constexpr int SC = DKP / 4;
 };
 
-// The copying warps move rows of VECS 16-byte pieces; a thread keeps to one piece and to every
-// (DW_HELP / VECS)-th row, four rows at a time: their token rows are read before the first of
-// the four copies, which those reads could not pass. Not unrolled further: this code runs once
-// a chunk between the computing warps' long one, and unrolled it spent its time on
-// instruction-cache misses (70 to 140 cycles a piece).
-template <int VECS, typename F>
-__device__ __forceinline__ void copy_rows(const int* rows, int tid, F copy)
-{
-    constexpr int step = DW_HELP / VECS, B = 4;
-#pragma unroll 1
-    for (int r = tid / VECS; r < DL_C; r += B * step) {
-        int row[B];
-#pragma unroll
-        for (int i = 0; i < B; ++i) row[i] = rows[min(r + i * step, DL_C - 1)];
-#pragma unroll
-        for (int i = 0; i < B; ++i)
-            if (r + i * step < DL_C) copy(r + i * step, row[i]);
-    }
-}
-
 // The 64 rows of a token array into swizzled shared memory in bf16 planes, zero where there is
 // no token and from column `have` on.
 template <int COLS>
@@ -610,7 +753,7 @@ __device__ __forceinline__ void walk_load(unsigned char* dst, const __nv_bfloat1
     const int c = tid % vecs;
     const bool in = c * 8 < have;
     const __nv_bfloat16* at = in ? src + c * 8 : src;
-    copy_rows<vecs>(rows, tid, [&](int r, int row) {
+    copy_rows<vecs, DW_HELP>(rows, tid, [&](int r, int row) {
         const bool ok = in && row >= 0;
         copy16(dst + tc_swizzle(r, c), at + (ok ? row * tok : 0), ok);
     });
@@ -620,7 +763,7 @@ __device__ __forceinline__ void walk_load(unsigned char* dst, const float* src, 
 {
     constexpr int vecs = COLS / 8, plane = COLS / 64 * TC_TILE;
     const int c = tid % vecs;
-    copy_rows<vecs>(rows, tid, [&](int r, int row) {
+    copy_rows<vecs, DW_HELP>(rows, tid, [&](int r, int row) {
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f), z = x;
         if (row >= 0 && c * 8 < have) x = __ldg(reinterpret_cast<const float4*>(src + c * 8 + row * tok));
         if (row >= 0 && c * 8 + 4 < have) z = __ldg(reinterpret_cast<const float4*>(src + c * 8 + 4 + row * tok));
@@ -646,7 +789,7 @@ __device__ __forceinline__ void walk_load_values(T* dst, int pitch, const T* src
     const int c = tid % vecs * V;
     const bool in = c < have;
     const T* at = in ? src + c : src;
-    copy_rows<vecs>(rows, tid, [&](int r, int row) {
+    copy_rows<vecs, DW_HELP>(rows, tid, [&](int r, int row) {
         const bool ok = in && row >= 0;
         copy16(dst + r * pitch + c, at + (ok ? row * tok : 0), ok);
     });

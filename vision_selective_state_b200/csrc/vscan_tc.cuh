@@ -127,6 +127,15 @@ __device__ __forceinline__ void bulk_in(uint32_t smem, const void* gmem, uint32_
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(smem), "l"(gmem),
                  "r"(bytes), "r"(mbar) : "memory");
 }
+__device__ __forceinline__ void bulk_out(void* gmem, const void* smem, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n" ::"l"(gmem),
+                 "r"(static_cast<uint32_t>(__cvta_generic_to_shared(smem))), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_out_read()  // this thread's copies have read shared memory
+{
+    asm volatile("cp.async.bulk.commit_group;\ncp.async.bulk.wait_group.read 0;\n" ::: "memory");
+}
 __device__ __forceinline__ void mbar_arrive(uint32_t mbar)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(mbar) : "memory");
