@@ -191,15 +191,15 @@ DeltaParams make_params(const vscan_route* r, const vscan_delta_args* a)
     return p;
 }
 
-template <typename T, int DKP>
+template <typename T, int DKP, int PP>
 cudaError_t launch_prep(const DeltaParams& p, cudaStream_t stream)
 {
     if (p.slots == 0 || p.tokens == 0) return cudaSuccess;
     static int done[kAttrDevices];
-    const size_t smem = vscan::PrepShape<T, DKP>::smem(p.tplanes);
-    cudaError_t e = set_smem_once(vscan::delta_prep_kernel<T, DKP>, (int)smem, done, kAttrDevices);
+    constexpr size_t smem = vscan::PrepShape<T, DKP>::smem(PP);
+    cudaError_t e = set_smem_once(vscan::delta_prep_kernel<T, DKP, PP>, (int)smem, done, kAttrDevices);
     if (e != cudaSuccess) return e;
-    vscan::delta_prep_kernel<T, DKP><<<dim3((unsigned)p.slots, p.heads_v), vscan::DP_THREADS, smem, stream>>>(p);
+    vscan::delta_prep_kernel<T, DKP, PP><<<dim3((unsigned)p.slots, p.heads_v), vscan::DP_THREADS, smem, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -220,7 +220,7 @@ cudaError_t launch_scan(const DeltaParams& p, cudaStream_t stream)
 template <typename T, int DKP>
 cudaError_t run_forward(const DeltaParams& p, cudaStream_t stream)
 {
-    cudaError_t e = launch_prep<T, DKP>(p, stream);
+    cudaError_t e = launch_prep<T, DKP, vscan::WalkShape<T, DKP>::PP>(p, stream);
     if (e != cudaSuccess) return e;
     return launch_scan<T, DKP, false>(p, stream);
 }
@@ -231,7 +231,7 @@ cudaError_t run_backward(const DeltaParams& p, cudaStream_t stream)
     static int done_r[kAttrDevices], done_g[kAttrDevices];
     cudaError_t e;
     if (p.tokens > 0 && p.slots > 0) {
-        if ((e = launch_prep<T, DKP>(p, stream)) != cudaSuccess) return e;
+        if ((e = launch_prep<T, DKP, 3>(p, stream)) != cudaSuccess) return e;
         if ((e = launch_scan<T, DKP, true>(p, stream)) != cudaSuccess) return e;
     }
     constexpr size_t walk = vscan::WalkShape<T, DKP>::smem(3);

@@ -427,7 +427,7 @@ __device__ __forceinline__ void prep_load(__nv_bfloat16* dst, const float* src, 
     });
 }
 
-template <typename T, int DKP>
+template <typename T, int DKP, int PP>  // PP planes of P
 __global__ void __launch_bounds__(DP_THREADS) delta_prep_kernel(const DeltaParams p)
 {
     using Sh = PrepShape<T, DKP>;
@@ -439,10 +439,10 @@ __global__ void __launch_bounds__(DP_THREADS) delta_prep_kernel(const DeltaParam
     __nv_bfloat16* imgT = reinterpret_cast<__nv_bfloat16*>(vec + DL_VECS);
     float* Tr = reinterpret_cast<float*>(smem + Sh::image);                 // T_ij at [i][j mod 32]
     __nv_bfloat16* imgP = reinterpret_cast<__nv_bfloat16*>(smem + Sh::oP());
-    float* Lt = reinterpret_cast<float*>(smem + Sh::oL(p.tplanes));         // L_ij at [j][i]
-    float* Tt = reinterpret_cast<float*>(smem + Sh::oTt(p.tplanes));        // T_ij at [j][i mod 32]
-    float* M = reinterpret_cast<float*>(smem + Sh::oM(p.tplanes));
-    float2* G = reinterpret_cast<float2*>(smem + Sh::oGates(p.tplanes));    // running sum, rounded and rest
+    float* Lt = reinterpret_cast<float*>(smem + Sh::oL(PP));         // L_ij at [j][i]
+    float* Tt = reinterpret_cast<float*>(smem + Sh::oTt(PP));        // T_ij at [j][i mod 32]
+    float* M = reinterpret_cast<float*>(smem + Sh::oM(PP));
+    float2* G = reinterpret_cast<float2*>(smem + Sh::oGates(PP));    // running sum, rounded and rest
     float* beta = reinterpret_cast<float*>(G + DL_C);
     float *onward = beta + DL_C, *upto = onward + DL_C;                     // [64]; [4][64], row block 0 unused
     int* rows = reinterpret_cast<int*>(upto + 4 * DL_C);
@@ -539,56 +539,72 @@ __global__ void __launch_bounds__(DP_THREADS) delta_prep_kernel(const DeltaParam
     __syncthreads();  // K and Q are read: their place is the record's now
     {
         const int r0 = m0 + (lane >> 2), tc = (lane & 3) * 2;
-#pragma unroll
-        for (int nt = 0; nt < 8; ++nt) {
-            if (nt * 8 > m0 + 15) continue;
-            const bool within = nt * 8 >= m0;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int i = r0 + half * 8, j = nt * 8 + tc;
-                float v[2];
-                if (within) {
-                    const float2 gi = G[i];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float2 gj = G[j + e];
-                        // selected, not multiplied by zero: what lies above the diagonal is not looked at
-                        const float d = expf((gi.x - gj.x) + (gi.y - gj.y));
-                        v[e] = j + e < i + group ? d * acc[nt][half * 2 + e] : 0.f;
-                    }
+        float beta0, beta1;
+        // one pair of columns of one row, decayed: to P's planes, or to L
+        auto put = [&](int i, int half, int nt, float v0, float v1) {
+            const int j = nt * 8 + tc;
+            if (group) {
+                v0 *= p.scale;
+                v1 *= p.scale;
+                __nv_bfloat16* o = imgP + i * 64 + ((nt ^ (lane >> 2)) << 3) + tc;  // plane_at(i, j)
+                if (PP == 2) {  // rounded, both: what the product of the second terms would add is left out
+                    const uint32_t u = round_bf16(v0, v1);
+                    *reinterpret_cast<uint32_t*>(o) = u;
+                    *reinterpret_cast<uint32_t*>(o + DL_PLANE) =
+                        round_bf16(v0 - __uint_as_float(u << 16), v1 - __uint_as_float(u & 0xffff0000u));
                 } else {
-                    const float f = onward[i];
-                    const float2 h = *reinterpret_cast<const float2*>(upto + (m0 / 16) * DL_C + j);
-                    v[0] = f * h.x * acc[nt][half * 2];
-                    v[1] = f * h.y * acc[nt][half * 2 + 1];
+#pragma unroll
+                    for (int n = 0; n < 3; ++n) *reinterpret_cast<uint32_t*>(o + n * DL_PLANE) = split_bf16(v0, v1);
                 }
-                if (group) {
-                    v[0] *= p.scale;
-                    v[1] *= p.scale;
-                    const int at = i * 64 + ((nt ^ (lane >> 2)) << 3) + tc;  // plane_at(i, j)
-                    if (p.tplanes == 2) {  // rounded, both: what the product of the second terms would add is left out
-                        const uint32_t u = round_bf16(v[0], v[1]);
-                        *reinterpret_cast<uint32_t*>(imgP + at) = u;
-                        *reinterpret_cast<uint32_t*>(imgP + DL_PLANE + at) =
-                            round_bf16(v[0] - __uint_as_float(u << 16), v[1] - __uint_as_float(u & 0xffff0000u));
-                    } else {
-                        for (int n = 0; n < 3; ++n)
-                            *reinterpret_cast<uint32_t*>(imgP + n * DL_PLANE + at) = split_bf16(v[0], v[1]);
-                    }
-                } else {
-                    if (p.wL) *reinterpret_cast<float2*>(p.wL + rec * DL_PLANE + i * DL_C + j) = make_float2(v[0], v[1]);
-                    Lt[j * DP_LP + i] = beta[i] * v[0];
-                    Lt[(j + 1) * DP_LP + i] = beta[i] * v[1];
+            } else {
+                if (PP == 3 && p.wL) *reinterpret_cast<float2*>(p.wL + rec * DL_PLANE + i * DL_C + j) = make_float2(v0, v1);
+                const float be = half ? beta1 : beta0;
+                Lt[j * DP_LP + i] = be * v0;
+                Lt[(j + 1) * DP_LP + i] = be * v1;
+            }
+        };
+        beta0 = beta[r0];
+        beta1 = beta[r0 + 8];
+        const float f0 = onward[r0], f1 = onward[r0 + 8];
+        float diag[2][4];  // the block on the diagonal, moved to fixed registers: its code is there once
+#pragma unroll
+        for (int nt = 0; nt < 8; nt += 2) {
+            if (nt * 8 == m0) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    diag[0][e] = acc[nt][e];
+                    diag[1][e] = acc[nt + 1][e];
+                }
+            } else if (nt * 8 < m0) {
+#pragma unroll
+                for (int n = nt; n < nt + 2; ++n) {
+                    const float2 h = *reinterpret_cast<const float2*>(upto + (m0 / 16) * DL_C + n * 8 + tc);
+                    put(r0, 0, n, f0 * h.x * acc[n][0], f0 * h.y * acc[n][1]);
+                    put(r0 + 8, 1, n, f1 * h.x * acc[n][2], f1 * h.y * acc[n][3]);
                 }
             }
         }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int j = m0 + n * 8 + tc;
+            const float2 gj0 = G[j], gj1 = G[j + 1];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int i = r0 + half * 8;
+                const float2 gi = G[i];
+                // selected, not multiplied by zero: what lies above the diagonal is not looked at
+                const float d0 = expf((gi.x - gj0.x) + (gi.y - gj0.y)), d1 = expf((gi.x - gj1.x) + (gi.y - gj1.y));
+                put(i, half, m0 / 8 + n, j < i + group ? d0 * diag[n][half * 2] : 0.f,
+                    j + 1 < i + group ? d1 * diag[n][half * 2 + 1] : 0.f);
+            }
+        }
     }
-    unsigned char* out = p.wrec + rec * delta_record_bytes(p.tplanes);
+    unsigned char* out = p.wrec + rec * delta_record_bytes(PP);
     if (group) {
         tc_fence_smem();
         bar_sync(2, 128);
         if (tid == 128) {
-            bulk_out(out + Sh::image, imgP, p.tplanes * DL_PLANE * 2);
+            bulk_out(out + Sh::image, imgP, PP * DL_PLANE * 2);
             bulk_out_read();
         }
         return;
