@@ -238,52 +238,121 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaP
 }
 
 // ---- per-chunk gradients -------------------------------------------------------------
-// One CTA of eight warps per chunk and value head: four row blocks of 16 steps
-// times two halves of the key channels (of the steps j for E and M). The states
-// pass through shared memory in slabs of 64 value channels, split into bf16
-// terms once for all warps; dO, X's gradient and W go to registers directly.
+// One CTA of eight warps per chunk and value head. As in the walks the products stand
+// transposed, with the key channel as the row of the 128-row tile, so that a thread
+// holds half the steps of one key channel:
+//
+//   D1[dk][i | i] = S0 [dO | dV]^T      D2[i | i][j] = [dO | dV] W^T      D3[dk][j] = dS W^T
+//   (dq | dkr)^T = (scale e^G | -e^G) D1 + K^T [E | M]^T       dkc^T = e^{G_C - G} D3 + Q^T E + K^T M
+//
+// D1 .. D3 take both operands from shared memory, where everything float32 lies split in
+// bf16 planes, in slabs of 64 value channels; dO and dV share their tiles' rows, so that
+// they are one operand. E and M come from D2 through registers and back to shared memory,
+// [i][j], where the same tile is E (M) and its transpose; K^T and Q^T lie in tensor memory.
+// Bound by the products and by splitting the operands (S0 and dS are 32,768 values a chunk
+// and head at dk = dv = 128).
 template <typename T, int DKP>
 struct GradShape {
     static constexpr int NP = DeltaIo<T>::planes;
-    static constexpr int pitch = DKP + 8;
-    static constexpr int plane = DL_C * pitch;
-    static constexpr int splane = DKP * DL_TPITCH;  // a slab of a state: [DKP][64 value channels]
-    // K, Q; a slab of a state, E and M in three planes each; row sums
-    static constexpr size_t smem = (size_t)2 * NP * plane * 2 + (size_t)3 * splane * 2 + (size_t)6 * DL_C * DL_TPITCH * 2 +
-                                   6 * DL_C * 8 + (5 * DL_C + 16) * 4;
+    static constexpr int KB = DKP / 64;
+    static constexpr int plane = KB * TC_TILE;    // of K or Q; of a slab of a state: [DKP][64]
+    static constexpr int oK = 0, oQ = NP * plane, oS = 2 * NP * plane, oW = oS + 3 * plane;
+    static constexpr int oX = oW + 3 * TC_TILE;   // three pairs of tiles: dO's and dV's terms; later E's and M's
+    static constexpr int oEnd = oX + 6 * TC_TILE;
+    static constexpr int front = 7168;  // GradShared
+    static constexpr size_t smem = 1024 + front + oEnd;
 };
 
-__device__ __forceinline__ float2 load_pair(const float* p) { return __ldg(reinterpret_cast<const float2*>(p)); }
-__device__ __forceinline__ float2 load_pair(const __nv_bfloat16* p)
+struct GradShared {
+    unsigned long long done;
+    uint32_t tmem;
+    int dead;
+    alignas(16) int rows[DL_C];
+    double hrow[2][2][DL_C];  // row sums of H: E's and M's part, halves of the columns
+    double hcol[4][DL_C];     // column sums, by quarters of the 128 rows of D2
+    float U[4][DL_C], V[4][DL_C];  // by quarters of the key channels
+    float xw[DL_C];           // dX.w
+    float red[8];             // <dS, S0>
+};
+static_assert(sizeof(GradShared) <= 7168, "shared memory in front of the tiles");
+
+// Sum over the warp of each of 32 values; lane l gets the l-th.
+template <typename V>
+__device__ __forceinline__ V reduce_columns(V (&v)[32], int lane)
 {
-    const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(p));
-    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const V send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+    }
+    return v[0];
 }
-__device__ __forceinline__ void store_pair(float* p, float x, float y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); }
-__device__ __forceinline__ void store_pair(__nv_bfloat16* p, float x, float y)
+
+// Four values of a row into three planes of a swizzled tile (planes `plane` bytes apart).
+__device__ __forceinline__ void put_planes(unsigned char* dst, int plane, int r, int c, float4 x)
 {
-    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(x, y);
+    unsigned char* o = dst + r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2;
+#pragma unroll
+    for (int n = 0; n < 3; ++n) {
+        uint2 u;
+        u.x = split_bf16(x.x, x.y);
+        u.y = split_bf16(x.z, x.w);
+        *reinterpret_cast<uint2*>(o + n * plane) = u;
+    }
+}
+
+// 32 values of a row, NP bf16 terms, from a column of a [64][DKP] tile of K or Q.
+template <int NP, int DKP>
+__device__ __forceinline__ void column_of(const unsigned char* tile, int plane, int col, int first, float (&v)[32])
+{
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        float x = 0.f;
+        const unsigned char* at = tile + tc_swizzle(first + i, col >> 3) + (col & 7) * 2;
+#pragma unroll
+        for (int n = NP - 1; n >= 0; --n) x += __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(at + n * plane));
+        v[i] = x;
+    }
+}
+
+// Rows of K or Q into swizzled tiles, by all threads.
+template <int DKP>
+__device__ __forceinline__ void grad_load(unsigned char* dst, const __nv_bfloat16* src, long long tok, const int* rows, int have, int tid)
+{
+    constexpr int vecs = DKP / 8;
+    const int c = tid % vecs;
+    const bool in = c * 8 < have;
+    const __nv_bfloat16* at = in ? src + c * 8 : src;
+    copy_rows<vecs, 256>(rows, tid, [&](int r, int row) {
+        const bool ok = in && row >= 0;
+        copy16(dst + tc_swizzle(r, c), at + (ok ? row * tok : 0), ok);
+    });
+}
+template <int DKP>
+__device__ __forceinline__ void grad_load(unsigned char* dst, const float* src, long long tok, const int* rows, int have, int tid)
+{
+    constexpr int vecs = DKP / 4;
+    const int c = tid % vecs * 4;
+    copy_rows<vecs, 256>(rows, tid, [&](int r, int row) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (row >= 0 && c < have) x = __ldg(reinterpret_cast<const float4*>(src + c + row * tok));
+        put_planes(dst + (c >> 6) * TC_TILE, DKP / 64 * TC_TILE, r, c & 63, x);
+    });
 }
 
 template <typename T, int DKP>
-__global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaParams p)
+__global__ void __launch_bounds__(256, 1) delta_grad_kernel(const DeltaParams p)
 {
     using Sh = GradShape<T, DKP>;
-    constexpr int NP = Sh::NP, PITCH = Sh::pitch, PLANE = Sh::plane;
-    constexpr int NH = DKP / 16;  // 8-wide tiles in half of the key channels (2 at DKP = 32)
-    extern __shared__ __align__(16) unsigned char smem[];
-    double* hrow = reinterpret_cast<double*>(smem);  // [2 halves][64] row sums of H
-    double* hcol = hrow + 2 * DL_C;                  // [4 row blocks][64] column sums of H
-    float* rows = reinterpret_cast<float*>(hcol + 4 * DL_C);  // [2 halves][64] U, then V; [64] dX.w
-    float* red = rows + 5 * DL_C;                    // [8] <dS, S0>
-    __nv_bfloat16* K = reinterpret_cast<__nv_bfloat16*>(red + 16);
-    __nv_bfloat16* Q = K + NP * PLANE;
-    __nv_bfloat16* St = Q + NP * PLANE;
-    __nv_bfloat16* E = St + 3 * Sh::splane;
-    __nv_bfloat16* M = E + 3 * DL_C * DL_TPITCH;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tc = (lane & 3) * 2;
+    constexpr int NP = Sh::NP;
+    constexpr int c1 = 0, c2 = 128, c3 = 192, cKT = 256, cQT = cKT + NP * 32;  // tensor-memory columns
+    extern __shared__ unsigned char smem_raw[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = warp >> 2;
     const int head = blockIdx.y, hk = head / p.group;
-    const int m0 = (warp & 3) * 16, half = warp >> 2, n0 = half * (DKP / 2);
 
     int b;
     if (p.offsets) {
@@ -307,308 +376,255 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaParams p)
     const float* wdS = p.wdS + rec * p.dv * DKP;
     const float* wW = p.wW + rec * DL_C * p.dv;
     const float* wdX = p.wdX + rec * DL_C * p.dv;
-
-    load_tile(K, PITCH, PLANE, reinterpret_cast<const T*>(p.k) + img * p.k_img + (long long)hk * p.dk, p.k_tok, p, s, t0,
-              DKP, p.dk, tid, 256);
-    load_tile(Q, PITCH, PLANE, reinterpret_cast<const T*>(p.q) + img * p.q_img + (long long)hk * p.dk, p.q_tok, p, s, t0,
-              DKP, p.dk, tid, 256);
-    cp_async_commit();
-
-    // this thread's two rows of the chunk
-    const int r0 = m0 + gr, r1 = r0 + 8;
-    const int row0 = delta_row(p, s, t0 + r0), row1 = delta_row(p, s, t0 + r1);
     const T* dy = reinterpret_cast<const T*>(p.dy) + img * p.y_img + (long long)head * p.dv;
-    const float eG0 = vec[r0], eG1 = vec[r1], eD0 = vec[DL_C + r0], eD1 = vec[DL_C + r1];
-    const float beta0 = vec[2 * DL_C + r0], beta1 = vec[2 * DL_C + r1];
 
-    float dq[NH][4] = {}, dkr[NH][4] = {}, dkc[NH][4] = {}, e[4][4] = {}, m[4][4] = {};
-    float xw0 = 0.f, xw1 = 0.f, dots = 0.f;
-    for (int slab = 0; slab < p.dv; slab += DL_C) {
-        const int cols = min(DL_C, p.dv - slab);
-        auto load_state = [&](const float* src, const float* other) {
-            for (int i = tid; i < DKP * (DL_C / 4); i += 256) {
-                const int r = i / (DL_C / 4), cc = (i - r * (DL_C / 4)) * 4;
-                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (cc < cols) {
-                    x = __ldg(reinterpret_cast<const float4*>(src + (size_t)r * p.dv + slab + cc));
-                    if (other) {
-                        const float4 z = __ldg(reinterpret_cast<const float4*>(other + (size_t)r * p.dv + slab + cc));
-                        dots += x.x * z.x + x.y * z.y + x.z * z.z + x.w * z.w;
+    GradShared* sh = reinterpret_cast<GradShared*>(smem_raw);
+    unsigned char* tiles = smem_raw + Sh::front;
+    tiles += (1024 - (__cvta_generic_to_shared(tiles) & 1023)) % 1024;
+    const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(tiles));
+    const uint32_t done = static_cast<uint32_t>(__cvta_generic_to_shared(&sh->done));
+    if (warp == 0) tc_alloc(static_cast<uint32_t>(__cvta_generic_to_shared(&sh->tmem)));
+    if (tid == 0) {
+        mbar_init(done, 1);
+        sh->dead = 0;
+        mbar_fence_init();
+    }
+    if (tid < DL_C) {
+        sh->rows[tid] = delta_row(p, s, t0 + tid);
+        sh->xw[tid] = 0.f;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = sh->tmem, tl = tm + ((uint32_t)(warp & 3) << 21);
+    uint32_t phase = 0;
+
+    // K and Q
+    {
+        const T* k = reinterpret_cast<const T*>(p.k) + img * p.k_img + (long long)hk * p.dk;
+        const T* q = reinterpret_cast<const T*>(p.q) + img * p.q_img + (long long)hk * p.dk;
+        grad_load<DKP>(tiles + Sh::oK, k, p.k_tok, sh->rows, p.dk, tid);
+        grad_load<DKP>(tiles + Sh::oQ, q, p.q_tok, sh->rows, p.dk, tid);
+        cp_async_commit();
+    }
+    if (NP == 1)  // an exact dO has no second and third term
+        for (int i = tid; i < 2 * TC_TILE / 16; i += 256)
+            *reinterpret_cast<uint4*>(tiles + Sh::oX + 2 * TC_TILE + (i >> 9) * 2 * TC_TILE + (i & 511) * 16) = make_uint4(0, 0, 0, 0);
+
+    const uint64_t aS = tc_desc(at + Sh::oS), aX = tc_desc(at + Sh::oX), bW = tc_desc(at + Sh::oW);
+    float dots = 0.f;
+    for (int slab = 0; slab < p.dv; slab += 64) {
+        const int cols = min(64, p.dv - slab);
+        const bool more = slab > 0;
+        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+        // the state entering the chunk
+#pragma unroll 4
+        for (int i = tid; i < DKP * 16; i += 256) {
+            const int r = i >> 4, cc = (i & 15) * 4;
+            put_planes(tiles + Sh::oS, Sh::plane, r, cc,
+                       cc < cols ? __ldg(reinterpret_cast<const float4*>(wS + (size_t)r * p.dv + slab + cc)) : zero);
+        }
+        // W, dV and dO; a row's sixteen pieces are in half a warp
+#pragma unroll 2
+        for (int i = tid; i < DL_C * 16; i += 256) {
+            const int r = i >> 4, cc = (i & 15) * 4;
+            const bool in = cc < cols;
+            const float4 w = in ? __ldg(reinterpret_cast<const float4*>(wW + (size_t)r * p.dv + slab + cc)) : zero;
+            float4 x = in ? __ldg(reinterpret_cast<const float4*>(wdX + (size_t)r * p.dv + slab + cc)) : zero;
+            float xw = w.x * x.x + w.y * x.y + w.z * x.z + w.w * x.w;
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) xw += __shfl_xor_sync(0xffffffffu, xw, o);
+            if ((lane & 15) == 0) sh->xw[r] += xw;
+            put_planes(tiles + Sh::oW, TC_TILE, r, cc, w);
+            const float beta = vec[2 * DL_C + r];
+            x.x *= beta; x.y *= beta; x.z *= beta; x.w *= beta;
+            put_planes(tiles + Sh::oX + TC_TILE, 2 * TC_TILE, r, cc, x);
+            const int row = sh->rows[r];
+            unsigned char* o = tiles + Sh::oX + r * 128 + (((cc >> 3) ^ (r & 7)) << 4) + (cc & 7) * 2;
+            if constexpr (NP == 1) {
+                uint2 u = make_uint2(0, 0);
+                if (in && row >= 0) u = __ldg(reinterpret_cast<const uint2*>(dy + row * p.y_tok + slab + cc));
+                *reinterpret_cast<uint2*>(o) = u;
+            } else {
+                put_planes(tiles + Sh::oX, 2 * TC_TILE, r, cc,
+                           in && row >= 0 ? __ldg(reinterpret_cast<const float4*>(dy + row * p.y_tok + slab + cc)) : zero);
+            }
+        }
+        if (!more) cp_async_wait<0>();
+        tc_fence_smem();
+        __syncthreads();
+        if (warp == 0 && tc_elect()) {
+            tc_fence_after();
+            tc_product<3, 3, 2, 4, 0>(more, [&](int x, int y, int ks, bool add) {  // S0 [dO | dV]^T
+                const uint64_t a = aS + (x * Sh::plane + ks * 32) / 16;
+                if (NP == 1 && y > 0)
+                    tc_mma_ss(tm + c1 + 64, a, aX + ((2 * y + 1) * TC_TILE + ks * 32) / 16, tc_idesc(64, false), add);
+                else
+                    tc_mma_ss(tm + c1, a, aX + (2 * y * TC_TILE + ks * 32) / 16, tc_idesc(128, false), add);
+            });
+            tc_product<3, 3, 2, 4, 0>(more, [&](int x, int y, int ks, bool add) {  // [dO | dV] W^T
+                tc_mma_ss(tm + c2, aX + (2 * x * TC_TILE + ks * 32) / 16, bW + (y * TC_TILE + ks * 32) / 16, tc_idesc(64, false), add);
+            });
+            tc_commit(done);
+        }
+        __syncwarp();
+        mbar_wait(done, phase, &sh->dead);
+        phase ^= 1;
+        // the gradient of the state leaving it
+#pragma unroll 4
+        for (int i = tid; i < DKP * 16; i += 256) {
+            const int r = i >> 4, cc = (i & 15) * 4;
+            float4 x = zero;
+            if (cc < cols) {
+                x = __ldg(reinterpret_cast<const float4*>(wdS + (size_t)r * p.dv + slab + cc));
+                const float4 z = __ldg(reinterpret_cast<const float4*>(wS + (size_t)r * p.dv + slab + cc));
+                dots += x.x * z.x + x.y * z.y + x.z * z.z + x.w * z.w;
+            }
+            put_planes(tiles + Sh::oS, Sh::plane, r, cc, x);
+        }
+        tc_fence_smem();
+        __syncthreads();
+        if (warp == 0 && tc_elect()) {
+            tc_product<3, 3, 2, 4, 0>(more, [&](int x, int y, int ks, bool add) {  // dS W^T
+                tc_mma_ss(tm + c3, aS + (x * Sh::plane + ks * 32) / 16, bW + (y * TC_TILE + ks * 32) / 16, tc_idesc(64, false), add);
+            });
+            tc_commit(done);
+        }
+        __syncwarp();
+        mbar_wait(done, phase, &sh->dead);
+        phase ^= 1;
+    }
+    tc_fence_after();
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dots += __shfl_xor_sync(0xffffffffu, dots, o);
+    if (lane == 0) sh->red[warp] = dots;
+
+    // E and M: rows 0-63 of D2 and rows 64-127, columns 32 half .. of this thread's step i
+    {
+        const int part = (warp >> 1) & 1, i = (warp & 1) * 32 + lane, j0 = half * 32;
+        float e[32], f[32];
+        tc_ld32(tl + c2 + j0, e);
+        if (part == 0) {  // P, whole again
+            const __nv_bfloat16* wP = record_P(p, rec);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float z[8] = {};
+#pragma unroll
+                for (int n = 2; n >= 0; --n) {
+                    const uint4 u = __ldg(reinterpret_cast<const uint4*>(wP + n * DL_PLANE + plane_at(i, j0 + q * 8)));
+                    const uint32_t a[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        z[2 * k] += __uint_as_float(a[k] << 16);
+                        z[2 * k + 1] += __uint_as_float(a[k] & 0xffff0000u);
                     }
                 }
 #pragma unroll
-                for (int n = 0; n < 3; ++n) {
-                    uint2 u;
-                    u.x = split_bf16(x.x, x.y);
-                    u.y = split_bf16(x.z, x.w);
-                    *reinterpret_cast<uint2*>(St + n * Sh::splane + r * DL_TPITCH + cc) = u;
-                }
+                for (int k = 0; k < 8; ++k) f[q * 8 + k] = z[k];
             }
-        };
-        // rows r0, r1 at columns col and col + 8 of a [64][dv] array, as two C tiles
-        auto rows_of = [&](const float* src, int col, float (&lo)[4], float (&hi)[4]) {
-            const float2 z = make_float2(0.f, 0.f);
-            const float2 a = col < p.dv ? load_pair(src + (size_t)r0 * p.dv + col) : z;
-            const float2 bb = col < p.dv ? load_pair(src + (size_t)r1 * p.dv + col) : z;
-            const float2 cc = col + 8 < p.dv ? load_pair(src + (size_t)r0 * p.dv + col + 8) : z;
-            const float2 d = col + 8 < p.dv ? load_pair(src + (size_t)r1 * p.dv + col + 8) : z;
-            lo[0] = a.x; lo[1] = a.y; lo[2] = bb.x; lo[3] = bb.y;
-            hi[0] = cc.x; hi[1] = cc.y; hi[2] = d.x; hi[3] = d.y;
-        };
-        load_state(wS, nullptr);
-        cp_async_wait<0>();
-        __syncthreads();
-        for (int kt = 0; kt * 16 < cols; ++kt) {
-            const int col = slab + kt * 16 + tc;
-            float lo[4], hi[4], wl[4], wh[4];
-            Frag4 oa[NP], va[3];
-            {
-                const float2 z = make_float2(0.f, 0.f);
-                const float2 a = row0 >= 0 && col < p.dv ? load_pair(dy + row0 * p.y_tok + col) : z;
-                const float2 bb = row1 >= 0 && col < p.dv ? load_pair(dy + row1 * p.y_tok + col) : z;
-                const float2 cc = row0 >= 0 && col + 8 < p.dv ? load_pair(dy + row0 * p.y_tok + col + 8) : z;
-                const float2 d = row1 >= 0 && col + 8 < p.dv ? load_pair(dy + row1 * p.y_tok + col + 8) : z;
-                lo[0] = a.x; lo[1] = a.y; lo[2] = bb.x; lo[3] = bb.y;
-                hi[0] = cc.x; hi[1] = cc.y; hi[2] = d.x; hi[3] = d.y;
-            }
-            split_tiles<NP>(lo, hi, oa);
-            rows_of(wdX, col, lo, hi);
-            rows_of(wW, col, wl, wh);
+        } else {
+            const float4* wL = reinterpret_cast<const float4*>(p.wL + rec * DL_PLANE + i * DL_C + j0);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                xw0 += lo[i] * wl[i] + hi[i] * wh[i];
-                xw1 += lo[2 + i] * wl[2 + i] + hi[2 + i] * wh[2 + i];
-                lo[i] *= beta0; hi[i] *= beta0;
-                lo[2 + i] *= beta1; hi[2 + i] *= beta1;
-            }
-            split_tiles<3>(lo, hi, va);
-            // dO S0^T and dV S0^T
-#pragma unroll
-            for (int nt = 0; nt < NH; nt += 2) {
-                Frag4 f[3];
-#pragma unroll
-                for (int n = 0; n < 3; ++n) f[n] = load_b(St + n * Sh::splane, DL_TPITCH, n0 + nt * 8, kt * 16, lane);
-                mma_terms<NP, 3>(dq[nt], dq[nt + 1], oa, f);
-                mma_terms<3, 3>(dkr[nt], dkr[nt + 1], va, f);
-            }
-            // dO W^T and dV W^T, columns 32 half .. of the steps j up to this row block
-#pragma unroll
-            for (int nt = 0; nt < 4; nt += 2) {
-                const int j = half * 32 + nt * 8;
-                if (j <= m0 + 15) {
-                    float b0[4], b1[4];  // step j + gr, then j + 8 + gr: channels col.. and col + 8..
-                    const float2 z = make_float2(0.f, 0.f);
-                    const float2 w00 = col < p.dv ? load_pair(wW + (size_t)(j + gr) * p.dv + col) : z;
-                    const float2 w01 = col + 8 < p.dv ? load_pair(wW + (size_t)(j + gr) * p.dv + col + 8) : z;
-                    const float2 w10 = col < p.dv ? load_pair(wW + (size_t)(j + 8 + gr) * p.dv + col) : z;
-                    const float2 w11 = col + 8 < p.dv ? load_pair(wW + (size_t)(j + 8 + gr) * p.dv + col + 8) : z;
-                    b0[0] = w00.x; b0[1] = w00.y; b0[2] = w01.x; b0[3] = w01.y;
-                    b1[0] = w10.x; b1[1] = w10.y; b1[2] = w11.x; b1[3] = w11.y;
-                    Frag4 f[3];
-                    split_tiles<3>(b0, b1, f);
-                    mma_terms<NP, 3>(e[nt], e[nt + 1], oa, f);
-                    mma_terms<3, 3>(m[nt], m[nt + 1], va, f);
-                }
+            for (int q = 0; q < 8; ++q) {
+                const float4 u = __ldg(wL + q);
+                f[4 * q] = -u.x; f[4 * q + 1] = -u.y; f[4 * q + 2] = -u.z; f[4 * q + 3] = -u.w;
             }
         }
-        __syncthreads();
-        load_state(wdS, wS);
-        __syncthreads();
-        for (int kt = 0; kt * 16 < cols; ++kt) {  // W dS^T
-            float lo[4], hi[4];
-            rows_of(wW, slab + kt * 16 + tc, lo, hi);
-            Frag4 wa[3];
-            split_tiles<3>(lo, hi, wa);
+        tc_wait_ld();
+        // a step's own product carries no decay: it is no part of dg. Blocks above the diagonal
+        // hold nothing: selected, not multiplied by zero
+        double sum = 0.0, h[32];
 #pragma unroll
-            for (int nt = 0; nt < NH; nt += 2) {
-                Frag4 f[3];
-#pragma unroll
-                for (int n = 0; n < 3; ++n) f[n] = load_b(St + n * Sh::splane, DL_TPITCH, n0 + nt * 8, kt * 16, lane);
-                mma_terms<3, 3>(dkc[nt], dkc[nt + 1], wa, f);
-            }
+        for (int k = 0; k < 32; ++k) {
+            h[k] = j0 + k < i ? (double)(e[k] * f[k]) : 0.0;
+            sum += h[k];
         }
-        __syncthreads();
-    }
-
-    // the decays, and E and M to shared memory
-    auto k_at = [&](const __nv_bfloat16* t, int r, int col) {  // a pair of the tile's values
-        float2 x = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int n = NP - 1; n >= 0; --n) {
-            const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162*>(t + n * PLANE + r * PITCH + col);
-            x.x += __low2float(h);
-            x.y += __high2float(h);
-        }
-        return x;
-    };
-    float u0 = 0.f, u1 = 0.f, v0 = 0.f, v1 = 0.f;  // this thread's part of U and V of its rows
-#pragma unroll
-    for (int nt = 0; nt < NH; ++nt) {
-        const int col = n0 + nt * 8 + tc;
-        const float2 k0 = k_at(K, r0, col), k1 = k_at(K, r1, col), q0 = k_at(Q, r0, col), q1 = k_at(Q, r1, col);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            dq[nt][i] *= p.scale * (i < 2 ? eG0 : eG1);
-            dkr[nt][i] *= -(i < 2 ? eG0 : eG1);
-            dkc[nt][i] *= i < 2 ? eD0 : eD1;
-        }
-        u0 += q0.x * dq[nt][0] + q0.y * dq[nt][1] + k0.x * dkr[nt][0] + k0.y * dkr[nt][1];
-        u1 += q1.x * dq[nt][2] + q1.y * dq[nt][3] + k1.x * dkr[nt][2] + k1.y * dkr[nt][3];
-        v0 += k0.x * dkc[nt][0] + k0.y * dkc[nt][1];
-        v1 += k1.x * dkc[nt][2] + k1.y * dkc[nt][3];
-    }
-    {
+        sh->hrow[part][half][i] = sum;
+        sh->hcol[warp & 3][j0 + lane] = reduce_columns(h, lane);
         const double* G = reinterpret_cast<const double*>(vec + 4 * DL_C);
-        const double g0 = G[r0], g1 = G[r1];
-        const __nv_bfloat16* wP = record_P(p, rec);
-        const float* wL = p.wL + rec * DL_PLANE;
-        double hr0 = 0.0, hr1 = 0.0;
+        const double gi = G[i];
+        const float factor = part == 0 ? p.scale : -1.f;
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-            const int j = half * 32 + nt * 8 + tc;
-            float ev[4], mv[4];
-            double hc[2] = {0.0, 0.0};
-            if (j <= r1) {
-                float pv[4] = {}, lv[4];
-#pragma unroll
-                for (int n = 2; n >= 0; --n) {
-                    const float2 x = load_pair(wP + n * DL_PLANE + plane_at(r0, j));
-                    const float2 z = load_pair(wP + n * DL_PLANE + plane_at(r1, j));
-                    pv[0] += x.x; pv[1] += x.y; pv[2] += z.x; pv[3] += z.y;
-                }
-                const float2 l0 = load_pair(wL + r0 * DL_C + j), l1 = load_pair(wL + r1 * DL_C + j);
-                lv[0] = l0.x; lv[1] = l0.y; lv[2] = l1.x; lv[3] = l1.y;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = i < 2 ? r0 : r1, jj = j + (i & 1);
-                    // a step's own product carries no decay: it is no part of dg
-                    const float h = jj < r ? e[nt][i] * pv[i] - m[nt][i] * lv[i] : 0.f;
-                    (i < 2 ? hr0 : hr1) += (double)h;
-                    hc[i & 1] += (double)h;
-                }
-            }
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-                hc[0] += __shfl_xor_sync(0xffffffffu, hc[0], o);
-                hc[1] += __shfl_xor_sync(0xffffffffu, hc[1], o);
-            }
-            if (gr == 0) {
-                hcol[(warp & 3) * DL_C + j] = hc[0];
-                hcol[(warp & 3) * DL_C + j + 1] = hc[1];
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = i < 2 ? r0 : r1, jj = j + (i & 1);
-                const float d = jj <= r ? exp_diff((i < 2 ? g0 : g1) - G[jj]) : 0.f;
-                ev[i] = jj <= r ? p.scale * (d * e[nt][i]) : 0.f;
-                mv[i] = jj < r ? -d * m[nt][i] : 0.f;
-            }
-#pragma unroll
-            for (int n = 0; n < 3; ++n) {
-                __nv_bfloat16 *eo = E + n * DL_C * DL_TPITCH, *mo = M + n * DL_C * DL_TPITCH;
-                *reinterpret_cast<uint32_t*>(eo + r0 * DL_TPITCH + j) = split_bf16(ev[0], ev[1]);
-                *reinterpret_cast<uint32_t*>(eo + r1 * DL_TPITCH + j) = split_bf16(ev[2], ev[3]);
-                *reinterpret_cast<uint32_t*>(mo + r0 * DL_TPITCH + j) = split_bf16(mv[0], mv[1]);
-                *reinterpret_cast<uint32_t*>(mo + r1 * DL_TPITCH + j) = split_bf16(mv[2], mv[3]);
-            }
+        for (int k = 0; k < 32; ++k) {
+            const float d = j0 + k <= i ? exp_diff(gi - G[j0 + k]) : 0.f;
+            e[k] = j0 + k <= i - part ? factor * (d * e[k]) : 0.f;
         }
+        unsigned char* o = tiles + Sh::oX + part * TC_TILE;
 #pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-            hr0 += __shfl_xor_sync(0xffffffffu, hr0, o);
-            hr1 += __shfl_xor_sync(0xffffffffu, hr1, o);
-            u0 += __shfl_xor_sync(0xffffffffu, u0, o);
-            u1 += __shfl_xor_sync(0xffffffffu, u1, o);
-            v0 += __shfl_xor_sync(0xffffffffu, v0, o);
-            v1 += __shfl_xor_sync(0xffffffffu, v1, o);
-            xw0 += __shfl_xor_sync(0xffffffffu, xw0, o);
-            xw1 += __shfl_xor_sync(0xffffffffu, xw1, o);
-        }
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) dots += __shfl_xor_sync(0xffffffffu, dots, o);
-        if ((lane & 3) == 0) {
-            hrow[half * DL_C + r0] = hr0;
-            hrow[half * DL_C + r1] = hr1;
-            rows[half * DL_C + r0] = u0;
-            rows[half * DL_C + r1] = u1;
-            rows[(2 + half) * DL_C + r0] = v0;
-            rows[(2 + half) * DL_C + r1] = v1;
-            if (half == 0) {
-                rows[4 * DL_C + r0] = xw0;
-                rows[4 * DL_C + r1] = xw1;
-            }
-        }
-        if (lane == 0) red[warp] = dots;
+        for (int k = 0; k < 32; k += 4) put_planes(o, 2 * TC_TILE, i, j0 + k, make_float4(e[k], e[k + 1], e[k + 2], e[k + 3]));
     }
-    __syncthreads();
-    // dq += E K, dkr += M K over the steps up to the row block
-    for (int kt = 0; kt * 16 <= m0; ++kt) {
-        Frag4 ea[3], ma[3];
-#pragma unroll
-        for (int n = 0; n < 3; ++n) {
-            ea[n] = load_a(E + n * DL_C * DL_TPITCH, DL_TPITCH, m0, kt * 16, lane);
-            ma[n] = load_a(M + n * DL_C * DL_TPITCH, DL_TPITCH, m0, kt * 16, lane);
-        }
-#pragma unroll
-        for (int nt = 0; nt < NH; nt += 2) {
-            Frag4 f[NP];
-#pragma unroll
-            for (int n = 0; n < NP; ++n) f[n] = load_b_t(K + n * PLANE, PITCH, n0 + nt * 8, kt * 16, lane);
-            mma_terms<3, NP>(dq[nt], dq[nt + 1], ea, f);
-            mma_terms<3, NP>(dkr[nt], dkr[nt + 1], ma, f);
-        }
-    }
-    // dkc += E^T Q + M^T K over the steps from the row block on
-    for (int kt = m0 / 16; kt < 4; ++kt) {
-        Frag4 ea[3], ma[3];
-#pragma unroll
-        for (int n = 0; n < 3; ++n) {
-            ea[n] = load_a_t(E + n * DL_C * DL_TPITCH, DL_TPITCH, m0, kt * 16, lane);
-            ma[n] = load_a_t(M + n * DL_C * DL_TPITCH, DL_TPITCH, m0, kt * 16, lane);
-        }
-#pragma unroll
-        for (int nt = 0; nt < NH; nt += 2) {
-            Frag4 f[NP];
-#pragma unroll
-            for (int n = 0; n < NP; ++n) f[n] = load_b_t(Q + n * PLANE, PITCH, n0 + nt * 8, kt * 16, lane);
-            mma_terms<3, NP>(dkc[nt], dkc[nt + 1], ea, f);
-#pragma unroll
-            for (int n = 0; n < NP; ++n) f[n] = load_b_t(K + n * PLANE, PITCH, n0 + nt * 8, kt * 16, lane);
-            mma_terms<3, NP>(dkc[nt], dkc[nt + 1], ma, f);
-        }
-    }
-    // rows out
-#pragma unroll
-    for (int nt = 0; nt < NH; ++nt) {
-        const int col = n0 + nt * 8 + tc;
-        if (col < p.dk) {
+    // K^T (half 0) and Q^T: this thread's key channel, all steps
+    const int dk = (warp & 3) * 32 + lane;
+    const bool live = dk < DKP;  // DKP = 64: the upper two warps of each four idle here
+    {
+        const unsigned char* tile = tiles + (half ? Sh::oQ : Sh::oK);
+        const uint32_t to = tl + (half ? cQT : cKT);
+        if ((warp & 3) * 32 < DKP) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int row = h ? row1 : row0;
-                if (row < 0) continue;
-                const float x0 = dkr[nt][2 * h] + dkc[nt][2 * h], x1 = dkr[nt][2 * h + 1] + dkc[nt][2 * h + 1];
-                const size_t at = (size_t)(img * p.tokens + row);
-                if (p.wdq) {
-                    const size_t o = (at * p.heads_v + head) * p.dk + col;
-                    store_pair(p.wdq + o, dq[nt][2 * h], dq[nt][2 * h + 1]);
-                    store_pair(p.wdk + o, x0, x1);
-                } else {
-                    const size_t o = (at * p.heads_k + hk) * p.dk + col;
-                    if (p.dq) store_pair(reinterpret_cast<T*>(p.dq) + o, dq[nt][2 * h], dq[nt][2 * h + 1]);
-                    if (p.dkey) store_pair(reinterpret_cast<T*>(p.dkey) + o, x0, x1);
-                }
+                float x[32];
+                column_of<NP, DKP>(tile, Sh::plane, dk, h * 32, x);
+                put_terms<NP, NP == 3>(to + h * 16, 32, x);
             }
         }
     }
-    if (warp == 0) {  // dg, two steps a lane; then a, b and the sums for A and bias
+    // D1 and D3, scaled, and their part of dg
+    float dq[32], dkr[32], dkc[32];
+    tc_ld32(tl + c1 + half * 32, dq);
+    tc_ld32(tl + c1 + 64 + half * 32, dkr);
+    tc_ld32(tl + c3 + half * 32, dkc);
+    tc_wait_ld();
+    {
+        float u[32], x[32];
+        if (live) column_of<NP, DKP>(tiles + Sh::oQ, Sh::plane, dk, half * 32, x);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const float eG = vec[half * 32 + i];
+            dq[i] *= p.scale * eG;
+            dkr[i] *= -eG;
+            dkc[i] *= vec[DL_C + half * 32 + i];
+            u[i] = live ? x[i] * dq[i] : 0.f;
+        }
+        if (live) column_of<NP, DKP>(tiles + Sh::oK, Sh::plane, dk, half * 32, x);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) u[i] += live ? x[i] * dkr[i] : 0.f;
+        sh->U[warp & 3][half * 32 + lane] = reduce_columns(u, lane);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = live ? x[i] * dkc[i] : 0.f;
+        sh->V[warp & 3][half * 32 + lane] = reduce_columns(x, lane);
+    }
+    tc_wait_st();
+    tc_fence_smem();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0 && tc_elect()) {
+        tc_fence_after();
+        auto aK = [&](int x, int ks) { return tm + cKT + x * 32 + ks * 8; };
+        tc_product<NP, 3, 2, 4, 0>(false, [&](int x, int y, int ks, bool add) {  // K^T [E | M]^T
+            tc_mma(tm + c1, aK(x, ks), aX + (2 * y * TC_TILE + ks * 32) / 16, tc_idesc(128, false), add);
+        });
+        tc_product<NP, 3, 2, 4, 0>(false, [&](int x, int y, int ks, bool add) {  // Q^T E
+            tc_mma(tm + c3, tm + cQT + x * 32 + ks * 8, aX + (2 * y * TC_TILE + ks * 2048) / 16, tc_idesc(64, true), add);
+        });
+        tc_product<NP, 3, 2, 4, 0>(true, [&](int x, int y, int ks, bool add) {  // + K^T M
+            tc_mma(tm + c3, aK(x, ks), aX + ((2 * y + 1) * TC_TILE + ks * 2048) / 16, tc_idesc(64, true), add);
+        });
+        tc_commit(done);
+    }
+    __syncwarp();
+    if (warp == 7) {  // dg, two steps a lane; then a, b and the sums for A and bias
         double x[2], v[2], base = 0.0;
-        for (int w = 0; w < 8; ++w) base += (double)red[w];
+        for (int w = 0; w < 8; ++w) base += (double)sh->red[w];
         base *= (double)vec[3 * DL_C];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int r = 2 * lane + i;
-            x[i] = hrow[r] + hrow[DL_C + r] - (hcol[r] + hcol[DL_C + r] + hcol[2 * DL_C + r] + hcol[3 * DL_C + r]) +
-                   (double)rows[r] + (double)rows[DL_C + r];
-            v[i] = (double)rows[2 * DL_C + r] + (double)rows[3 * DL_C + r];
+            x[i] = v[i] = 0.0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                x[i] += sh->hrow[q >> 1][q & 1][r] - sh->hcol[q][r] + (double)sh->U[q][r];
+                v[i] += (double)sh->V[q][r];
+            }
         }
         double sum = x[0] + x[1], before = v[0] + v[1];
 #pragma unroll
@@ -625,7 +641,7 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaParams p)
         for (int i = 0; i < 2; ++i) {
             const int r = 2 * lane + i;
             if (t0 + r >= s.len) continue;
-            const int row = delta_row(p, s, t0 + r);
+            const int row = sh->rows[r];
             const float a = row >= 0 ? to_float(reinterpret_cast<const T*>(p.a)[img * p.a_img + row * p.a_tok + head]) : 0.f;
             const float da = (float)dg[i] * A * delta_sigmoid(a + bias);
             sA += dg[i] * (double)delta_softplus(a + bias);
@@ -634,7 +650,7 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaParams p)
                 const size_t o = (size_t)(img * p.tokens + row) * p.heads_v + head;
                 const float bb = to_float(reinterpret_cast<const T*>(p.b)[img * p.b_img + row * p.b_tok + head]);
                 if (p.da) store_elem(reinterpret_cast<T*>(p.da) + o, da);
-                if (p.db) store_elem(reinterpret_cast<T*>(p.db) + o, rows[4 * DL_C + r] * delta_sigmoid(-bb));
+                if (p.db) store_elem(reinterpret_cast<T*>(p.db) + o, sh->xw[r] * delta_sigmoid(-bb));
             }
         }
 #pragma unroll
@@ -647,6 +663,49 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaParams p)
             p.wpart[2 * rec + 1] = (float)sb;
         }
     }
+    mbar_wait(done, phase, &sh->dead);
+    tc_fence_after();
+    {
+        float x[32];
+        tc_ld32(tl + c1 + half * 32, x);
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) dq[i] += x[i];
+        tc_ld32(tl + c1 + 64 + half * 32, x);
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) dkr[i] += x[i];
+        tc_ld32(tl + c3 + half * 32, x);
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) dkc[i] += dkr[i] + x[i];
+    }
+    // rows out, over the states' place
+    const int* rows = sh->rows + half * 32;
+    const size_t first = (size_t)img * p.tokens;
+    if ((warp & 3) * 32 < DKP) {
+        const int have = p.dk - (warp & 3) * 32;
+        if (p.wdq) {
+            float* mine = reinterpret_cast<float*>(tiles + Sh::oS) + warp * (32 * 36) + lane;
+            const long long tok = (long long)p.heads_v * p.dk;
+            const size_t o = (first * p.heads_v + head) * p.dk + (warp & 3) * 32;
+            walk_store(p.wdq + o, tok, rows, mine, 36, have, lane, dq);
+            __syncwarp();
+            walk_store(p.wdk + o, tok, rows, mine, 36, have, lane, dkc);
+        } else {
+            constexpr int pitch = 32 + 16 / (int)sizeof(T);
+            T* mine = reinterpret_cast<T*>(tiles + Sh::oS) + warp * (32 * pitch) + lane;
+            const long long tok = (long long)p.heads_k * p.dk;
+            const size_t o = (first * p.heads_k + hk) * p.dk + (warp & 3) * 32;
+            if (p.dq) walk_store(reinterpret_cast<T*>(p.dq) + o, tok, rows, mine, pitch, have, lane, dq);
+            __syncwarp();
+            if (p.dkey) walk_store(reinterpret_cast<T*>(p.dkey) + o, tok, rows, mine, pitch, have, lane, dkc);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0 && p.status && sh->dead) atomicOr(p.status, DEV_STATUS_TIMEOUT);
+    if (warp == 0) tc_free(tm);
 }
 
 // dA and dbias of one head: its chunks' sums added in a fixed order.
