@@ -251,6 +251,10 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaP
 // [i][j], where the same tile is E (M) and its transpose; K^T and Q^T lie in tensor memory.
 // Bound by the products and by splitting the operands (S0 and dS are 32,768 values a chunk
 // and head at dk = dv = 128).
+template <typename T> struct GradRaw;  // four values of dy
+template <> struct GradRaw<__nv_bfloat16> { using type = uint2; };
+template <> struct GradRaw<float> { using type = float4; };
+
 template <typename T, int DKP>
 struct GradShape {
     static constexpr int NP = DeltaIo<T>::planes;
@@ -277,15 +281,14 @@ struct GradShared {
 static_assert(sizeof(GradShared) <= 7168, "shared memory in front of the tiles");
 
 // Sum over the warp of each of 32 values; lane l gets the l-th.
-template <typename V>
-__device__ __forceinline__ V reduce_columns(V (&v)[32], int lane)
+__device__ __forceinline__ float reduce_columns(float (&v)[32], int lane)
 {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const bool up = lane & o;
 #pragma unroll
         for (int i = 0; i < o; ++i) {
-            const V send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+            const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
             v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
         }
     }
@@ -389,15 +392,40 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(const DeltaParams p)
         sh->dead = 0;
         mbar_fence_init();
     }
-    if (tid < DL_C) {
-        sh->rows[tid] = delta_row(p, s, t0 + tid);
-        sh->xw[tid] = 0.f;
-    }
+    if (tid < DL_C) sh->rows[tid] = delta_row(p, s, t0 + tid);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = sh->tmem, tl = tm + ((uint32_t)(warp & 3) << 21);
     uint32_t phase = 0;
+
+    // A slab of everything else passes through registers, fetched ahead: a state is NS pieces of
+    // four channels a thread, W, dX and dO four each (a row's sixteen pieces are in half a warp).
+    constexpr int NS = DKP / 16;
+    using Raw = typename GradRaw<T>::type;
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int pr = tid >> 4, pc = (tid & 15) * 4;  // first row of this thread's pieces, 16 apart, and their columns
+    float4 s0[NS], ds[NS], w[4], x[4];
+    Raw o[4];
+    auto fetch_state = [&](float4 (&v)[NS], const float* src, int slab) {
+        const bool in = slab + pc < p.dv;
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+            v[i] = in ? __ldg(reinterpret_cast<const float4*>(src + (size_t)(pr + 16 * i) * p.dv + slab + pc)) : zero;
+    };
+    auto fetch = [&](int slab) {
+        fetch_state(s0, wS, slab);
+        const bool in = slab + pc < p.dv;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = pr + 16 * i, row = sh->rows[r];
+            w[i] = in ? __ldg(reinterpret_cast<const float4*>(wW + (size_t)r * p.dv + slab + pc)) : zero;
+            x[i] = in ? __ldg(reinterpret_cast<const float4*>(wdX + (size_t)r * p.dv + slab + pc)) : zero;
+            o[i] = Raw{};
+            if (in && row >= 0) o[i] = __ldg(reinterpret_cast<const Raw*>(dy + row * p.y_tok + slab + pc));
+        }
+    };
+    fetch(0);
 
     // K and Q
     {
@@ -413,42 +441,22 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(const DeltaParams p)
 
     const uint64_t aS = tc_desc(at + Sh::oS), aX = tc_desc(at + Sh::oX), bW = tc_desc(at + Sh::oW);
     float dots = 0.f;
+    float xw[4] = {};
     for (int slab = 0; slab < p.dv; slab += 64) {
-        const int cols = min(64, p.dv - slab);
         const bool more = slab > 0;
-        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-        // the state entering the chunk
-#pragma unroll 4
-        for (int i = tid; i < DKP * 16; i += 256) {
-            const int r = i >> 4, cc = (i & 15) * 4;
-            put_planes(tiles + Sh::oS, Sh::plane, r, cc,
-                       cc < cols ? __ldg(reinterpret_cast<const float4*>(wS + (size_t)r * p.dv + slab + cc)) : zero);
-        }
-        // W, dV and dO; a row's sixteen pieces are in half a warp
-#pragma unroll 2
-        for (int i = tid; i < DL_C * 16; i += 256) {
-            const int r = i >> 4, cc = (i & 15) * 4;
-            const bool in = cc < cols;
-            const float4 w = in ? __ldg(reinterpret_cast<const float4*>(wW + (size_t)r * p.dv + slab + cc)) : zero;
-            float4 x = in ? __ldg(reinterpret_cast<const float4*>(wdX + (size_t)r * p.dv + slab + cc)) : zero;
-            float xw = w.x * x.x + w.y * x.y + w.z * x.z + w.w * x.w;
 #pragma unroll
-            for (int o = 1; o < 16; o <<= 1) xw += __shfl_xor_sync(0xffffffffu, xw, o);
-            if ((lane & 15) == 0) sh->xw[r] += xw;
-            put_planes(tiles + Sh::oW, TC_TILE, r, cc, w);
+        for (int i = 0; i < NS; ++i) put_planes(tiles + Sh::oS, Sh::plane, pr + 16 * i, pc, s0[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = pr + 16 * i;
+            xw[i] += w[i].x * x[i].x + w[i].y * x[i].y + w[i].z * x[i].z + w[i].w * x[i].w;
+            put_planes(tiles + Sh::oW, TC_TILE, r, pc, w[i]);
             const float beta = vec[2 * DL_C + r];
-            x.x *= beta; x.y *= beta; x.z *= beta; x.w *= beta;
-            put_planes(tiles + Sh::oX + TC_TILE, 2 * TC_TILE, r, cc, x);
-            const int row = sh->rows[r];
-            unsigned char* o = tiles + Sh::oX + r * 128 + (((cc >> 3) ^ (r & 7)) << 4) + (cc & 7) * 2;
-            if constexpr (NP == 1) {
-                uint2 u = make_uint2(0, 0);
-                if (in && row >= 0) u = __ldg(reinterpret_cast<const uint2*>(dy + row * p.y_tok + slab + cc));
-                *reinterpret_cast<uint2*>(o) = u;
-            } else {
-                put_planes(tiles + Sh::oX, 2 * TC_TILE, r, cc,
-                           in && row >= 0 ? __ldg(reinterpret_cast<const float4*>(dy + row * p.y_tok + slab + cc)) : zero);
-            }
+            put_planes(tiles + Sh::oX + TC_TILE, 2 * TC_TILE, r, pc, make_float4(beta * x[i].x, beta * x[i].y, beta * x[i].z, beta * x[i].w));
+            if constexpr (NP == 1)
+                *reinterpret_cast<uint2*>(tiles + Sh::oX + r * 128 + (((pc >> 3) ^ (r & 7)) << 4) + (pc & 7) * 2) = o[i];
+            else
+                put_planes(tiles + Sh::oX, 2 * TC_TILE, r, pc, o[i]);
         }
         if (!more) cp_async_wait<0>();
         tc_fence_smem();
@@ -462,26 +470,20 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(const DeltaParams p)
                 else
                     tc_mma_ss(tm + c1, a, aX + (2 * y * TC_TILE + ks * 32) / 16, tc_idesc(128, false), add);
             });
+            tc_commit(done);
             tc_product<3, 3, 2, 4, 0>(more, [&](int x, int y, int ks, bool add) {  // [dO | dV] W^T
                 tc_mma_ss(tm + c2, aX + (2 * x * TC_TILE + ks * 32) / 16, bW + (y * TC_TILE + ks * 32) / 16, tc_idesc(64, false), add);
             });
-            tc_commit(done);
         }
         __syncwarp();
+        // the gradient of the state leaving the chunk, over the one entering it once D1 has read that
+        fetch_state(ds, wdS, slab);
+#pragma unroll
+        for (int i = 0; i < NS; ++i) dots += ds[i].x * s0[i].x + ds[i].y * s0[i].y + ds[i].z * s0[i].z + ds[i].w * s0[i].w;
         mbar_wait(done, phase, &sh->dead);
         phase ^= 1;
-        // the gradient of the state leaving it
-#pragma unroll 4
-        for (int i = tid; i < DKP * 16; i += 256) {
-            const int r = i >> 4, cc = (i & 15) * 4;
-            float4 x = zero;
-            if (cc < cols) {
-                x = __ldg(reinterpret_cast<const float4*>(wdS + (size_t)r * p.dv + slab + cc));
-                const float4 z = __ldg(reinterpret_cast<const float4*>(wS + (size_t)r * p.dv + slab + cc));
-                dots += x.x * z.x + x.y * z.y + x.z * z.z + x.w * z.w;
-            }
-            put_planes(tiles + Sh::oS, Sh::plane, r, cc, x);
-        }
+#pragma unroll
+        for (int i = 0; i < NS; ++i) put_planes(tiles + Sh::oS, Sh::plane, pr + 16 * i, pc, ds[i]);
         tc_fence_smem();
         __syncthreads();
         if (warp == 0 && tc_elect()) {
@@ -491,8 +493,15 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(const DeltaParams p)
             tc_commit(done);
         }
         __syncwarp();
+        if (slab + 64 < p.dv) fetch(slab + 64);
         mbar_wait(done, phase, &sh->dead);
         phase ^= 1;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int q = 1; q < 16; q <<= 1) xw[i] += __shfl_xor_sync(0xffffffffu, xw[i], q);
+        if ((lane & 15) == 0) sh->xw[pr + 16 * i] = xw[i];
     }
     tc_fence_after();
 #pragma unroll
@@ -533,14 +542,19 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(const DeltaParams p)
         tc_wait_ld();
         // a step's own product carries no decay: it is no part of dg. Blocks above the diagonal
         // hold nothing: selected, not multiplied by zero
-        double sum = 0.0, h[32];
+        double sum = 0.0, col = 0.0;
+        float* h = reinterpret_cast<float*>(tiles + Sh::oS) + warp * (32 * 33);  // this warp's [row][column], over the states
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
-            h[k] = j0 + k < i ? (double)(e[k] * f[k]) : 0.0;
-            sum += h[k];
+            f[k] = j0 + k < i ? e[k] * f[k] : 0.f;
+            h[lane * 33 + k] = f[k];
+            sum += (double)f[k];
         }
         sh->hrow[part][half][i] = sum;
-        sh->hcol[warp & 3][j0 + lane] = reduce_columns(h, lane);
+        __syncwarp();
+#pragma unroll 8
+        for (int k = 0; k < 32; ++k) col += (double)h[k * 33 + lane];
+        sh->hcol[warp & 3][j0 + lane] = col;
         const double* G = reinterpret_cast<const double*>(vec + 4 * DL_C);
         const double gi = G[i];
         const float factor = part == 0 ? p.scale : -1.f;
