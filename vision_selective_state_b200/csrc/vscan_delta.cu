@@ -241,7 +241,7 @@ cudaError_t run_backward(const DeltaParams& p, cudaStream_t stream)
     if (p.tokens > 0 && p.slots > 0) {
         constexpr size_t smem = vscan::GradShape<T, DKP>::smem;
         if ((e = set_smem_once(vscan::delta_grad_kernel<T, DKP>, (int)smem, done_g, kAttrDevices)) != cudaSuccess) return e;
-        vscan::delta_grad_kernel<T, DKP><<<dim3((unsigned)p.slots, p.heads_v), 256, smem, stream>>>(p);
+        vscan::delta_grad_kernel<T, DKP><<<dim3((unsigned)p.slots, p.heads_v), vscan::DG_THREADS, smem, stream>>>(p);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         if (p.wdq && (p.dq || p.dkey)) {
             const long long vecs = (long long)(p.offsets ? 1 : p.batch) * p.tokens * p.heads_k * (p.dk / 4);

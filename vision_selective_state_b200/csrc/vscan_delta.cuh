@@ -41,7 +41,7 @@ namespace vscan {
 constexpr int DL_C = 64;          // steps per chunk
 constexpr int DL_TPITCH = 72;     // shared-memory row pitch of a 64-wide bf16 tile: 144 bytes, an odd
                                   // multiple of 16, so ldmatrix rows fall into different banks
-// Floats per chunk in the workspace: e^{G_i}, e^{G_C - G_i}, beta_i, {e^{G_C}}, and G_i in float64.
+// Floats per chunk in the workspace: e^{G_i}, e^{G_C - G_i}, beta_i, {e^{G_C}}, and G_i rounded and the rest of it.
 constexpr int DL_VECS = 8 * DL_C;  // 2048 bytes, so that the planes behind them keep their alignment
 constexpr int DL_PLANE = DL_C * DL_C;
 
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(DP_THREADS) delta_prep_kernel(const DeltaParam
     float* Lt = reinterpret_cast<float*>(smem + Sh::oL(PP));         // L_ij at [j][i]
     float* Tt = reinterpret_cast<float*>(smem + Sh::oTt(PP));        // T_ij at [j][i mod 32]
     float* M = reinterpret_cast<float*>(smem + Sh::oM(PP));
-    float2* G = reinterpret_cast<float2*>(smem + Sh::oGates(PP));    // running sum, rounded and rest
+    float2* G = reinterpret_cast<float2*>(smem + Sh::oGates(PP));           // running sum, rounded and rest
     float* beta = reinterpret_cast<float*>(G + DL_C);
     float *onward = beta + DL_C, *upto = onward + DL_C;                     // [64]; [4][64], row block 0 unused
     int* rows = reinterpret_cast<int*>(upto + 4 * DL_C);
@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(DP_THREADS) delta_prep_kernel(const DeltaParam
             vec[2 * DL_C + r] = beta[r];
         }
         if (lane == 0) vec[3 * DL_C] = exp_diff(last);
-        *reinterpret_cast<double2*>(vec + 4 * DL_C + 4 * lane) = make_double2(g[0], g[1]);
+        *reinterpret_cast<float4*>(vec + 4 * DL_C + 4 * lane) = *reinterpret_cast<const float4*>(G + 2 * lane);
     }
     bar_sync(1, 128);
     if (lane < 16) {  // inverse of diagonal block m0, column `lane`

@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaP
 }
 
 // ---- per-chunk gradients -------------------------------------------------------------
-// One CTA of eight warps per chunk and value head. As in the walks the products stand
+// One CTA per chunk and value head. As in the walks the products stand
 // transposed, with the key channel as the row of the 128-row tile, so that a thread
 // holds half the steps of one key channel:
 //
@@ -251,6 +251,8 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaP
 // [i][j], where the same tile is E (M) and its transpose; K^T and Q^T lie in tensor memory.
 // Bound by the products and by splitting the operands (S0 and dS are 32,768 values a chunk
 // and head at dk = dv = 128).
+constexpr int DG_THREADS = 288;  // eight warps and one that issues the products
+
 template <typename T> struct GradRaw;  // four values of dy
 template <> struct GradRaw<__nv_bfloat16> { using type = uint2; };
 template <> struct GradRaw<float> { using type = float4; };
@@ -263,7 +265,7 @@ struct GradShape {
     static constexpr int oK = 0, oQ = NP * plane, oS = 2 * NP * plane, oW = oS + 3 * plane;
     static constexpr int oX = oW + 3 * TC_TILE;   // three pairs of tiles: dO's and dV's terms; later E's and M's
     static constexpr int oEnd = oX + 6 * TC_TILE;
-    static constexpr int front = 7168;  // GradShared
+    static constexpr int front = 9216;  // GradShared
     static constexpr size_t smem = 1024 + front + oEnd;
 };
 
@@ -277,8 +279,9 @@ struct GradShared {
     float U[4][DL_C], V[4][DL_C];  // by quarters of the key channels
     float xw[DL_C];           // dX.w
     float red[8];             // <dS, S0>
+    alignas(16) float vec[DL_VECS];
 };
-static_assert(sizeof(GradShared) <= 7168, "shared memory in front of the tiles");
+static_assert(sizeof(GradShared) <= 9216, "shared memory in front of the tiles");
 
 // Sum over the warp of each of 32 values; lane l gets the l-th.
 __device__ __forceinline__ float reduce_columns(float (&v)[32], int lane)
@@ -348,7 +351,7 @@ __device__ __forceinline__ void grad_load(unsigned char* dst, const float* src, 
 }
 
 template <typename T, int DKP>
-__global__ void __launch_bounds__(256, 1) delta_grad_kernel(const DeltaParams p)
+__global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaParams p)
 {
     using Sh = GradShape<T, DKP>;
     constexpr int NP = Sh::NP;
@@ -374,7 +377,6 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(const DeltaParams p)
     const int t0 = (int)c * DL_C;
     const long long img = delta_img(p, b);
     const size_t rec = (size_t)blockIdx.x * p.heads_v + head;
-    const float* vec = record_vec(p, rec);
     const float* wS = p.wS + rec * p.dv * DKP;
     const float* wdS = p.wdS + rec * p.dv * DKP;
     const float* wW = p.wW + rec * DL_C * p.dv;
@@ -393,11 +395,69 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(const DeltaParams p)
         mbar_fence_init();
     }
     if (tid < DL_C) sh->rows[tid] = delta_row(p, s, t0 + tid);
+    if (tid < DL_VECS / 4) reinterpret_cast<float4*>(sh->vec)[tid] = __ldg(reinterpret_cast<const float4*>(record_vec(p, rec)) + tid);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = sh->tmem, tl = tm + ((uint32_t)(warp & 3) << 21);
     uint32_t phase = 0;
+    const float* vec = sh->vec;
+    const uint64_t aS = tc_desc(at + Sh::oS), aX = tc_desc(at + Sh::oX), bW = tc_desc(at + Sh::oW);
+    auto aK = [&](int x, int ks) { return tm + cKT + x * 32 + ks * 8; };
+
+    if (warp == 8) {  // issues the products
+        for (int slab = 0; slab < p.dv; slab += 64) {
+            const bool more = slab > 0;
+            bar_sync(1, DG_THREADS);
+            tc_fence_after();
+            if (tc_elect()) {
+                tc_product<3, 3, 2, 4, 0>(more, [&](int x, int y, int ks, bool add) {  // S0 [dO | dV]^T
+                    const uint64_t a = aS + (x * Sh::plane + ks * 32) / 16;
+                    if (NP == 1 && y > 0)
+                        tc_mma_ss(tm + c1 + 64, a, aX + ((2 * y + 1) * TC_TILE + ks * 32) / 16, tc_idesc(64, false), add);
+                    else
+                        tc_mma_ss(tm + c1, a, aX + (2 * y * TC_TILE + ks * 32) / 16, tc_idesc(128, false), add);
+                });
+                tc_commit(done);
+                tc_product<3, 3, 2, 4, 0>(more, [&](int x, int y, int ks, bool add) {  // [dO | dV] W^T
+                    tc_mma_ss(tm + c2, aX + (2 * x * TC_TILE + ks * 32) / 16, bW + (y * TC_TILE + ks * 32) / 16, tc_idesc(64, false),
+                              add);
+                });
+            }
+            __syncwarp();
+            bar_sync(2, DG_THREADS);
+            tc_fence_after();
+            if (tc_elect()) {
+                tc_product<3, 3, 2, 4, 0>(more, [&](int x, int y, int ks, bool add) {  // dS W^T
+                    tc_mma_ss(tm + c3, aS + (x * Sh::plane + ks * 32) / 16, bW + (y * TC_TILE + ks * 32) / 16, tc_idesc(64, false), add);
+                });
+                tc_commit(done);
+            }
+            __syncwarp();
+        }
+        bar_sync(3, DG_THREADS);
+        tc_fence_after();
+        if (tc_elect()) {
+            tc_product<NP, 3, 2, 4, 0>(false, [&](int x, int y, int ks, bool add) {  // K^T [E | M]^T
+                tc_mma(tm + c1, aK(x, ks), aX + (2 * y * TC_TILE + ks * 32) / 16, tc_idesc(128, false), add);
+            });
+            tc_product<NP, 3, 2, 4, 0>(false, [&](int x, int y, int ks, bool add) {  // Q^T E
+                tc_mma(tm + c3, tm + cQT + x * 32 + ks * 8, aX + (2 * y * TC_TILE + ks * 2048) / 16, tc_idesc(64, true), add);
+            });
+            tc_product<NP, 3, 2, 4, 0>(true, [&](int x, int y, int ks, bool add) {  // + K^T M
+                tc_mma(tm + c3, aK(x, ks), aX + ((2 * y + 1) * TC_TILE + ks * 2048) / 16, tc_idesc(64, true), add);
+            });
+            tc_commit(done);
+        }
+        __syncwarp();
+        __syncthreads();
+        return;
+    }
+    auto ready = [&](int id) {  // this thread's part of the operands lies in shared (tensor) memory
+        tc_fence_smem();
+        tc_fence_before();
+        bar_arrive(id, DG_THREADS);
+    };
 
     // A slab of everything else passes through registers, fetched ahead: a state is NS pieces of
     // four channels a thread, W, dX and dO four each (a row's sixteen pieces are in half a warp).
@@ -439,7 +499,6 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(const DeltaParams p)
         for (int i = tid; i < 2 * TC_TILE / 16; i += 256)
             *reinterpret_cast<uint4*>(tiles + Sh::oX + 2 * TC_TILE + (i >> 9) * 2 * TC_TILE + (i & 511) * 16) = make_uint4(0, 0, 0, 0);
 
-    const uint64_t aS = tc_desc(at + Sh::oS), aX = tc_desc(at + Sh::oX), bW = tc_desc(at + Sh::oW);
     float dots = 0.f;
     float xw[4] = {};
     for (int slab = 0; slab < p.dv; slab += 64) {
@@ -459,23 +518,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(const DeltaParams p)
                 put_planes(tiles + Sh::oX, 2 * TC_TILE, r, pc, o[i]);
         }
         if (!more) cp_async_wait<0>();
-        tc_fence_smem();
-        __syncthreads();
-        if (warp == 0 && tc_elect()) {
-            tc_fence_after();
-            tc_product<3, 3, 2, 4, 0>(more, [&](int x, int y, int ks, bool add) {  // S0 [dO | dV]^T
-                const uint64_t a = aS + (x * Sh::plane + ks * 32) / 16;
-                if (NP == 1 && y > 0)
-                    tc_mma_ss(tm + c1 + 64, a, aX + ((2 * y + 1) * TC_TILE + ks * 32) / 16, tc_idesc(64, false), add);
-                else
-                    tc_mma_ss(tm + c1, a, aX + (2 * y * TC_TILE + ks * 32) / 16, tc_idesc(128, false), add);
-            });
-            tc_commit(done);
-            tc_product<3, 3, 2, 4, 0>(more, [&](int x, int y, int ks, bool add) {  // [dO | dV] W^T
-                tc_mma_ss(tm + c2, aX + (2 * x * TC_TILE + ks * 32) / 16, bW + (y * TC_TILE + ks * 32) / 16, tc_idesc(64, false), add);
-            });
-        }
-        __syncwarp();
+        ready(1);
         // the gradient of the state leaving the chunk, over the one entering it once D1 has read that
         fetch_state(ds, wdS, slab);
 #pragma unroll
@@ -484,15 +527,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(const DeltaParams p)
         phase ^= 1;
 #pragma unroll
         for (int i = 0; i < NS; ++i) put_planes(tiles + Sh::oS, Sh::plane, pr + 16 * i, pc, ds[i]);
-        tc_fence_smem();
-        __syncthreads();
-        if (warp == 0 && tc_elect()) {
-            tc_product<3, 3, 2, 4, 0>(more, [&](int x, int y, int ks, bool add) {  // dS W^T
-                tc_mma_ss(tm + c3, aS + (x * Sh::plane + ks * 32) / 16, bW + (y * TC_TILE + ks * 32) / 16, tc_idesc(64, false), add);
-            });
-            tc_commit(done);
-        }
-        __syncwarp();
+        ready(2);
         if (slab + 64 < p.dv) fetch(slab + 64);
         mbar_wait(done, phase, &sh->dead);
         phase ^= 1;
@@ -555,12 +590,13 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(const DeltaParams p)
 #pragma unroll 8
         for (int k = 0; k < 32; ++k) col += (double)h[k * 33 + lane];
         sh->hcol[warp & 3][j0 + lane] = col;
-        const double* G = reinterpret_cast<const double*>(vec + 4 * DL_C);
-        const double gi = G[i];
+        const float2* G = reinterpret_cast<const float2*>(vec + 4 * DL_C);
+        const float2 gi = G[i];
         const float factor = part == 0 ? p.scale : -1.f;
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
-            const float d = j0 + k <= i ? exp_diff(gi - G[j0 + k]) : 0.f;
+            const float2 gj = G[j0 + k];
+            const float d = expf((gi.x - gj.x) + (gi.y - gj.y));
             e[k] = j0 + k <= i - part ? factor * (d * e[k]) : 0.f;
         }
         unsigned char* o = tiles + Sh::oX + part * TC_TILE;
@@ -608,24 +644,8 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(const DeltaParams p)
         sh->V[warp & 3][half * 32 + lane] = reduce_columns(x, lane);
     }
     tc_wait_st();
-    tc_fence_smem();
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 0 && tc_elect()) {
-        tc_fence_after();
-        auto aK = [&](int x, int ks) { return tm + cKT + x * 32 + ks * 8; };
-        tc_product<NP, 3, 2, 4, 0>(false, [&](int x, int y, int ks, bool add) {  // K^T [E | M]^T
-            tc_mma(tm + c1, aK(x, ks), aX + (2 * y * TC_TILE + ks * 32) / 16, tc_idesc(128, false), add);
-        });
-        tc_product<NP, 3, 2, 4, 0>(false, [&](int x, int y, int ks, bool add) {  // Q^T E
-            tc_mma(tm + c3, tm + cQT + x * 32 + ks * 8, aX + (2 * y * TC_TILE + ks * 2048) / 16, tc_idesc(64, true), add);
-        });
-        tc_product<NP, 3, 2, 4, 0>(true, [&](int x, int y, int ks, bool add) {  // + K^T M
-            tc_mma(tm + c3, aK(x, ks), aX + ((2 * y + 1) * TC_TILE + ks * 2048) / 16, tc_idesc(64, true), add);
-        });
-        tc_commit(done);
-    }
-    __syncwarp();
+    ready(3);
+    bar_sync(4, 256);  // the parts of dg are there
     if (warp == 7) {  // dg, two steps a lane; then a, b and the sums for A and bias
         double x[2], v[2], base = 0.0;
         for (int w = 0; w < 8; ++w) base += (double)sh->red[w];
