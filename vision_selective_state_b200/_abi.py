@@ -5,6 +5,7 @@ fails loudly when the library has not been built; there is no fallback path.
 """
 import ctypes
 import os
+import struct
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libvscan.so")
@@ -170,6 +171,36 @@ def _load():
 
 
 lib = _load()
+
+
+class Call:
+    """A library function whose argument struct is passed as the bytes of a struct.Struct: filling
+    a ctypes structure field by field costs more than the smallest kernels take. `fields` is the
+    struct's format, which has to have the ctypes mirror's size."""
+
+    def __init__(self, name, fields, mirror, argtypes):
+        self.pack = struct.Struct(fields).pack
+        if struct.calcsize(fields) != ctypes.sizeof(mirror):
+            raise ImportError(f"{name}: {fields} is not the layout of {mirror.__name__}")
+        self.fn = ctypes.CDLL(LIB_PATH)[name]  # a function object of its own, with its own argument types
+        self.fn.argtypes, self.fn.restype = argtypes, ctypes.c_int32
+
+
+DELTA_FIELDS = "@8i11Q2f12q3Q"
+QKNORM_FIELDS = "@9if8Q2i8q"
+delta_workspace_size = Call("vscan_delta_workspace_size", DELTA_FIELDS, VscanDeltaArgs,
+                            [ctypes.c_void_p, ctypes.c_char_p, ctypes.c_void_p])
+delta_forward = Call("vscan_delta_forward", DELTA_FIELDS, VscanDeltaArgs, [ctypes.c_void_p, ctypes.c_char_p, ctypes.c_void_p])
+delta_backward_workspace_size = Call("vscan_delta_backward_workspace_size", DELTA_FIELDS, VscanDeltaArgs,
+                                     [ctypes.c_void_p, ctypes.c_char_p, ctypes.c_void_p])
+delta_backward = Call("vscan_delta_backward", DELTA_FIELDS, VscanDeltaArgs,
+                      [ctypes.c_void_p, ctypes.c_char_p, ctypes.c_void_p, ctypes.POINTER(VscanDeltaGrads), ctypes.c_void_p])
+delta_step = Call("vscan_delta_step", DELTA_FIELDS, VscanDeltaArgs, [ctypes.c_char_p, ctypes.c_void_p])
+qknorm_forward = Call("vscan_qknorm_forward", QKNORM_FIELDS, VscanQkNormArgs, [ctypes.c_char_p, ctypes.c_void_p])
+qknorm_backward_workspace_size = Call("vscan_qknorm_backward_workspace_size", QKNORM_FIELDS, VscanQkNormArgs,
+                                      [ctypes.c_char_p, ctypes.c_void_p])
+qknorm_backward = Call("vscan_qknorm_backward", QKNORM_FIELDS, VscanQkNormArgs,
+                       [ctypes.c_char_p, ctypes.POINTER(VscanQkNormGrads), ctypes.c_void_p])
 
 
 def check(status):

@@ -21,61 +21,78 @@ import ctypes
 
 import torch
 
-from ._abi import BF16, F32, ROUTES, VscanDeltaArgs, VscanDeltaGrads, check, lib
+from . import _abi
+from ._abi import BF16, F32, ROUTES, VscanDeltaGrads, check
 
-_CODES = {torch.float32: F32, torch.bfloat16: BF16}
+CODES = {torch.float32: F32, torch.bfloat16: BF16}
+_here = contextlib.nullcontext()
+_pack = _abi.delta_forward.pack
 
 
-def on_device(device):
+def on_device(index):
     """Context in which the runtime's current device is the tensors' own."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+    return _here if torch._C._cuda_getDevice() == index else torch.cuda.device(index)
 
 
-def stream_handle(stream, device, *scratch):
+def stream_handle(stream, index, *scratch):
     """The launch stream's handle. Tensors made here for a call on a stream other than the
     current one are marked as used there, so that their memory is not handed out again early."""
-    current = torch.cuda.current_stream(device)
+    current = torch._C._cuda_getCurrentRawStream(index)
     if stream is None:
-        return current.cuda_stream
-    if stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
-    if stream != current:
+        return current
+    if stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{index}")
+    if stream.cuda_stream != current:
         for t in scratch:
             if t is not None:
                 t.record_stream(stream)
     return stream.cuda_stream
 
 
-def check_tensor(name, t, shape, dtype, device):
-    if t.dtype != dtype:
+def check_tensor(name, t, shape, dtype, index):
+    """Raise for a tensor that is not what a call takes."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if tuple(t.shape) != tuple(shape):
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+    if t.shape != shape:
         raise ValueError(f"{name} shape {tuple(t.shape)} != {tuple(shape)}")
 
 
-def check_dense(name, t, shape, dtype, device):
-    check_tensor(name, t, shape, dtype, device)
+def check_dense(name, t, shape, dtype, index):
+    check_tensor(name, t, shape, dtype, index)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
-def head_strides(name, t):
-    """(token, image) strides of a [batch, tokens, heads, dim] tensor with contiguous heads."""
+def device_index(q):
+    """Index of the tensors' device, and the dtype's code."""
+    code = CODES.get(q.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {q.dtype} (float32 or bfloat16)")
+    index = q.get_device()
+    if index < 0:
+        raise ValueError("the tensors must be on a CUDA device")
+    return index, code
+
+
+def head_strides(name, t, dense):
+    """(token, image) strides of a [batch, tokens, heads, dim] tensor with contiguous heads;
+    a size-1 axis has no meaningful stride and takes the dense value (0)."""
+    if dense:
+        return 0, 0
     b, n, h, d = t.shape
     sb, sn, sh, sd = t.stride()
     if (sd != 1 and d > 1) or (sh != d and h > 1):
         raise ValueError(f"the heads of one token of {name} must be contiguous")
-    # a size-1 axis has no meaningful stride: take the dense value
     tok = sn if n > 1 else h * d
     return tok, (sb if b > 1 else n * tok)
 
 
-def _row_strides(name, t):
+def _row_strides(name, t, dense):
     """(token, image) strides of a [batch, tokens, heads] tensor with contiguous heads."""
+    if dense:
+        return 0, 0
     b, n, h = t.shape
     if t.stride(2) != 1 and h > 1:
         raise ValueError(f"the heads of one token of {name} must be contiguous")
@@ -83,47 +100,52 @@ def _row_strides(name, t):
     return tok, (t.stride(0) if b > 1 else n * tok)
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _marshal(q, k, v, a, b, A, bias, y, *, route, direction, seq_offsets, scale, beta_scale, initial_state,
-             final_state):
-    if q.dtype not in _CODES:
-        raise TypeError(f"unsupported dtype {q.dtype} (float32 or bfloat16)")
+def _fields(q, k, v, a, b, A, bias, y, direction, seq_offsets, scale, beta_scale, initial_state, final_state):
+    """(device index, fields of vscan_delta_args up to the strides)."""
+    index, code = device_index(q)
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q and k are [batch, tokens, heads_k, dim_k], v is [batch, tokens, heads_v, dim_v]")
-    dev = q.device
-    if dev.type != "cuda":
-        raise ValueError("the tensors must be on a CUDA device")
-    batch, tokens, hk, dk = q.shape
+    dtype, shape = q.dtype, q.shape
+    batch, tokens, hk, dk = shape
     hv, dv = v.shape[2:]
-    check_tensor("k", k, q.shape, q.dtype, dev)
-    check_tensor("v", v, (batch, tokens, hv, dv), q.dtype, dev)
-    check_tensor("a", a, (batch, tokens, hv), q.dtype, dev)
-    check_tensor("b", b, (batch, tokens, hv), q.dtype, dev)
-    check_tensor("y", y, v.shape, q.dtype, dev)
-    check_dense("A", A, (hv,), torch.float32, dev)
+    heads = (batch, tokens, hv)
+    check_tensor("k", k, shape, dtype, index)
+    check_tensor("v", v, (batch, tokens, hv, dv), dtype, index)
+    check_tensor("a", a, heads, dtype, index)
+    check_tensor("b", b, heads, dtype, index)
+    check_tensor("y", y, v.shape, dtype, index)
+    check_dense("A", A, (hv,), torch.float32, index)
     if bias is not None:
-        check_dense("bias", bias, (hv,), torch.float32, dev)
+        check_dense("bias", bias, (hv,), torch.float32, index)
     rows = batch
     if seq_offsets is not None:
         if batch != 1:
             raise ValueError("packed sequences have one row of tokens: batch must be 1")
         if seq_offsets.dim() != 1 or seq_offsets.numel() < 1:
             raise ValueError("seq_offsets must hold one more element than there are sequences")
-        check_dense("seq_offsets", seq_offsets, seq_offsets.shape, torch.int32, dev)
+        check_dense("seq_offsets", seq_offsets, seq_offsets.shape, torch.int32, index)
         rows = seq_offsets.numel() - 1
-    for name, t in (("initial_state", initial_state), ("final_state", final_state)):
-        if t is not None:
-            check_dense(name, t, (rows, hv, dk, dv), torch.float32, dev)
-    return VscanDeltaArgs(
-        rows, tokens, hk, hv, dk, dv, _CODES[q.dtype], int(direction),
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), a.data_ptr(), b.data_ptr(), y.data_ptr(), A.data_ptr(), _ptr(bias),
-        _ptr(initial_state), _ptr(final_state), _ptr(seq_offsets),
-        dk ** -0.5 if scale is None else float(scale), float(beta_scale),
-        *head_strides("q", q), *head_strides("k", k), *head_strides("v", v), *_row_strides("a", a),
-        *_row_strides("b", b), *head_strides("y", y))
+    if initial_state is not None:
+        check_dense("initial_state", initial_state, (rows, hv, dk, dv), torch.float32, index)
+    if final_state is not None:
+        check_dense("final_state", final_state, (rows, hv, dk, dv), torch.float32, index)
+    return index, (
+        rows, tokens, hk, hv, dk, dv, code, direction,
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), a.data_ptr(), b.data_ptr(), y.data_ptr(), A.data_ptr(),
+        0 if bias is None else bias.data_ptr(), 0 if initial_state is None else initial_state.data_ptr(),
+        0 if final_state is None else final_state.data_ptr(), 0 if seq_offsets is None else seq_offsets.data_ptr(),
+        dk ** -0.5 if scale is None else scale, beta_scale,
+        *head_strides("q", q, q.is_contiguous()), *head_strides("k", k, k.is_contiguous()),
+        *head_strides("v", v, v.is_contiguous()), *_row_strides("a", a, a.is_contiguous()),
+        *_row_strides("b", b, b.is_contiguous()), *head_strides("y", y, y.is_contiguous()))
+
+
+def _status(status, index):
+    if status is None:
+        return 0
+    if status.dtype is not torch.int32 or status.numel() < 1 or status.get_device() != index:
+        raise TypeError(f"status must be an int32 tensor on cuda:{index}")
+    return status.data_ptr()
 
 
 def _route_handle(route):
@@ -135,38 +157,43 @@ def _partial(route, seq_offsets):
     return seq_offsets is not None or (route is not None and route.kind == ROUTES["atrous2"])
 
 
-def _state_rows(q, seq_offsets):
-    return q.shape[0] if seq_offsets is None else seq_offsets.numel() - 1
+def _state_shape(q, v, seq_offsets):
+    return (q.shape[0] if seq_offsets is None else seq_offsets.numel() - 1, v.shape[2], q.shape[3], v.shape[3])
+
+
+def _scratch(query, handle, fields, index):
+    need = ctypes.c_uint64()
+    check(query.fn(handle, _pack(*fields, 0, 0, 0), ctypes.byref(need)))
+    return torch.empty(need.value, dtype=torch.uint8, device=f"cuda:{index}")
 
 
 def delta_forward(q, k, v, a, b, A, bias=None, *, route=None, direction=0, seq_offsets=None, scale=None,
-                  beta_scale=1.0, initial_state=None, final_state=False, out=None, workspace=None, stream=None):
+                  beta_scale=1.0, initial_state=None, final_state=False, out=None, workspace=None, stream=None,
+                  status=None):
     """Gated delta rule over every token (vscan_delta_forward). Returns y, or (y, final state).
 
     route, direction: visit the tokens in the order of one direction of a BIDIR, CROSS4 or
     ATROUS2 Route (an ATROUS2 direction writes its own group's tokens only); without a route,
     first to last. seq_offsets: int32 [n + 1] on the device for n packed sequences in one row
     of tokens (batch 1); rows outside every sequence are left as they are. Rows that a call
-    leaves are 0 in an output made here. scale: dim_k ** -0.5 if None. final_state: True, or a tensor to write
-    the state after the last token to (initial_state itself is allowed).
+    leaves are 0 in an output made here. scale: dim_k ** -0.5 if None. final_state: True, or a
+    tensor to write the state after the last token to (initial_state itself is allowed).
+    status: as in forward().
     """
     if out is None:
         out = (torch.zeros if _partial(route, seq_offsets) else torch.empty)(v.shape, dtype=v.dtype, device=v.device)
     if final_state is True:
-        final_state = torch.empty((_state_rows(q, seq_offsets), v.shape[2], q.shape[3], v.shape[3]),
-                                  dtype=torch.float32, device=q.device)
+        final_state = torch.empty(_state_shape(q, v, seq_offsets), dtype=torch.float32, device=q.device)
     elif final_state is False:
         final_state = None
-    args = _marshal(q, k, v, a, b, A, bias, out, route=route, direction=direction, seq_offsets=seq_offsets, scale=scale,
-                    beta_scale=beta_scale, initial_state=initial_state, final_state=final_state)
-    handle, ref = _route_handle(route), ctypes.byref(args)
+    index, fields = _fields(q, k, v, a, b, A, bias, out, direction, seq_offsets, scale, beta_scale, initial_state,
+                            final_state)
+    handle = _route_handle(route)
     if workspace is None:
-        need = ctypes.c_uint64()
-        check(lib.vscan_delta_workspace_size(handle, ref, ctypes.byref(need)))
-        workspace = torch.empty(need.value, dtype=torch.uint8, device=q.device)
-    args.workspace, args.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    with on_device(q.device):
-        check(lib.vscan_delta_forward(handle, ref, stream_handle(stream, q.device, out, final_state, workspace)))
+        workspace = _scratch(_abi.delta_workspace_size, handle, fields, index)
+    args = _pack(*fields, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _status(status, index))
+    with on_device(index):
+        check(_abi.delta_forward.fn(handle, args, stream_handle(stream, index, out, final_state, workspace)))
     return out if final_state is None else (out, final_state)
 
 
@@ -174,7 +201,8 @@ GRADIENTS = ("dq", "dk", "dv", "da", "db", "dA", "dbias", "d_initial_state")
 
 
 def delta_backward(q, k, v, a, b, A, bias=None, *, dy, route=None, direction=0, seq_offsets=None, scale=None,
-                   beta_scale=1.0, initial_state=None, d_final_state=None, want=None, workspace=None, stream=None):
+                   beta_scale=1.0, initial_state=None, d_final_state=None, want=None, workspace=None, stream=None,
+                   status=None):
     """Gradients of delta_forward (vscan_delta_backward) in a dict, from its arguments, dy = dL/dy
     and d_final_state = dL/d(final state).
 
@@ -182,30 +210,27 @@ def delta_backward(q, k, v, a, b, A, bias=None, *, dy, route=None, direction=0, 
     d_initial_state (float32). `want` limits the keys computed. Tokens that no step visits get
     zeros. Equal calls give equal bits.
     """
-    args = _marshal(q, k, v, a, b, A, bias, dy, route=route, direction=direction, seq_offsets=seq_offsets, scale=scale,
-                    beta_scale=beta_scale, initial_state=initial_state, final_state=None)
-    dev, grads, out = q.device, VscanDeltaGrads(), {}
-    like = {"dq": q, "dk": k, "dv": v, "da": a, "db": b, "dA": A, "dbias": A, "d_initial_state": initial_state}
+    index, fields = _fields(q, k, v, a, b, A, bias, dy, direction, seq_offsets, scale, beta_scale, initial_state, None)
     if want is not None and not set(want) <= set(GRADIENTS):
         raise ValueError(f"want holds unknown gradients {sorted(set(want) - set(GRADIENTS))}")
+    grads, out = VscanDeltaGrads(), {}
+    like = {"dq": q, "dk": k, "dv": v, "da": a, "db": b, "dA": A, "dbias": A, "d_initial_state": initial_state}
     for name in GRADIENTS if want is None else want:
         t = like[name]
         if t is not None:
-            out[name] = torch.empty(t.shape, dtype=t.dtype, device=dev)
+            out[name] = torch.empty(t.shape, dtype=t.dtype, device=t.device)
             setattr(grads, name, out[name].data_ptr())
     if d_final_state is not None:
-        check_dense("d_final_state", d_final_state, (_state_rows(q, seq_offsets), *v.shape[2:3], q.shape[3], v.shape[3]),
-                    torch.float32, dev)
+        check_dense("d_final_state", d_final_state, _state_shape(q, v, seq_offsets), torch.float32, index)
         grads.d_final_state = d_final_state.data_ptr()
-    handle, ref = _route_handle(route), ctypes.byref(args)
+    handle = _route_handle(route)
     if workspace is None:
-        need = ctypes.c_uint64()
-        check(lib.vscan_delta_backward_workspace_size(handle, ref, ctypes.byref(need)))
-        workspace = torch.empty(need.value, dtype=torch.uint8, device=dev)
+        workspace = _scratch(_abi.delta_backward_workspace_size, handle, fields, index)
     grads.workspace, grads.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    with on_device(dev):
-        check(lib.vscan_delta_backward(handle, ref, dy.data_ptr(), ctypes.byref(grads),
-                                       stream_handle(stream, dev, workspace, *out.values())))
+    args = _pack(*fields, 0, 0, _status(status, index))
+    with on_device(index):
+        check(_abi.delta_backward.fn(handle, args, dy.data_ptr(), ctypes.byref(grads),
+                                     stream_handle(stream, index, workspace, *out.values())))
     return out
 
 
@@ -216,13 +241,38 @@ def delta_step(q, k, v, a, b, A, bias=None, *, state, state_out=None, scale=None
     q, k: [batch, heads_k, dim_k]; v, y: [batch, heads_v, dim_v]; a, b: [batch, heads_v].
     The new state goes to state_out, or in place to state.
     """
+    index, code = device_index(q)
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q and k are [batch, heads_k, dim_k], v is [batch, heads_v, dim_v]")
+    dtype, shape, wide = q.dtype, q.shape, v.shape
+    batch, hk, dk = shape
+    hv, dv = wide[1:]
     if out is None:
-        out = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+        out = torch.empty(wide, dtype=dtype, device=v.device)
     if state_out is None:
         state_out = state
-    args = _marshal(q.unsqueeze(1), k.unsqueeze(1), v.unsqueeze(1), a.unsqueeze(1), b.unsqueeze(1), A, bias,
-                    out.unsqueeze(1), route=None, direction=0, seq_offsets=None, scale=scale, beta_scale=beta_scale,
-                    initial_state=state, final_state=state_out)
-    with on_device(q.device):
-        check(lib.vscan_delta_step(ctypes.byref(args), stream_handle(stream, q.device, out, state_out)))
+    check_tensor("k", k, shape, dtype, index)
+    check_tensor("v", v, (batch, hv, dv), dtype, index)
+    check_tensor("a", a, (batch, hv), dtype, index)
+    check_tensor("b", b, (batch, hv), dtype, index)
+    check_tensor("y", out, wide, dtype, index)
+    check_dense("A", A, (hv,), torch.float32, index)
+    if bias is not None:
+        check_dense("bias", bias, (hv,), torch.float32, index)
+    check_dense("state", state, (batch, hv, dk, dv), torch.float32, index)
+    if state_out is not state:
+        check_dense("state_out", state_out, (batch, hv, dk, dv), torch.float32, index)
+    strides = []
+    for name, t in (("q", q), ("k", k), ("v", v), ("a", a), ("b", b), ("y", out)):
+        if t.is_contiguous():
+            strides += (0, 0)
+        elif t.dim() == 3:
+            strides += (0, head_strides(name, t.unsqueeze(1), False)[1])
+        else:
+            strides += (0, _row_strides(name, t.unsqueeze(1), False)[1])
+    args = _pack(batch, 1, hk, hv, dk, dv, code, 0, q.data_ptr(), k.data_ptr(), v.data_ptr(), a.data_ptr(), b.data_ptr(),
+                 out.data_ptr(), A.data_ptr(), 0 if bias is None else bias.data_ptr(), state.data_ptr(),
+                 state_out.data_ptr(), 0, dk ** -0.5 if scale is None else scale, beta_scale, *strides, 0, 0, 0)
+    with on_device(index):
+        check(_abi.delta_step.fn(args, stream_handle(stream, index, out)))
     return out, state_out

@@ -14,48 +14,51 @@ import ctypes
 
 import torch
 
-from ._abi import VscanQkNormArgs, VscanQkNormGrads, check, lib
-from .delta import _CODES, check_dense, check_tensor, head_strides, on_device, stream_handle
+from . import _abi
+from ._abi import VscanQkNormGrads, check
+from .delta import check_dense, check_tensor, device_index, head_strides, on_device, stream_handle
 
 NORMS = {"l2": 0, "rms": 1}
 
 
 def _marshal(q, k, wq, wk, yq, yk, norm, eps, inv_freq, positions):
-    if q.dtype not in _CODES:
-        raise TypeError(f"unsupported dtype {q.dtype} (float32 or bfloat16)")
+    """(device index, packed vscan_qknorm_args)."""
+    index, code = device_index(q)
     if norm not in NORMS:
         raise ValueError(f"norm must be one of {sorted(NORMS)}")
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q and k are [batch, tokens, heads, dim]")
-    dev = q.device
-    if dev.type != "cuda":
-        raise ValueError("the tensors must be on a CUDA device")
+    dtype = q.dtype
     batch, tokens, hq, d = q.shape
     hk = k.shape[2]
-    check_tensor("k", k, (batch, tokens, hk, d), q.dtype, dev)
-    for name, t in (("wq", wq), ("wk", wk)):
-        if t is not None:
-            check_dense(name, t, (d,), torch.float32, dev)
+    check_tensor("k", k, (batch, tokens, hk, d), dtype, index)
+    check_tensor("yq (dyq)", yq, q.shape, dtype, index)
+    check_tensor("yk (dyk)", yk, k.shape, dtype, index)
+    if wq is not None:
+        check_dense("wq", wq, (d,), torch.float32, index)
+    if wk is not None:
+        check_dense("wk", wk, (d,), torch.float32, index)
     pairs, axes, per_image = 0, 1, 0
     if (inv_freq is None) != (positions is None):
         raise ValueError("inv_freq and positions belong together")
     if inv_freq is not None:
         pairs = inv_freq.numel()
-        check_dense("inv_freq", inv_freq, (pairs,), torch.float32, dev)
-        shape = tuple(positions.shape)
+        check_dense("inv_freq", inv_freq, (pairs,), torch.float32, index)
+        shape = positions.shape
         for lead in ((tokens,), (batch, tokens)):
             if shape == lead or (shape[:-1] == lead and shape[-1] in (1, 2)):
                 axes, per_image = (1 if shape == lead else shape[-1]), len(lead) - 1
                 break
         else:
-            raise ValueError(f"positions shape {shape} is not [tokens(, axes)] or [batch, tokens(, axes)]")
-        check_dense("positions", positions, shape, torch.int32, dev)
-    return VscanQkNormArgs(
-        batch, tokens, hq, hk, d, pairs, axes, _CODES[q.dtype], NORMS[norm], float(eps),
-        q.data_ptr(), k.data_ptr(), yq.data_ptr(), yk.data_ptr(), None if wq is None else wq.data_ptr(),
-        None if wk is None else wk.data_ptr(), inv_freq.data_ptr() if pairs else None,
-        positions.data_ptr() if pairs else None, per_image, 0,
-        *head_strides("q", q), *head_strides("k", k), *head_strides("yq", yq), *head_strides("yk", yk))
+            raise ValueError(f"positions shape {tuple(shape)} is not [tokens(, axes)] or [batch, tokens(, axes)]")
+        check_dense("positions", positions, shape, torch.int32, index)
+    return index, _abi.qknorm_forward.pack(
+        batch, tokens, hq, hk, d, pairs, axes, code, NORMS[norm], eps,
+        q.data_ptr(), k.data_ptr(), yq.data_ptr(), yk.data_ptr(), 0 if wq is None else wq.data_ptr(),
+        0 if wk is None else wk.data_ptr(), inv_freq.data_ptr() if pairs else 0, positions.data_ptr() if pairs else 0,
+        per_image, 0,
+        *head_strides("q", q, q.is_contiguous()), *head_strides("k", k, k.is_contiguous()),
+        *head_strides("yq", yq, yq.is_contiguous()), *head_strides("yk", yk, yk.is_contiguous()))
 
 
 def qk_norm(q, k, wq=None, wk=None, *, norm="rms", eps=1e-6, inv_freq=None, positions=None, out=None, stream=None):
@@ -63,11 +66,9 @@ def qk_norm(q, k, wq=None, wk=None, *, norm="rms", eps=1e-6, inv_freq=None, posi
     (vscan_qknorm_forward). out: a pair of tensors to write to; (q, k) itself works in place."""
     if out is None:
         out = (torch.empty(q.shape, dtype=q.dtype, device=q.device), torch.empty(k.shape, dtype=k.dtype, device=k.device))
-    for name, t, like in (("out[0]", out[0], q), ("out[1]", out[1], k)):
-        check_tensor(name, t, like.shape, q.dtype, q.device)
-    args = _marshal(q, k, wq, wk, *out, norm, eps, inv_freq, positions)
-    with on_device(q.device):
-        check(lib.vscan_qknorm_forward(ctypes.byref(args), stream_handle(stream, q.device, *out)))
+    index, args = _marshal(q, k, wq, wk, *out, norm, eps, inv_freq, positions)
+    with on_device(index):
+        check(_abi.qknorm_forward.fn(args, stream_handle(stream, index, *out)))
     return tuple(out)
 
 
@@ -77,26 +78,23 @@ def qk_norm_backward(q, k, wq=None, wk=None, *, dyq, dyk, norm="rms", eps=1e-6, 
     q) and, where there is a weight, dwq and dwk (float32, summed over the tokens in a fixed
     order). dyq, dyk: dL/dyq and dL/dyk in the dtype of q, with free strides. `want` limits
     the keys computed."""
-    for name, t, like in (("dyq", dyq, q), ("dyk", dyk, k)):
-        check_tensor(name, t, like.shape, q.dtype, q.device)
-    args = _marshal(q, k, wq, wk, dyq, dyk, norm, eps, inv_freq, positions)
+    index, args = _marshal(q, k, wq, wk, dyq, dyk, norm, eps, inv_freq, positions)
     like = {"dq": q, "dk": k, "dwq": wq, "dwk": wk}
     if not set(want) <= set(like):
         raise ValueError(f"want holds unknown gradients {sorted(set(want) - set(like))}")
-    grads, out, dev = VscanQkNormGrads(), {}, q.device
+    grads, out = VscanQkNormGrads(), {}
     grads.dyq, grads.dyk = dyq.data_ptr(), dyk.data_ptr()
     for name in want:
         t = like[name]
         if t is not None:
-            out[name] = torch.empty(t.shape, dtype=t.dtype, device=dev)
+            out[name] = torch.empty(t.shape, dtype=t.dtype, device=t.device)
             setattr(grads, name, out[name].data_ptr())
     workspace = None
     if "dwq" in out or "dwk" in out:
         need = ctypes.c_uint64()
-        check(lib.vscan_qknorm_backward_workspace_size(ctypes.byref(args), ctypes.byref(need)))
-        workspace = torch.empty(need.value, dtype=torch.uint8, device=dev)
+        check(_abi.qknorm_backward_workspace_size.fn(args, ctypes.byref(need)))
+        workspace = torch.empty(need.value, dtype=torch.uint8, device=q.device)
         grads.workspace, grads.workspace_bytes = workspace.data_ptr(), need.value
-    with on_device(dev):
-        check(lib.vscan_qknorm_backward(ctypes.byref(args), ctypes.byref(grads),
-                                        stream_handle(stream, dev, workspace, *out.values())))
+    with on_device(index):
+        check(_abi.qknorm_backward.fn(args, ctypes.byref(grads), stream_handle(stream, index, workspace, *out.values())))
     return out
