@@ -16,7 +16,7 @@ using vscan_host::cuda_fail;
 using vscan_host::fail;
 using vscan_host::NvtxRange;
 
-constexpr int kMaxBlocks = 148 * 8;  // eight CTAs of 256 threads per SM
+constexpr int kMaxBlocks = 148 * 4;  // of q and as many of k: eight CTAs of 256 threads an SM
 
 vscan_status check_stride(const char* name, int64_t tok, int64_t img, int64_t width, int vec)
 {
@@ -76,13 +76,16 @@ int unit_width(const vscan_qknorm_args* a)
     return v;
 }
 
-// CTAs: one for each position and group of images. Images share a position's
-// angles; they are spread over groups where the positions alone leave SMs idle.
+// CTAs: one for each position and group of images. Images share a position's angles; they are
+// spread over groups until every CTA slot has several items (so that the last round costs
+// little), as long as an item keeps 32 rows of the smaller side.
 int groups_of(const vscan_qknorm_args* a)
 {
     if (a->pairs && a->pos_per_image) return std::max(a->batch, 1);
-    const int want = (int)(kMaxBlocks / std::max(a->tokens, 1)) + 1;
-    return std::max(1, std::min(a->batch, want));
+    const long long heads = std::min(a->heads_q, a->heads_k);
+    const long long want = (6LL * kMaxBlocks + a->tokens - 1) / std::max(a->tokens, 1);
+    const long long most = std::max(1LL, std::max(a->batch * heads / 32, (long long)kMaxBlocks / std::max(a->tokens, 1)));
+    return (int)std::max(1LL, std::min(std::min(want, most), (long long)a->batch));
 }
 
 int blocks_of(const vscan_qknorm_args* a)
@@ -93,7 +96,7 @@ int blocks_of(const vscan_qknorm_args* a)
 QkNormParams make_params(const vscan_qknorm_args* a, int v)
 {
     QkNormParams p{};
-    p.batch = a->batch; p.tokens = a->tokens; p.heads_q = a->heads_q; p.heads_k = a->heads_k;
+    p.batch = a->batch; p.tokens = a->tokens;
     p.d = a->dim; p.pairs = a->pairs; p.axes = a->axes;
     p.rms = a->norm == VSCAN_NORM_RMS;
     p.pos_img = a->pos_per_image ? a->tokens * a->axes : 0;
@@ -102,16 +105,18 @@ QkNormParams make_params(const vscan_qknorm_args* a, int v)
     p.lanes = 1;
     while (p.lanes < 32 && p.lanes < p.units) p.lanes *= 2;
     p.eps = a->eps;
-    p.q = a->q; p.k = a->k; p.yq = a->yq; p.yk = a->yk;
-    p.wq = a->wq; p.wk = a->wk; p.inv_freq = a->inv_freq; p.positions = a->positions;
+    p.inv_freq = a->inv_freq; p.positions = a->positions;
     auto stride = [&](int64_t tok, int64_t img, int heads, long long& t, long long& i) {
         t = tok ? tok : (long long)heads * a->dim;
         i = img ? img : t * a->tokens;
     };
-    stride(a->q_tok_stride, a->q_batch_stride, a->heads_q, p.q_tok, p.q_img);
-    stride(a->k_tok_stride, a->k_batch_stride, a->heads_k, p.k_tok, p.k_img);
-    stride(a->yq_tok_stride, a->yq_batch_stride, a->heads_q, p.yq_tok, p.yq_img);
-    stride(a->yk_tok_stride, a->yk_batch_stride, a->heads_k, p.yk_tok, p.yk_img);
+    vscan::QkNormSide &q = p.side[0], &k = p.side[1];
+    q.heads = a->heads_q; q.x = a->q; q.w = a->wq; q.y = a->yq;
+    k.heads = a->heads_k; k.x = a->k; k.w = a->wk; k.y = a->yk;
+    stride(a->q_tok_stride, a->q_batch_stride, a->heads_q, q.x_tok, q.x_img);
+    stride(a->k_tok_stride, a->k_batch_stride, a->heads_k, k.x_tok, k.x_img);
+    stride(a->yq_tok_stride, a->yq_batch_stride, a->heads_q, q.y_tok, q.y_img);
+    stride(a->yk_tok_stride, a->yk_batch_stride, a->heads_k, k.y_tok, k.y_img);
     p.blocks = blocks_of(a);
     return p;
 }
@@ -121,19 +126,19 @@ void launch_units(const QkNormParams& p, size_t smem, cudaStream_t s)
 {
     const int per_lane = (p.units + p.lanes - 1) / p.lanes;
     if (per_lane == 1)
-        vscan::qk_norm_kernel<T, V, 1, BACK><<<p.blocks, vscan::QN_THREADS, smem, s>>>(p);
+        vscan::qk_norm_kernel<T, V, 1, BACK><<<dim3(p.blocks, 2), vscan::QN_THREADS, smem, s>>>(p);
     else if constexpr (V <= 2) {
         if (per_lane == 2)
-            vscan::qk_norm_kernel<T, V, 2, BACK><<<p.blocks, vscan::QN_THREADS, smem, s>>>(p);
+            vscan::qk_norm_kernel<T, V, 2, BACK><<<dim3(p.blocks, 2), vscan::QN_THREADS, smem, s>>>(p);
         else if constexpr (V == 1)
-            vscan::qk_norm_kernel<T, V, 4, BACK><<<p.blocks, vscan::QN_THREADS, smem, s>>>(p);
+            vscan::qk_norm_kernel<T, V, 4, BACK><<<dim3(p.blocks, 2), vscan::QN_THREADS, smem, s>>>(p);
     }
 }
 
 template <bool BACK>
 cudaError_t launch(const vscan_qknorm_args* a, const QkNormParams& p, int v, cudaStream_t s)
 {
-    const size_t smem = BACK && p.part ? (size_t)(vscan::QN_THREADS / 32) * 2 * p.d * 4 : 0;
+    const size_t smem = BACK && p.part ? (size_t)(vscan::QN_THREADS / 32) * p.d * 4 : 0;
     if (a->dtype == VSCAN_F32) {
         if (v == 4) launch_units<float, 4, BACK>(p, smem, s);
         else if (v == 2) launch_units<float, 2, BACK>(p, smem, s);
@@ -205,14 +210,13 @@ vscan_status vscan_qknorm_backward(const vscan_qknorm_args* args, const vscan_qk
         return fail(VSCAN_ERR_WORKSPACE, "workspace of %llu bytes, %llu needed", (unsigned long long)grads->workspace_bytes,
                     (unsigned long long)need);
     NvtxRange range("vscan_qknorm_backward");
-    p.dyq = grads->dyq; p.dyk = grads->dyk;
-    p.dq = grads->dq; p.dk = grads->dk;
+    p.side[0].dy = grads->dyq; p.side[0].y = grads->dq;
+    p.side[1].dy = grads->dyk; p.side[1].y = grads->dk;
     p.part = weights ? static_cast<float*>(grads->workspace) : nullptr;
     e = launch<true>(args, p, v, s);
     if (e == cudaSuccess && weights) {
-        constexpr int per = vscan::QN_THREADS / 32;
-        vscan::qk_norm_weight_kernel<<<(2 * args->dim + per - 1) / per, vscan::QN_THREADS, 0, s>>>(
-            p.part, p.blocks, args->dim, grads->dwq, grads->dwk);
+        vscan::qk_norm_weight_kernel<<<dim3((args->dim + 31) / 32, 2), vscan::QN_THREADS, 0, s>>>(p.part, p.blocks, args->dim,
+                                                                                             grads->dwq, grads->dwk);
         e = cudaGetLastError();
     }
     return e == cudaSuccess ? VSCAN_OK : cuda_fail(e, "vscan_qknorm_backward");

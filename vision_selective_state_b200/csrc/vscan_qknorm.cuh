@@ -11,10 +11,12 @@
 // channels are split into units of V: unit i is channels [i V, i V + V) together
 // with the V at distance R that they turn with (behind 2 R: with the next half of
 // the rest), so that a lane holds both halves of its pairs and a row needs no
-// exchange but the sum of squares. A CTA takes one position and turns all images
-// and heads of it by one set of angles: sines and cosines are computed once a
+// exchange but the sum of squares. A CTA takes one position of q or of k and turns
+// its images and heads by one set of angles: sines and cosines are computed once a
 // position, from float64 angles (a float32 product is off by whole radians at
-// positions of 2^24).
+// positions of 2^24). Two rows a lane are in flight, and weights wait in shared
+// memory, for more CTAs an SM. On 64 images of 4097 tokens, 6 + 6 heads of 128, bf16:
+// see the table beside the measurements for the rate.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -28,23 +30,27 @@ namespace vscan {
 constexpr int QN_THREADS = 256;
 constexpr int QN_MAX_PAIRS = 128;  // d <= 256
 
+struct QkNormSide {  // q or k
+    int heads;
+    const void* x;
+    const float* w;
+    void* y;             // backward: dense gradient of x
+    const void* dy;
+    long long x_tok, x_img, y_tok, y_img;  // y's (backward: dy's) strides
+};
+
 struct QkNormParams {
-    int batch, tokens, heads_q, heads_k, d, pairs, axes;
+    int batch, tokens, d, pairs, axes;
     int rms;             // 1: mean of squares, 0: sum
     int pos_img;         // elements between images of positions (0: shared)
     int groups;          // CTAs that share one position's images
     int lanes;           // lanes of a row: a power of two
     int units;           // units of a row
     float eps;
-    const void *q, *k;
-    const float *wq, *wk, *inv_freq;
+    const float* inv_freq;
     const int* positions;
-    void *yq, *yk;
-    long long q_tok, q_img, k_tok, k_img, yq_tok, yq_img, yk_tok, yk_img;
-    // backward: dyq, dyk at the y strides, dense dq, dk
-    const void *dyq, *dyk;
-    void *dq, *dk;
-    float* part;         // [CTAs][2][d] sums for the weights, or null
+    QkNormSide side[2];
+    float* part;         // backward: [2][blocks][d] sums for the weights, or null
     int blocks;
 };
 
@@ -117,162 +123,162 @@ __device__ __forceinline__ void qn_angles(const QkNormParams& p, const int* pos,
 {
     const int per = p.pairs / p.axes;
     for (int i = threadIdx.x; i < p.pairs; i += QN_THREADS) {
-        // the product is exact in float64 (31 + 24 bits round to 53: 2^-53 of it); whole turns come off there
-        const double turn = (double)pos[i / per] * (double)p.inv_freq[i];
-        const double two_pi = 6.283185307179586476925;
-        const double r = fma(-rint(turn / two_pi), two_pi, turn);
+        // the product rounds to 2^-53 of itself; whole turns come off in float64
+        const double angle = (double)pos[i / per] * (double)p.inv_freq[i];
+        constexpr double two_pi = 6.283185307179586476925, per_turn = 0.15915494309189533577;
+        const double rest = fma(-rint(angle * per_turn), two_pi, angle);
         float s, c;
-        sincosf((float)r, &s, &c);
+        sincospif((float)(rest * (2.0 * per_turn)), &s, &c);
         cs[i] = make_float2(c, s);
     }
 }
 
-// Rows of one position: (image of the group) x (query heads, then key heads).
+// Rows of one position: (image of the group) x head. blockIdx.y: q or k.
 template <typename T, int V, int U, bool BACK>
 __global__ void __launch_bounds__(QN_THREADS) qk_norm_kernel(const QkNormParams p)
 {
+    constexpr int R = U == 1 && (!BACK || V <= 4) ? 2 : 1;  // rows a lane has in flight
     __shared__ float2 cs[QN_MAX_PAIRS];
-    extern __shared__ float wsum[];  // backward with weights: [warps][2][d]
+    __shared__ float weight[2 * QN_MAX_PAIRS];
+    extern __shared__ float wsum[];  // backward with weights: [warps][d]
+    const QkNormSide& side = p.side[blockIdx.y];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int sub = lane & (p.lanes - 1), per_warp = 32 / p.lanes;
-    const int heads = p.heads_q + p.heads_k;
     const int row_slot = warp * per_warp + lane / p.lanes, row_slots = (QN_THREADS / 32) * per_warp;
+    const bool weighted = side.w != nullptr;
+    if (weighted)
+        for (int i = tid; i < p.d; i += QN_THREADS) weight[i] = side.w[i];
     int lo[U], hi[U];
-    float w[2][U][2 * V];
-    float acc[BACK ? 2 : 1][U][2 * V];
+    float acc[BACK ? U : 1][2 * V];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int i = u * p.lanes + sub;
         lo[u] = hi[u] = -1;
         if (i < p.units) qn_unit(p, V, i, lo[u], hi[u]);
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const float* src = t ? p.wk : p.wq;
-                w[t][u][e] = src && lo[u] >= 0 ? src[lo[u] + e] : 1.f;
-                w[t][u][V + e] = src && hi[u] >= 0 ? src[hi[u] + e] : 1.f;
-            }
     }
     if (BACK) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int e = 0; e < 2 * V; ++e) acc[t][u][e] = 0.f;
+            for (int e = 0; e < 2 * V; ++e) acc[u][e] = 0.f;
     }
     const long long work = (long long)p.tokens * p.groups;
     for (long long item = blockIdx.x; item < work; item += gridDim.x) {
         const int token = (int)(item / p.groups), group = (int)(item - (long long)token * p.groups);
-        if (p.pairs) {
-            __syncthreads();
-            qn_angles(p, p.positions + (long long)group * p.pos_img + (long long)token * p.axes, cs);
-            __syncthreads();
-        }
+        __syncthreads();
+        if (p.pairs) qn_angles(p, p.positions + (long long)group * p.pos_img + (long long)token * p.axes, cs);
+        __syncthreads();
         const int images = (p.batch - group + p.groups - 1) / p.groups;  // group, group + groups, ..
-        const int rows = images * heads;
-        for (int first = 0; first < rows; first += row_slots) {
-            const int row = first + row_slot;
-            const bool live = row < rows;
-            const int image = group + (row / heads) * p.groups, h = row - (row / heads) * heads;
-            const bool key = h >= p.heads_q;
-            const int head = key ? h - p.heads_q : h;
-            const T* src = key ? reinterpret_cast<const T*>(p.k) + image * p.k_img + token * p.k_tok
-                               : reinterpret_cast<const T*>(p.q) + image * p.q_img + token * p.q_tok;
-            const long long yat = key ? image * p.yk_img + token * p.yk_tok : image * p.yq_img + token * p.yq_tok;
-            src += (long long)head * p.d;
-            float x[U][2 * V], dy[BACK ? U : 1][2 * V];
-            float sq = 0.f;
+        const int rows = images * side.heads;
+        for (int first = 0; first < rows; first += R * row_slots) {
+            float x[R][U][2 * V], dy[BACK ? R : 1][U][2 * V];
+            long long yat[R], dense[BACK ? R : 1];
+            bool live[R];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float a[V] = {}, b[V] = {};
-                if (live && lo[u] >= 0) qn_load<T, V>(src + lo[u], a);
-                if (live && hi[u] >= 0) qn_load<T, V>(src + hi[u], b);
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    x[u][e] = a[e];
-                    x[u][V + e] = b[e];
-                    sq += a[e] * a[e] + b[e] * b[e];
-                }
-            }
-            if (BACK) {
-                const T* g = reinterpret_cast<const T*>(key ? p.dyk : p.dyq) + yat + (long long)head * p.d;
+            for (int k = 0; k < R; ++k) {
+                const int row = first + k * row_slots + row_slot;
+                live[k] = row < rows;
+                const int at = live[k] ? row / side.heads : 0, head = live[k] ? row - at * side.heads : 0;
+                const int image = group + at * p.groups;
+                const T* src = reinterpret_cast<const T*>(side.x) + image * side.x_img + token * side.x_tok + (long long)head * p.d;
+                yat[k] = image * side.y_img + token * side.y_tok + (long long)head * p.d;
+                if (BACK) dense[k] = (((long long)image * p.tokens + token) * side.heads + head) * p.d;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     float a[V] = {}, b[V] = {};
-                    if (live && lo[u] >= 0) qn_load<T, V>(g + lo[u], a);
-                    if (live && hi[u] >= 0) qn_load<T, V>(g + hi[u], b);
+                    if (live[k] && lo[u] >= 0) qn_load<T, V>(src + lo[u], a);
+                    if (live[k] && hi[u] >= 0) qn_load<T, V>(src + hi[u], b);
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
-                        dy[u][e] = a[e];
-                        dy[u][V + e] = b[e];
+                        x[k][u][e] = a[e];
+                        x[k][u][V + e] = b[e];
+                    }
+                    if (BACK) {
+                        const T* g = reinterpret_cast<const T*>(side.dy) + yat[k];
+                        float c[V] = {}, d[V] = {};
+                        if (live[k] && lo[u] >= 0) qn_load<T, V>(g + lo[u], c);
+                        if (live[k] && hi[u] >= 0) qn_load<T, V>(g + hi[u], d);
+#pragma unroll
+                        for (int e = 0; e < V; ++e) {
+                            dy[k][u][e] = c[e];
+                            dy[k][u][V + e] = d[e];
+                        }
                     }
                 }
             }
-            for (int o = p.lanes >> 1; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-            const float r = 1.f / sqrtf((p.rms ? sq / p.d : sq) + p.eps);
-            if (!BACK) {
-                T* dst = reinterpret_cast<T*>(key ? p.yk : p.yq) + yat + (long long)head * p.d;
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    float a[V], b[V];
-#pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        a[e] = x[u][e] * r * (key ? w[1][u][e] : w[0][u][e]);
-                        b[e] = x[u][V + e] * r * (key ? w[1][u][V + e] : w[0][u][V + e]);
-                        if (lo[u] >= 0 && lo[u] < p.pairs) {
-                            const float2 t = cs[lo[u] + e];
-                            const float y = a[e] * t.x - b[e] * t.y;
-                            b[e] = a[e] * t.y + b[e] * t.x;
-                            a[e] = y;
-                        }
-                    }
-                    if (live && lo[u] >= 0) qn_store<T, V>(dst + lo[u], a);
-                    if (live && hi[u] >= 0) qn_store<T, V>(dst + hi[u], b);
-                }
-            } else {
-                float inner = 0.f;
+            for (int k = 0; k < R; ++k) {
+                float sq = 0.f;
 #pragma unroll
                 for (int u = 0; u < U; ++u)
 #pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        float a = dy[u][e], b = dy[u][V + e];
-                        if (lo[u] >= 0 && lo[u] < p.pairs) {  // turned back
-                            const float2 t = cs[lo[u] + e];
-                            const float y = a * t.x + b * t.y;
-                            b = b * t.x - a * t.y;
-                            a = y;
-                        }
-                        const float ga = a * x[u][e] * r, gb = b * x[u][V + e] * r;
-                        if (key) {
-                            acc[BACK ? 1 : 0][u][e] += ga;
-                            acc[BACK ? 1 : 0][u][V + e] += gb;
-                        } else {
-                            acc[0][u][e] += ga;
-                            acc[0][u][V + e] += gb;
-                        }
-                        a *= key ? w[1][u][e] : w[0][u][e];
-                        b *= key ? w[1][u][V + e] : w[0][u][V + e];
-                        inner += a * x[u][e] + b * x[u][V + e];
-                        dy[u][e] = a;
-                        dy[u][V + e] = b;
-                    }
-                for (int o = p.lanes >> 1; o > 0; o >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, o);
-                const float f = (p.rms ? inner / p.d : inner) * r * r;
-                T* dst = reinterpret_cast<T*>(key ? p.dk : p.dq);
-                if (dst) {
-                    dst += (((long long)image * p.tokens + token) * (key ? p.heads_k : p.heads_q) + head) * p.d;
+                    for (int e = 0; e < 2 * V; ++e) sq += x[k][u][e] * x[k][u][e];
+                for (int o = p.lanes >> 1; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+                const float r = 1.f / sqrtf((p.rms ? sq / p.d : sq) + p.eps);
+                if (!BACK) {
+                    T* dst = reinterpret_cast<T*>(side.y) + yat[k];
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
                         float a[V], b[V];
+                        const bool turned = lo[u] >= 0 && lo[u] < p.pairs;
 #pragma unroll
                         for (int e = 0; e < V; ++e) {
-                            a[e] = r * (dy[u][e] - x[u][e] * f);
-                            b[e] = r * (dy[u][V + e] - x[u][V + e] * f);
+                            a[e] = x[k][u][e] * r;
+                            b[e] = x[k][u][V + e] * r;
+                            if (weighted) {
+                                a[e] *= lo[u] >= 0 ? weight[lo[u] + e] : 1.f;
+                                b[e] *= hi[u] >= 0 ? weight[hi[u] + e] : 1.f;
+                            }
+                            if (turned) {
+                                const float2 t = cs[lo[u] + e];
+                                const float y = a[e] * t.x - b[e] * t.y;
+                                b[e] = a[e] * t.y + b[e] * t.x;
+                                a[e] = y;
+                            }
                         }
-                        if (live && lo[u] >= 0) qn_store<T, V>(dst + lo[u], a);
-                        if (live && hi[u] >= 0) qn_store<T, V>(dst + hi[u], b);
+                        if (live[k] && lo[u] >= 0) qn_store<T, V>(dst + lo[u], a);
+                        if (live[k] && hi[u] >= 0) qn_store<T, V>(dst + hi[u], b);
+                    }
+                } else {
+                    float inner = 0.f;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const bool turned = lo[u] >= 0 && lo[u] < p.pairs;
+#pragma unroll
+                        for (int e = 0; e < V; ++e) {
+                            float a = dy[k][u][e], b = dy[k][u][V + e];
+                            if (turned) {  // back
+                                const float2 t = cs[lo[u] + e];
+                                const float y = a * t.x + b * t.y;
+                                b = b * t.x - a * t.y;
+                                a = y;
+                            }
+                            acc[u][e] += a * (x[k][u][e] * r);
+                            acc[u][V + e] += b * (x[k][u][V + e] * r);
+                            if (weighted) {
+                                a *= lo[u] >= 0 ? weight[lo[u] + e] : 1.f;
+                                b *= hi[u] >= 0 ? weight[hi[u] + e] : 1.f;
+                            }
+                            inner += a * x[k][u][e] + b * x[k][u][V + e];
+                            dy[k][u][e] = a;
+                            dy[k][u][V + e] = b;
+                        }
+                    }
+                    for (int o = p.lanes >> 1; o > 0; o >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, o);
+                    const float f = (p.rms ? inner / p.d : inner) * r * r;
+                    if (side.y) {
+                        T* dst = reinterpret_cast<T*>(side.y) + dense[k];
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            float a[V], b[V];
+#pragma unroll
+                            for (int e = 0; e < V; ++e) {
+                                a[e] = r * (dy[k][u][e] - x[k][u][e] * f);
+                                b[e] = r * (dy[k][u][V + e] - x[k][u][V + e] * f);
+                            }
+                            if (live[k] && lo[u] >= 0) qn_store<T, V>(dst + lo[u], a);
+                            if (live[k] && hi[u] >= 0) qn_store<T, V>(dst + hi[u], b);
+                        }
                     }
                 }
             }
@@ -281,37 +287,41 @@ __global__ void __launch_bounds__(QN_THREADS) qk_norm_kernel(const QkNormParams 
     if (BACK && p.part) {
         // the rows of a warp hold the same channels: add them up, then the warps, in a fixed order
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int e = 0; e < 2 * V; ++e) {
-                    float a = acc[BACK ? t : 0][u][e];
-                    for (int o = p.lanes; o < 32; o <<= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-                    const int base = e < V ? lo[u] : hi[u];
-                    if (lane < p.lanes && base >= 0) wsum[(warp * 2 + t) * p.d + base + (e < V ? e : e - V)] = a;
-                }
+            for (int e = 0; e < 2 * V; ++e) {
+                float a = acc[u][e];
+                for (int o = p.lanes; o < 32; o <<= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+                const int base = e < V ? lo[u] : hi[u];
+                if (lane < p.lanes && base >= 0) wsum[warp * p.d + base + (e < V ? e : e - V)] = a;
+            }
         __syncthreads();
-        for (int i = tid; i < 2 * p.d; i += QN_THREADS) {
+        for (int i = tid; i < p.d; i += QN_THREADS) {
             float a = 0.f;
-            for (int wp = 0; wp < QN_THREADS / 32; ++wp) a += wsum[wp * 2 * p.d + i];
-            p.part[(long long)blockIdx.x * 2 * p.d + i] = a;
+            for (int wp = 0; wp < QN_THREADS / 32; ++wp) a += wsum[wp * p.d + i];
+            p.part[((long long)blockIdx.y * p.blocks + blockIdx.x) * p.d + i] = a;
         }
     }
 }
 
-// dwq, dwk: the CTAs' sums added in a fixed order, in float64. One warp a channel.
+// dwq, dwk: the CTAs' sums added in a fixed order, in float64. A CTA takes 32 channels of one of
+// the two, a warp every eighth sum of them.
 __global__ void __launch_bounds__(QN_THREADS) qk_norm_weight_kernel(const float* part, int blocks, int d, float* dwq, float* dwk)
 {
-    const int i = blockIdx.x * (QN_THREADS / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (i >= 2 * d) return;
-    float* dst = i < d ? dwq : dwk;
-    if (!dst) return;
+    __shared__ double sum[QN_THREADS / 32][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = blockIdx.x * 32 + lane;
+    float* dst = blockIdx.y ? dwk : dwq;
     double a = 0.0;
-    for (int b = lane; b < blocks; b += 32) a += (double)part[(long long)b * 2 * d + i];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a += __shfl_down_sync(0xffffffffu, a, o);
-    if (lane == 0) dst[i < d ? i : i - d] = (float)a;
+    if (i < d && dst) {
+#pragma unroll 4
+        for (int b = warp; b < blocks; b += QN_THREADS / 32) a += (double)part[((long long)blockIdx.y * blocks + b) * d + i];
+    }
+    sum[warp][lane] = a;
+    __syncthreads();
+    if (warp == 0 && i < d && dst) {
+        for (int w = 1; w < QN_THREADS / 32; ++w) a += sum[w][lane];
+        dst[i] = (float)a;
+    }
 }
 
 }  // namespace vscan
