@@ -215,7 +215,7 @@ vscan_status vscan_qknorm_backward(const vscan_qknorm_args* args, const vscan_qk
     p.part = weights ? static_cast<float*>(grads->workspace) : nullptr;
     e = launch<true>(args, p, v, s);
     if (e == cudaSuccess && weights) {
-        vscan::qk_norm_weight_kernel<<<dim3((args->dim + 31) / 32, 2), vscan::QN_THREADS, 0, s>>>(p.part, p.blocks, args->dim,
+        vscan::qk_norm_weight_kernel<<<dim3((args->dim + 31) / 32, 2), vscan::QN_SUM_THREADS, 0, s>>>(p.part, p.blocks, args->dim,
                                                                                              grads->dwq, grads->dwk);
         e = cudaGetLastError();
     }

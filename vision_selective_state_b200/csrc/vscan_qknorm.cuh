@@ -27,7 +27,7 @@
 
 namespace vscan {
 
-constexpr int QN_THREADS = 256;
+constexpr int QN_THREADS = 256, QN_SUM_THREADS = 1024;
 constexpr int QN_MAX_PAIRS = 128;  // d <= 256
 
 struct QkNormSide {  // q or k
@@ -118,8 +118,21 @@ __device__ __forceinline__ void qn_store(T* p, const float (&x)[V])
     }
 }
 
+// V neighbouring values from shared memory, 16 bytes at a time where V allows.
+template <int V>
+__device__ __forceinline__ void qn_shared(const float* s, float (&v)[V])
+{
+    if constexpr (V >= 4) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(v + i) = *reinterpret_cast<const float4*>(s + i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = s[i];
+    }
+}
+
 // Cosine and sine of every pair's angle at one position, by the whole CTA.
-__device__ __forceinline__ void qn_angles(const QkNormParams& p, const int* pos, float2* cs)
+__device__ __forceinline__ void qn_angles(const QkNormParams& p, const int* pos, float* cosine, float* sine)
 {
     const int per = p.pairs / p.axes;
     for (int i = threadIdx.x; i < p.pairs; i += QN_THREADS) {
@@ -127,19 +140,16 @@ __device__ __forceinline__ void qn_angles(const QkNormParams& p, const int* pos,
         const double angle = (double)pos[i / per] * (double)p.inv_freq[i];
         constexpr double two_pi = 6.283185307179586476925, per_turn = 0.15915494309189533577;
         const double rest = fma(-rint(angle * per_turn), two_pi, angle);
-        float s, c;
-        sincospif((float)(rest * (2.0 * per_turn)), &s, &c);
-        cs[i] = make_float2(c, s);
+        sincospif((float)(rest * (2.0 * per_turn)), sine + i, cosine + i);
     }
 }
 
 // Rows of one position: (image of the group) x head. blockIdx.y: q or k.
 template <typename T, int V, int U, bool BACK>
-__global__ void __launch_bounds__(QN_THREADS) qk_norm_kernel(const QkNormParams p)
+__global__ void __launch_bounds__(QN_THREADS, BACK ? 3 : 4) qk_norm_kernel(const QkNormParams p)
 {
     constexpr int R = U == 1 && (!BACK || V <= 4) ? 2 : 1;  // rows a lane has in flight
-    __shared__ float2 cs[QN_MAX_PAIRS];
-    __shared__ float weight[2 * QN_MAX_PAIRS];
+    __shared__ __align__(16) float cosine[QN_MAX_PAIRS], sine[QN_MAX_PAIRS], weight[2 * QN_MAX_PAIRS];
     extern __shared__ float wsum[];  // backward with weights: [warps][d]
     const QkNormSide& side = p.side[blockIdx.y];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -166,7 +176,7 @@ __global__ void __launch_bounds__(QN_THREADS) qk_norm_kernel(const QkNormParams 
     for (long long item = blockIdx.x; item < work; item += gridDim.x) {
         const int token = (int)(item / p.groups), group = (int)(item - (long long)token * p.groups);
         __syncthreads();
-        if (p.pairs) qn_angles(p, p.positions + (long long)group * p.pos_img + (long long)token * p.axes, cs);
+        if (p.pairs) qn_angles(p, p.positions + (long long)group * p.pos_img + (long long)token * p.axes, cosine, sine);
         __syncthreads();
         const int images = (p.batch - group + p.groups - 1) / p.groups;  // group, group + groups, ..
         const int rows = images * side.heads;
@@ -219,20 +229,28 @@ __global__ void __launch_bounds__(QN_THREADS) qk_norm_kernel(const QkNormParams 
                     T* dst = reinterpret_cast<T*>(side.y) + yat[k];
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
-                        float a[V], b[V];
-                        const bool turned = lo[u] >= 0 && lo[u] < p.pairs;
+                        float a[V], b[V], c[V], d[V];
 #pragma unroll
                         for (int e = 0; e < V; ++e) {
                             a[e] = x[k][u][e] * r;
                             b[e] = x[k][u][V + e] * r;
-                            if (weighted) {
-                                a[e] *= lo[u] >= 0 ? weight[lo[u] + e] : 1.f;
-                                b[e] *= hi[u] >= 0 ? weight[hi[u] + e] : 1.f;
+                        }
+                        if (weighted) {
+                            qn_shared<V>(weight + max(lo[u], 0), c);
+                            qn_shared<V>(weight + max(hi[u], 0), d);
+#pragma unroll
+                            for (int e = 0; e < V; ++e) {
+                                a[e] *= c[e];
+                                b[e] *= d[e];
                             }
-                            if (turned) {
-                                const float2 t = cs[lo[u] + e];
-                                const float y = a[e] * t.x - b[e] * t.y;
-                                b[e] = a[e] * t.y + b[e] * t.x;
+                        }
+                        if (lo[u] >= 0 && lo[u] < p.pairs) {  // turned
+                            qn_shared<V>(cosine + lo[u], c);
+                            qn_shared<V>(sine + lo[u], d);
+#pragma unroll
+                            for (int e = 0; e < V; ++e) {
+                                const float y = a[e] * c[e] - b[e] * d[e];
+                                b[e] = a[e] * d[e] + b[e] * c[e];
                                 a[e] = y;
                             }
                         }
@@ -243,25 +261,41 @@ __global__ void __launch_bounds__(QN_THREADS) qk_norm_kernel(const QkNormParams 
                     float inner = 0.f;
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
-                        const bool turned = lo[u] >= 0 && lo[u] < p.pairs;
+                        float a[V], b[V], c[V], d[V];
 #pragma unroll
                         for (int e = 0; e < V; ++e) {
-                            float a = dy[k][u][e], b = dy[k][u][V + e];
-                            if (turned) {  // back
-                                const float2 t = cs[lo[u] + e];
-                                const float y = a * t.x + b * t.y;
-                                b = b * t.x - a * t.y;
-                                a = y;
+                            a[e] = dy[k][u][e];
+                            b[e] = dy[k][u][V + e];
+                        }
+                        if (lo[u] >= 0 && lo[u] < p.pairs) {  // turned back
+                            qn_shared<V>(cosine + lo[u], c);
+                            qn_shared<V>(sine + lo[u], d);
+#pragma unroll
+                            for (int e = 0; e < V; ++e) {
+                                const float y = a[e] * c[e] + b[e] * d[e];
+                                b[e] = b[e] * c[e] - a[e] * d[e];
+                                a[e] = y;
                             }
-                            acc[u][e] += a * (x[k][u][e] * r);
-                            acc[u][V + e] += b * (x[k][u][V + e] * r);
-                            if (weighted) {
-                                a *= lo[u] >= 0 ? weight[lo[u] + e] : 1.f;
-                                b *= hi[u] >= 0 ? weight[hi[u] + e] : 1.f;
+                        }
+#pragma unroll
+                        for (int e = 0; e < V; ++e) {
+                            acc[u][e] += a[e] * (x[k][u][e] * r);
+                            acc[u][V + e] += b[e] * (x[k][u][V + e] * r);
+                        }
+                        if (weighted) {
+                            qn_shared<V>(weight + max(lo[u], 0), c);
+                            qn_shared<V>(weight + max(hi[u], 0), d);
+#pragma unroll
+                            for (int e = 0; e < V; ++e) {
+                                a[e] *= c[e];
+                                b[e] *= d[e];
                             }
-                            inner += a * x[k][u][e] + b * x[k][u][V + e];
-                            dy[k][u][e] = a;
-                            dy[k][u][V + e] = b;
+                        }
+#pragma unroll
+                        for (int e = 0; e < V; ++e) {
+                            inner += a[e] * x[k][u][e] + b[e] * x[k][u][V + e];
+                            dy[k][u][e] = a[e];
+                            dy[k][u][V + e] = b[e];
                         }
                     }
                     for (int o = p.lanes >> 1; o > 0; o >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, o);
@@ -305,21 +339,21 @@ __global__ void __launch_bounds__(QN_THREADS) qk_norm_kernel(const QkNormParams 
 }
 
 // dwq, dwk: the CTAs' sums added in a fixed order, in float64. A CTA takes 32 channels of one of
-// the two, a warp every eighth sum of them.
-__global__ void __launch_bounds__(QN_THREADS) qk_norm_weight_kernel(const float* part, int blocks, int d, float* dwq, float* dwk)
+// the two, a warp every 32nd sum of them.
+__global__ void __launch_bounds__(QN_SUM_THREADS) qk_norm_weight_kernel(const float* part, int blocks, int d, float* dwq, float* dwk)
 {
-    __shared__ double sum[QN_THREADS / 32][32];
+    __shared__ double sum[QN_SUM_THREADS / 32][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = blockIdx.x * 32 + lane;
     float* dst = blockIdx.y ? dwk : dwq;
     double a = 0.0;
     if (i < d && dst) {
 #pragma unroll 4
-        for (int b = warp; b < blocks; b += QN_THREADS / 32) a += (double)part[((long long)blockIdx.y * blocks + b) * d + i];
+        for (int b = warp; b < blocks; b += QN_SUM_THREADS / 32) a += (double)part[((long long)blockIdx.y * blocks + b) * d + i];
     }
     sum[warp][lane] = a;
     __syncthreads();
     if (warp == 0 && i < d && dst) {
-        for (int w = 1; w < QN_THREADS / 32; ++w) a += sum[w][lane];
+        for (int w = 1; w < QN_SUM_THREADS / 32; ++w) a += sum[w][lane];
         dst[i] = (float)a;
     }
 }
