@@ -131,7 +131,10 @@ Layout forward_layout(const vscan_route* r, const vscan_delta_args* a, int pplan
 {
     const size_t n = (size_t)slots_of(r, a) * a->heads_v;
     Layout l;
-    l.total = round256(n * vscan::delta_record_bytes(pplanes));
+    const bool wide = padded_dim_k(a->dim_k) == 128;
+    l.total = round256(n * (a->dtype == VSCAN_F32
+                                ? (wide ? vscan::delta_record_bytes<float, 128>(pplanes) : vscan::delta_record_bytes<float, 64>(pplanes))
+                                : vscan::delta_record_bytes<__nv_bfloat16, 64>(pplanes)));
     return l;
 }
 

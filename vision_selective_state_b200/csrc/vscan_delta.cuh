@@ -64,8 +64,9 @@ struct DeltaParams {
     float scale, beta_scale;
     long long q_tok, q_img, k_tok, k_img, v_tok, v_img, a_tok, a_img, b_tok, b_img, y_tok, y_img;
     // workspace, indexed by slot * heads_v + head
-    unsigned char* wrec; // records: DL_VECS floats, three planes of T, tplanes planes of P; each plane [64][64]
-                         // the image of a swizzled tile, so that a walk copies a record as it is
+    unsigned char* wrec; // records: DL_VECS floats, three planes of T, tplanes planes of P, in float32 also three
+                         // planes each of K and Q; each plane [64][64] the image of a swizzled tile, so that a walk
+                         // copies a record as it is
     float* wL;           // [..][64][64]: e^{G_i - G_j} k_i.k_j below the diagonal (backward, else null)
     float* wS;           // [..][DKP][dv]: state entering the chunk (backward)
     float* wW;           // [..][64][dv]: W of the chunk (backward)
@@ -119,16 +120,21 @@ __device__ __forceinline__ int delta_row(const DeltaParams& p, const DeltaSeq& s
 __device__ __forceinline__ long long delta_img(const DeltaParams& p, int b) { return p.offsets ? 0 : b; }
 
 // Parts of a record.
-__host__ __device__ __forceinline__ size_t delta_record_bytes(int tplanes) { return DL_VECS * 4 + (size_t)(3 + tplanes) * DL_PLANE * 2; }
+template <typename T, int DKP>
+__host__ __device__ constexpr size_t delta_record_bytes(int tplanes)
+{
+    return DL_VECS * 4 + (size_t)(3 + tplanes + (sizeof(T) == 4 ? 6 * (DKP / 64) : 0)) * DL_PLANE * 2;
+}
+template <typename T, int DKP>
 __device__ __forceinline__ float* record_vec(const DeltaParams& p, size_t rec)
 {
-    return reinterpret_cast<float*>(p.wrec + rec * delta_record_bytes(p.tplanes));
+    return reinterpret_cast<float*>(p.wrec + rec * delta_record_bytes<T, DKP>(p.tplanes));
 }
-__device__ __forceinline__ __nv_bfloat16* record_T(const DeltaParams& p, size_t rec)
+template <typename T, int DKP>
+__device__ __forceinline__ __nv_bfloat16* record_P(const DeltaParams& p, size_t rec)
 {
-    return reinterpret_cast<__nv_bfloat16*>(record_vec(p, rec) + DL_VECS);
+    return reinterpret_cast<__nv_bfloat16*>(record_vec<T, DKP>(p, rec) + DL_VECS) + 3 * DL_PLANE;
 }
-__device__ __forceinline__ __nv_bfloat16* record_P(const DeltaParams& p, size_t rec) { return record_T(p, rec) + 3 * DL_PLANE; }
 
 // ---- tensor-core fragments ------------------------------------------------------
 // m16n8k16: lane (g, t) = (lane / 4, lane % 4) holds of A the pairs of columns
@@ -242,6 +248,10 @@ __device__ __forceinline__ void mma_terms(float (&c0)[4], float (&c1)[4], const 
         }
     }
 }
+
+// e^{G_i - G_j} from running sums held as a rounded value and the rest of it. (ex2 is good to
+// 2^-22; the product with log2 e rounds by 2^-24 of an exponent whose power is small where it is large.)
+__device__ __forceinline__ float decay_between(float2 gi, float2 gj) { return fast_exp2(((gi.x - gj.x) + (gi.y - gj.y)) * LOG2E); }
 
 // ---- tiles ------------------------------------------------------------------------
 template <typename T> struct DeltaIo;
@@ -394,9 +404,11 @@ __device__ __forceinline__ void image_put(__nv_bfloat16* img, int at, float x)
     }
 }
 
-// The rows of K or Q to padded rows in bf16 planes, by all warps but the first.
+// The rows of K or Q to padded rows in bf16 planes, by all warps but the first; float32 ones, split,
+// to the record as well.
 template <int DKP>
-__device__ __forceinline__ void prep_load(__nv_bfloat16* dst, const __nv_bfloat16* src, long long tok, const int* rows, int have, int tid)
+__device__ __forceinline__ void prep_load(__nv_bfloat16* dst, unsigned char*, const __nv_bfloat16* src, long long tok,
+                                          const int* rows, int have, int tid)
 {
     constexpr int vecs = DKP / 8;
     const int c = tid % vecs * 8;
@@ -407,7 +419,8 @@ __device__ __forceinline__ void prep_load(__nv_bfloat16* dst, const __nv_bfloat1
     });
 }
 template <int DKP>
-__device__ __forceinline__ void prep_load(__nv_bfloat16* dst, const float* src, long long tok, const int* rows, int have, int tid)
+__device__ __forceinline__ void prep_load(__nv_bfloat16* dst, unsigned char* image, const float* src, long long tok,
+                                          const int* rows, int have, int tid)
 {
     constexpr int vecs = DKP / 8;
     const int c = tid % vecs * 8;
@@ -423,6 +436,7 @@ __device__ __forceinline__ void prep_load(__nv_bfloat16* dst, const float* src, 
             u.z = split_bf16(z.x, z.y);
             u.w = split_bf16(z.z, z.w);
             *reinterpret_cast<uint4*>(dst + n * (DL_C * (DKP + 8)) + r * (DKP + 8) + c) = u;
+            *reinterpret_cast<uint4*>(image + n * (DKP / 64 * TC_TILE) + tc_swizzle(r, c / 8)) = u;
         }
     });
 }
@@ -469,6 +483,7 @@ __global__ void __launch_bounds__(DP_THREADS) delta_prep_kernel(const DeltaParam
     const int hk = head / p.group;
     const size_t rec = (size_t)blockIdx.x * p.heads_v + head;
 
+    unsigned char* out = p.wrec + rec * delta_record_bytes<T, DKP>(PP);
     double g[2];
     if (warp == 0) {  // running sum of the log decay: two steps a lane, then a scan over the lanes
         const float A = p.A[head], bias = p.bias ? p.bias[head] : 0.f;
@@ -499,8 +514,9 @@ __global__ void __launch_bounds__(DP_THREADS) delta_prep_kernel(const DeltaParam
         const int ht = tid - 32;
         if (ht < DL_C) rows[ht] = delta_row(p, s, t0 + ht);
         bar_sync(3, DP_THREADS - 32);
-        prep_load<DKP>(K, reinterpret_cast<const T*>(p.k) + img * p.k_img + (long long)hk * p.dk, p.k_tok, rows, p.dk, ht);
-        prep_load<DKP>(Q, reinterpret_cast<const T*>(p.q) + img * p.q_img + (long long)hk * p.dk, p.q_tok, rows, p.dk, ht);
+        unsigned char* kq = out + DL_VECS * 4 + (3 + PP) * TC_TILE;
+        prep_load<DKP>(K, kq, reinterpret_cast<const T*>(p.k) + img * p.k_img + (long long)hk * p.dk, p.k_tok, rows, p.dk, ht);
+        prep_load<DKP>(Q, kq + 3 * (DKP / 64) * TC_TILE, reinterpret_cast<const T*>(p.q) + img * p.q_img + (long long)hk * p.dk, p.q_tok, rows, p.dk, ht);
         cp_async_commit();
         cp_async_wait<0>();
     }
@@ -593,13 +609,12 @@ __global__ void __launch_bounds__(DP_THREADS) delta_prep_kernel(const DeltaParam
                 const int i = r0 + half * 8;
                 const float2 gi = G[i];
                 // selected, not multiplied by zero: what lies above the diagonal is not looked at
-                const float d0 = expf((gi.x - gj0.x) + (gi.y - gj0.y)), d1 = expf((gi.x - gj1.x) + (gi.y - gj1.y));
+                const float d0 = decay_between(gi, gj0), d1 = decay_between(gi, gj1);
                 put(i, half, m0 / 8 + n, j < i + group ? d0 * diag[n][half * 2] : 0.f,
                     j + 1 < i + group ? d1 * diag[n][half * 2 + 1] : 0.f);
             }
         }
     }
-    unsigned char* out = p.wrec + rec * delta_record_bytes(PP);
     if (group) {
         tc_fence_smem();
         bar_sync(2, 128);
@@ -738,16 +753,19 @@ template <typename T, int DKP>
 struct WalkShape {
     static constexpr int NP = DeltaIo<T>::planes;
     static constexpr int PP = NP == 1 ? 2 : 3;   // terms of P and W in O: a bf16 y needs two
-    static constexpr int STAGES = NP == 1 ? 2 : 1;
+    static constexpr int STAGES = NP == 1 || DKP == 64 ? 2 : 1;
     static constexpr int KB = DKP / 64;          // 64-wide tiles of K
     static constexpr int plane = KB * TC_TILE;   // bytes
     static constexpr int vpitch = 128 + 16 / (int)sizeof(T);
-    // a stage: K, Q, the chunk's record, V
-    static constexpr int oQ = NP * plane, oVec = 2 * NP * plane, oT = oVec + DL_VECS * 4, oP = oT + 3 * TC_TILE;
-    static __host__ __device__ constexpr int oV(int pplanes) { return oP + pplanes * TC_TILE; }
+    // a stage: the chunk's record (decays, T, P), K, Q, and V where it is bf16. Float32 K and Q come
+    // split, as a part of the record; float32 values go straight to registers and back
+    static constexpr int oT = DL_VECS * 4, oP = oT + 3 * TC_TILE;
+    static __host__ __device__ constexpr int oK(int pplanes) { return oP + pplanes * TC_TILE; }
+    static __host__ __device__ constexpr int oQ(int pplanes) { return oK(pplanes) + NP * plane; }
+    static __host__ __device__ constexpr int oV(int pplanes) { return oQ(pplanes) + NP * plane; }
     static __host__ __device__ constexpr int stage(int pplanes)
     {
-        return (oV(pplanes) + DL_C * vpitch * (int)sizeof(T) + 1023) / 1024 * 1024;
+        return (oV(pplanes) + (NP == 1 ? DL_C * vpitch * (int)sizeof(T) : 0) + 1023) / 1024 * 1024;
     }
     // at least half of the SM's shared memory: one CTA an SM, which owns all tensor memory
     static __host__ __device__ constexpr size_t smem(int pplanes)
@@ -774,27 +792,6 @@ __device__ __forceinline__ void walk_load(unsigned char* dst, const __nv_bfloat1
         copy16(dst + tc_swizzle(r, c), at + (ok ? row * tok : 0), ok);
     });
 }
-template <int COLS>
-__device__ __forceinline__ void walk_load(unsigned char* dst, const float* src, long long tok, const int* rows, int have, int tid)
-{
-    constexpr int vecs = COLS / 8, plane = COLS / 64 * TC_TILE;
-    const int c = tid % vecs;
-    copy_rows<vecs, DW_HELP>(rows, tid, [&](int r, int row) {
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), z = x;
-        if (row >= 0 && c * 8 < have) x = __ldg(reinterpret_cast<const float4*>(src + c * 8 + row * tok));
-        if (row >= 0 && c * 8 + 4 < have) z = __ldg(reinterpret_cast<const float4*>(src + c * 8 + 4 + row * tok));
-#pragma unroll
-        for (int n = 0; n < 3; ++n) {
-            uint4 u;
-            u.x = split_bf16(x.x, x.y);
-            u.y = split_bf16(x.z, x.w);
-            u.z = split_bf16(z.x, z.y);
-            u.w = split_bf16(z.z, z.w);
-            *reinterpret_cast<uint4*>(dst + n * plane + tc_swizzle(r, c)) = u;
-        }
-    });
-}
-
 // The rows of a value-shaped token array (up to 128 channels of them), unsplit, in and out. A
 // bulk copy a row would be fewer instructions, but they issue one after the other: 64 of them
 // took 2600 cycles.
@@ -810,6 +807,30 @@ __device__ __forceinline__ void walk_load_values(T* dst, int pitch, const T* src
         copy16(dst + r * pitch + c, at + (ok ? row * tok : 0), ok);
     });
 }
+// 32 steps of a float32 value channel, neighbouring lanes neighbouring channels.
+__device__ __forceinline__ void walk_fetch(float (&x)[32], const float* src, long long tok, const int* rows, bool live)
+{
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+        const int4 r = *reinterpret_cast<const int4*>(rows + i);
+        x[i] = live && r.x >= 0 ? __ldg(src + r.x * tok) : 0.f;
+        x[i + 1] = live && r.y >= 0 ? __ldg(src + r.y * tok) : 0.f;
+        x[i + 2] = live && r.z >= 0 ? __ldg(src + r.z * tok) : 0.f;
+        x[i + 3] = live && r.w >= 0 ? __ldg(src + r.w * tok) : 0.f;
+    }
+}
+__device__ __forceinline__ void walk_put(float* dst, long long tok, const int* rows, bool live, const float (&x)[32])
+{
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+        const int4 r = *reinterpret_cast<const int4*>(rows + i);
+        if (live && r.x >= 0) dst[r.x * tok] = x[i];
+        if (live && r.y >= 0) dst[r.y * tok] = x[i + 1];
+        if (live && r.z >= 0) dst[r.z * tok] = x[i + 2];
+        if (live && r.w >= 0) dst[r.w * tok] = x[i + 3];
+    }
+}
+
 // 32 steps of a warp's 32 value channels to their token rows, through the warp's own corner of the
 // stage's value tile (whose values it alone has read): one value at a time from the registers,
 // 32 stores a lane took 2100 cycles a chunk, this takes 500. `mine` is this thread's value of
@@ -1012,7 +1033,8 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_scan_kernel(const DeltaPa
                 const int st = STAGES == 2 ? c & 1 : 0;
                 const uint32_t par = c & 1;
                 const uint32_t bK = static_cast<uint32_t>(__cvta_generic_to_shared(stages + st * STAGE));
-                const uint64_t dK = tc_desc(bK), dQ = tc_desc(bK + Sh::oQ), dT = tc_desc(bK + Sh::oT), dP = tc_desc(bK + Sh::oP);
+                const uint64_t dK = tc_desc(bK + Sh::oK(PP)), dQ = tc_desc(bK + Sh::oQ(PP));
+                const uint64_t dT = tc_desc(bK + Sh::oT), dP = tc_desc(bK + Sh::oP);
                 mbar_wait(bar.full + 8 * st, (c / STAGES) & 1, &ws->dead);
                 bar_sync(1, DW_COMPUTE + 32);
                 tc_fence_after();
@@ -1081,13 +1103,15 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_scan_kernel(const DeltaPa
                     unsigned char* base = stages + st * STAGE;
                     const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(base)), full = bar.full + 8 * st;
                     const size_t rec = (size_t)(s.slot + c) * p.heads_v + head;
-                    walk_load<DKP>(base, k, p.k_tok, rows, p.dk, ht);
-                    if (!SAVE) walk_load<DKP>(base + Sh::oQ, q, p.q_tok, rows, p.dk, ht);
-                    walk_load_values(reinterpret_cast<T*>(base + Sh::oV(PP)), Sh::vpitch, v, p.v_tok, rows, dvs, ht);
+                    if constexpr (NP == 1) {
+                        walk_load<DKP>(base + Sh::oK(PP), k, p.k_tok, rows, p.dk, ht);
+                        if (!SAVE) walk_load<DKP>(base + Sh::oQ(PP), q, p.q_tok, rows, p.dk, ht);
+                        walk_load_values(reinterpret_cast<T*>(base + Sh::oV(PP)), Sh::vpitch, v, p.v_tok, rows, dvs, ht);
+                    }
                     uint32_t bytes = 0;
                     if (ht == 0) {
-                        bytes = DL_VECS * 4 + (3 + (SAVE ? 0 : PP)) * TC_TILE;
-                        bulk_in(at + Sh::oVec, record_vec(p, rec), bytes, full);
+                        bytes = DL_VECS * 4 + (NP == 1 ? (3 + (SAVE ? 0 : PP)) * TC_TILE : (3 + PP) * TC_TILE + 2 * NP * Sh::plane);
+                        bulk_in(at, record_vec<T, DKP>(p, rec), bytes, full);
                     }
                     return bytes;
                 });
@@ -1097,6 +1121,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_scan_kernel(const DeltaPa
         const int half = warp >> 2, row = (warp & 3) * 32 + lane, vc = slice + row;  // this thread's value channel
         const bool live = vc < p.dv;
         const uint32_t tl = tm + ((uint32_t)(warp & 3) << 21);  // this warp's 32 rows
+        const T* v = reinterpret_cast<const T*>(p.v) + delta_img(p, b) * p.v_img + (long long)head * p.dv + vc;
         T* y = reinterpret_cast<T*>(p.y) + delta_img(p, b) * p.y_img + (long long)head * p.dv + vc - lane;
         float S[HS];  // S^T[row][half * HS + i]
 #pragma unroll
@@ -1112,7 +1137,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_scan_kernel(const DeltaPa
             const int st = STAGES == 2 ? c & 1 : 0;
             const uint32_t par = c & 1;
             T* vd = reinterpret_cast<T*>(stages + st * STAGE + Sh::oV(PP)) + half * 32 * Sh::vpitch + row;
-            const float* vec = reinterpret_cast<const float*>(stages + st * STAGE + Sh::oVec) + half * 32;
+            const float* vec = reinterpret_cast<const float*>(stages + st * STAGE) + half * 32;
             const size_t rec = (size_t)(s.slot + c) * p.heads_v + head;
             if (SAVE && live) {  // the state entering the chunk, for the gradients
                 float* o = p.wS + rec * p.dv * DKP + vc;
@@ -1123,8 +1148,12 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_scan_kernel(const DeltaPa
             mbar_wait(bar.full + 8 * st, (c / STAGES) & 1, &ws->dead);
             {
                 float u[32];
+                if constexpr (NP == 1) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) u[i] = to_float(vd[i * Sh::vpitch]);
+                    for (int i = 0; i < 32; ++i) u[i] = to_float(vd[i * Sh::vpitch]);
+                } else {
+                    walk_fetch(u, v, p.v_tok, ws->rows[c % 3] + half * 32, live);
+                }
                 mbar_wait(bar.done, par, &ws->dead);
                 tc_fence_after();
                 tc_ld32(tl + cKS + half * 32, x);
@@ -1192,7 +1221,10 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_scan_kernel(const DeltaPa
                 tc_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 32; ++i) x[i] += o[i];
-                walk_store(y, p.y_tok, ws->rows[c % 3] + half * 32, vd, Sh::vpitch, p.dv - vc + lane, lane, x);
+                if constexpr (NP == 1)
+                    walk_store(y, p.y_tok, ws->rows[c % 3] + half * 32, vd, Sh::vpitch, p.dv - vc + lane, lane, x);
+                else
+                    walk_put(y + lane, p.y_tok, ws->rows[c % 3] + half * 32, live, x);
             }
             mbar_arrive(bar.empty + 8 * st);
         }

@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaP
             for (int n = 0; n < chunks; ++n) {
                 const int st = STAGES == 2 ? n & 1 : 0;
                 const uint32_t bK = static_cast<uint32_t>(__cvta_generic_to_shared(stages + st * STAGE));
-                const uint64_t dK = tc_desc(bK), dQ = tc_desc(bK + Sh::oQ), dT = tc_desc(bK + Sh::oT), dP = tc_desc(bK + Sh::oP);
+                const uint64_t dK = tc_desc(bK + Sh::oK(3)), dQ = tc_desc(bK + Sh::oQ(3)), dT = tc_desc(bK + Sh::oT), dP = tc_desc(bK + Sh::oP);
                 mbar_wait(bar.full + 8 * st, (n / STAGES) & 1, &ws->dead);
                 bar_sync(1, DW_COMPUTE + 32);
                 tc_fence_after();
@@ -131,13 +131,15 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaP
                     unsigned char* base = stages + st * STAGE;
                     const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(base)), full = bar.full + 8 * st;
                     const size_t rec = (size_t)(s.slot + chunks - 1 - n) * p.heads_v + head;
-                    walk_load<DKP>(base, k, p.k_tok, rows, p.dk, ht);
-                    walk_load<DKP>(base + Sh::oQ, q, p.q_tok, rows, p.dk, ht);
-                    walk_load_values(reinterpret_cast<T*>(base + Sh::oV(3)), Sh::vpitch, dy, p.y_tok, rows, dvs, ht);
+                    if constexpr (NP == 1) {
+                        walk_load<DKP>(base + Sh::oK(3), k, p.k_tok, rows, p.dk, ht);
+                        walk_load<DKP>(base + Sh::oQ(3), q, p.q_tok, rows, p.dk, ht);
+                        walk_load_values(reinterpret_cast<T*>(base + Sh::oV(3)), Sh::vpitch, dy, p.y_tok, rows, dvs, ht);
+                    }
                     uint32_t bytes = 0;
                     if (ht == 0) {
-                        bytes = DL_VECS * 4 + 6 * TC_TILE;
-                        bulk_in(at + Sh::oVec, record_vec(p, rec), bytes, full);
+                        bytes = DL_VECS * 4 + 6 * TC_TILE + (NP == 1 ? 0 : 2 * NP * Sh::plane);
+                        bulk_in(at, record_vec<T, DKP>(p, rec), bytes, full);
                     }
                     return bytes;
                 });
@@ -147,6 +149,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaP
         const int half = warp >> 2, row = (warp & 3) * 32 + lane, vc = slice + row;
         const bool live = vc < p.dv;
         const uint32_t tl = tm + ((uint32_t)(warp & 3) << 21);
+        const T* dy = reinterpret_cast<const T*>(p.dy) + delta_img(p, b) * p.y_img + (long long)head * p.dv + vc;
         T* dvalue = reinterpret_cast<T*>(p.dvalue);
         if (dvalue) dvalue += (delta_img(p, b) * p.tokens * p.heads_v + head) * (long long)p.dv + vc - lane;
         float S[HS];  // dS^T[row][half * HS + i]
@@ -163,12 +166,18 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaP
             const int st = STAGES == 2 ? n & 1 : 0;
             const uint32_t par = n & 1;
             T* vd = reinterpret_cast<T*>(stages + st * STAGE + Sh::oV(3)) + half * 32 * Sh::vpitch + row;
-            const float* vec = reinterpret_cast<const float*>(stages + st * STAGE + Sh::oVec) + half * 32;
+            const float* vec = reinterpret_cast<const float*>(stages + st * STAGE) + half * 32;
             const size_t rec = (size_t)(s.slot + chunks - 1 - n) * p.heads_v + head;
             float o[32], x[32];
             mbar_wait(bar.full + 8 * st, (n / STAGES) & 1, &ws->dead);
+            if constexpr (NP == 1) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = o[i] = to_float(vd[i * Sh::vpitch]);
+                for (int i = 0; i < 32; ++i) o[i] = to_float(vd[i * Sh::vpitch]);
+            } else {
+                walk_fetch(o, dy, p.y_tok, ws->rows[n % 3] + half * 32, live);
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = o[i];
             put_terms<NP>(tl + cA + half * (NP * 16), 16, x);
             walk_ready(2);
             if (live) {  // the gradient of the state leaving the chunk
@@ -211,8 +220,13 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaP
                 put_terms<3>(tl + cW + half * 48, 16, u);
             }
             walk_ready(5);
-            if (dvalue)
-                walk_store(dvalue, (long long)p.heads_v * p.dv, ws->rows[n % 3] + half * 32, vd, Sh::vpitch, p.dv - vc + lane, lane, x);
+            if (dvalue) {
+                if constexpr (NP == 1)
+                    walk_store(dvalue, (long long)p.heads_v * p.dv, ws->rows[n % 3] + half * 32, vd, Sh::vpitch, p.dv - vc + lane,
+                               lane, x);
+                else
+                    walk_put(dvalue + lane, (long long)p.heads_v * p.dv, ws->rows[n % 3] + half * 32, live, x);
+            }
             const float eC = vec[3 * DL_C - half * 32];
             mbar_wait(bar.done + 16, par, &ws->dead);
             tc_fence_after();
@@ -395,7 +409,7 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
         mbar_fence_init();
     }
     if (tid < DL_C) sh->rows[tid] = delta_row(p, s, t0 + tid);
-    if (tid < DL_VECS / 4) reinterpret_cast<float4*>(sh->vec)[tid] = __ldg(reinterpret_cast<const float4*>(record_vec(p, rec)) + tid);
+    if (tid < DL_VECS / 4) reinterpret_cast<float4*>(sh->vec)[tid] = __ldg(reinterpret_cast<const float4*>(record_vec<T, DKP>(p, rec)) + tid);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -549,7 +563,7 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
         float e[32], f[32];
         tc_ld32(tl + c2 + j0, e);
         if (part == 0) {  // P, whole again
-            const __nv_bfloat16* wP = record_P(p, rec);
+            const __nv_bfloat16* wP = record_P<T, DKP>(p, rec);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 float z[8] = {};
@@ -596,7 +610,7 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
             const float2 gj = G[j0 + k];
-            const float d = expf((gi.x - gj.x) + (gi.y - gj.y));
+            const float d = decay_between(gi, gj);
             e[k] = j0 + k <= i - part ? factor * (d * e[k]) : 0.f;
         }
         unsigned char* o = tiles + Sh::oX + part * TC_TILE;
