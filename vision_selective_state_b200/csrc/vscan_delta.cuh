@@ -249,9 +249,14 @@ __device__ __forceinline__ void mma_terms(float (&c0)[4], float (&c1)[4], const 
     }
 }
 
-// e^{G_i - G_j} from running sums held as a rounded value and the rest of it. (ex2 is good to
-// 2^-22; the product with log2 e rounds by 2^-24 of an exponent whose power is small where it is large.)
-__device__ __forceinline__ float decay_between(float2 gi, float2 gj) { return fast_exp2(((gi.x - gj.x) + (gi.y - gj.y)) * LOG2E); }
+// e^{G_i - G_j} from running sums held as a rounded value and the rest of it. FAST: by ex2, good
+// to 2^-22, for what leaves in bf16.
+template <bool FAST>
+__device__ __forceinline__ float decay_between(float2 gi, float2 gj)
+{
+    const float d = (gi.x - gj.x) + (gi.y - gj.y);
+    return FAST ? fast_exp2(d * LOG2E) : expf(d);
+}
 
 // ---- tiles ------------------------------------------------------------------------
 template <typename T> struct DeltaIo;
@@ -609,7 +614,7 @@ __global__ void __launch_bounds__(DP_THREADS) delta_prep_kernel(const DeltaParam
                 const int i = r0 + half * 8;
                 const float2 gi = G[i];
                 // selected, not multiplied by zero: what lies above the diagonal is not looked at
-                const float d0 = decay_between(gi, gj0), d1 = decay_between(gi, gj1);
+                const float d0 = decay_between<false>(gi, gj0), d1 = decay_between<false>(gi, gj1);
                 put(i, half, m0 / 8 + n, j < i + group ? d0 * diag[n][half * 2] : 0.f,
                     j + 1 < i + group ? d1 * diag[n][half * 2 + 1] : 0.f);
             }
@@ -907,17 +912,17 @@ __device__ __forceinline__ void put_state(uint32_t addr, const float (&S)[HS])
     }
 }
 
-// All products of order up to ORD of an operand of NA terms in tensor memory with NB
-// planes in shared memory, small ones first: they add up before the large ones
+// All products of orders ORD down to LEAST of an operand of NA terms in tensor memory with
+// NB planes in shared memory, small ones first: they add up before the large ones
 // truncate the accumulator at their own size. mma(x, y, k, add) issues slice k (from
 // FIRST on, cyclically) of term x with plane y.
-template <int NA, int NB, int ORD, int KS, int FIRST, typename F>
+template <int NA, int NB, int ORD, int KS, int FIRST, int LEAST = 0, typename F>
 __device__ __forceinline__ void tc_product(bool add, F mma)
 {
     // unrolled, constants and all: a product issues in its 32 cycles or less; rolled it took 70
 #pragma unroll
-    for (int o = ORD; o >= 0; --o)
-#pragma unroll(NB == 1 ? 1 : 1)
+    for (int o = ORD; o >= LEAST; --o)
+#pragma unroll 1
         for (int y = o < NA ? 0 : o - NA + 1; y <= o && y < NB; ++y) {
 #pragma unroll
             for (int k = 0; k < KS; ++k) {

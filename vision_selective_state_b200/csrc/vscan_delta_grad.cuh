@@ -98,22 +98,28 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaP
                     tc_commit(bar.done + 8);
                 }
                 __syncwarp();
-                auto state = [&](auto a, uint64_t t, bool more) {
-#pragma unroll
-                    for (int nb = 0; nb < Sh::KB; ++nb)
-                        tc_product<3, NP, 2, 4, 0>(more, [&](int x, int y, int ks, bool add) {
-                            tc_mma(tm + cDS + nb * (3 * Sh::SC), a(x, ks),
-                                   t + (y * Sh::plane + nb * TC_TILE + ks * 2048) / 16, tc_idesc(64, true), add);
-                        });
+                // small terms of both parts before the large ones of either
+                auto part = [&](auto a, uint64_t t, int nb) {
+                    return [=](int x, int y, int ks, bool add) {
+                        tc_mma(tm + cDS + nb * (3 * Sh::SC), a(x, ks), t + (y * Sh::plane + nb * TC_TILE + ks * 2048) / 16,
+                               tc_idesc(64, true), add);
+                    };
                 };
                 bar_sync(4, DW_COMPUTE + 32);
                 tc_fence_after();
-                if (tc_elect()) state(aQ, dQ, false);  // 3
+                if (tc_elect())  // 3
+#pragma unroll
+                    for (int nb = 0; nb < Sh::KB; ++nb) tc_product<3, NP, 2, 4, 0, 1>(false, part(aQ, dQ, nb));
                 __syncwarp();
                 bar_sync(5, DW_COMPUTE + 32);
                 tc_fence_after();
                 if (tc_elect()) {
-                    state(aW, dK, true);
+#pragma unroll
+                    for (int nb = 0; nb < Sh::KB; ++nb) {
+                        tc_product<3, NP, 2, 4, 0, 1>(true, part(aW, dK, nb));
+                        tc_product<3, NP, 0, 4, 0>(true, part(aQ, dQ, nb));
+                        tc_product<3, NP, 0, 4, 0>(true, part(aW, dK, nb));
+                    }
                     tc_commit(bar.done + 16);
                 }
                 __syncwarp();
@@ -369,7 +375,9 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
 {
     using Sh = GradShape<T, DKP>;
     constexpr int NP = Sh::NP;
-    constexpr int c1 = 0, c2 = 128, c3 = 192, cKT = 256, cQT = cKT + NP * 32;  // tensor-memory columns
+    // tensor-memory columns; what D1 .. D3 get from the smaller terms is summed apart, cSmall further on
+    // (one accumulator over several slabs would be truncated by each of them), and K^T and Q^T follow there
+    constexpr int c1 = 0, c2 = 128, c3 = 192, cSmall = 256, cKT = 256, cQT = cKT + NP * 32;
     extern __shared__ unsigned char smem_raw[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = warp >> 2;
     const int head = blockIdx.y, hk = head / p.group;
@@ -425,26 +433,34 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
             bar_sync(1, DG_THREADS);
             tc_fence_after();
             if (tc_elect()) {
-                tc_product<3, 3, 2, 4, 0>(more, [&](int x, int y, int ks, bool add) {  // S0 [dO | dV]^T
+                auto d1 = [&](int x, int y, int ks, bool add) {  // S0 [dO | dV]^T
+                    const uint32_t d = tm + c1 + (x + y ? cSmall : 0);
                     const uint64_t a = aS + (x * Sh::plane + ks * 32) / 16;
                     if (NP == 1 && y > 0)
-                        tc_mma_ss(tm + c1 + 64, a, aX + ((2 * y + 1) * TC_TILE + ks * 32) / 16, tc_idesc(64, false), add);
+                        tc_mma_ss(d + 64, a, aX + ((2 * y + 1) * TC_TILE + ks * 32) / 16, tc_idesc(64, false), add);
                     else
-                        tc_mma_ss(tm + c1, a, aX + (2 * y * TC_TILE + ks * 32) / 16, tc_idesc(128, false), add);
-                });
+                        tc_mma_ss(d, a, aX + (2 * y * TC_TILE + ks * 32) / 16, tc_idesc(128, false), add);
+                };
+                tc_product<3, 3, 2, 4, 0, 1>(more, d1);
+                tc_product<3, 3, 0, 4, 0>(more, d1);
                 tc_commit(done);
-                tc_product<3, 3, 2, 4, 0>(more, [&](int x, int y, int ks, bool add) {  // [dO | dV] W^T
-                    tc_mma_ss(tm + c2, aX + (2 * x * TC_TILE + ks * 32) / 16, bW + (y * TC_TILE + ks * 32) / 16, tc_idesc(64, false),
+                auto d2 = [&](int x, int y, int ks, bool add) {  // [dO | dV] W^T
+                    tc_mma_ss(tm + c2 + (x + y ? cSmall : 0), aX + (2 * x * TC_TILE + ks * 32) / 16, bW + (y * TC_TILE + ks * 32) / 16, tc_idesc(64, false),
                               add);
-                });
+                };
+                tc_product<3, 3, 2, 4, 0, 1>(more, d2);
+                tc_product<3, 3, 0, 4, 0>(more, d2);
             }
             __syncwarp();
             bar_sync(2, DG_THREADS);
             tc_fence_after();
             if (tc_elect()) {
-                tc_product<3, 3, 2, 4, 0>(more, [&](int x, int y, int ks, bool add) {  // dS W^T
-                    tc_mma_ss(tm + c3, aS + (x * Sh::plane + ks * 32) / 16, bW + (y * TC_TILE + ks * 32) / 16, tc_idesc(64, false), add);
-                });
+                auto d3 = [&](int x, int y, int ks, bool add) {  // dS W^T
+                    tc_mma_ss(tm + c3 + (x + y ? cSmall : 0), aS + (x * Sh::plane + ks * 32) / 16,
+                              bW + (y * TC_TILE + ks * 32) / 16, tc_idesc(64, false), add);
+                };
+                tc_product<3, 3, 2, 4, 0, 1>(more, d3);
+                tc_product<3, 3, 0, 4, 0>(more, d3);
                 tc_commit(done);
             }
             __syncwarp();
@@ -455,12 +471,16 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
             tc_product<NP, 3, 2, 4, 0>(false, [&](int x, int y, int ks, bool add) {  // K^T [E | M]^T
                 tc_mma(tm + c1, aK(x, ks), aX + (2 * y * TC_TILE + ks * 32) / 16, tc_idesc(128, false), add);
             });
-            tc_product<NP, 3, 2, 4, 0>(false, [&](int x, int y, int ks, bool add) {  // Q^T E
+            auto qe = [&](int x, int y, int ks, bool add) {  // Q^T E
                 tc_mma(tm + c3, tm + cQT + x * 32 + ks * 8, aX + (2 * y * TC_TILE + ks * 2048) / 16, tc_idesc(64, true), add);
-            });
-            tc_product<NP, 3, 2, 4, 0>(true, [&](int x, int y, int ks, bool add) {  // + K^T M
+            };
+            auto km = [&](int x, int y, int ks, bool add) {  // K^T M
                 tc_mma(tm + c3, aK(x, ks), aX + ((2 * y + 1) * TC_TILE + ks * 2048) / 16, tc_idesc(64, true), add);
-            });
+            };
+            tc_product<NP, 3, 2, 4, 0, 1>(false, qe);
+            tc_product<NP, 3, 2, 4, 0, 1>(true, km);
+            tc_product<NP, 3, 0, 4, 0>(true, qe);
+            tc_product<NP, 3, 0, 4, 0>(true, km);
             tc_commit(done);
         }
         __syncwarp();
@@ -562,6 +582,10 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
         const int part = (warp >> 1) & 1, i = (warp & 1) * 32 + lane, j0 = half * 32;
         float e[32], f[32];
         tc_ld32(tl + c2 + j0, e);
+        tc_ld32(tl + c2 + cSmall + j0, f);
+        tc_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; ++k) e[k] += f[k];
         if (part == 0) {  // P, whole again
             const __nv_bfloat16* wP = record_P<T, DKP>(p, rec);
 #pragma unroll
@@ -588,7 +612,6 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
                 f[4 * q] = -u.x; f[4 * q + 1] = -u.y; f[4 * q + 2] = -u.z; f[4 * q + 3] = -u.w;
             }
         }
-        tc_wait_ld();
         // a step's own product carries no decay: it is no part of dg. Blocks above the diagonal
         // hold nothing: selected, not multiplied by zero
         double sum = 0.0, col = 0.0;
@@ -610,36 +633,34 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
             const float2 gj = G[j0 + k];
-            const float d = decay_between(gi, gj);
+            const float d = decay_between<NP == 1>(gi, gj);
             e[k] = j0 + k <= i - part ? factor * (d * e[k]) : 0.f;
         }
         unsigned char* o = tiles + Sh::oX + part * TC_TILE;
 #pragma unroll
         for (int k = 0; k < 32; k += 4) put_planes(o, 2 * TC_TILE, i, j0 + k, make_float4(e[k], e[k + 1], e[k + 2], e[k + 3]));
     }
-    // K^T (half 0) and Q^T: this thread's key channel, all steps
+    // D1 and D3, scaled, and their part of dg
     const int dk = (warp & 3) * 32 + lane;
     const bool live = dk < DKP;  // DKP = 64: the upper two warps of each four idle here
-    {
-        const unsigned char* tile = tiles + (half ? Sh::oQ : Sh::oK);
-        const uint32_t to = tl + (half ? cQT : cKT);
-        if ((warp & 3) * 32 < DKP) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float x[32];
-                column_of<NP, DKP>(tile, Sh::plane, dk, h * 32, x);
-                put_terms<NP, NP == 3>(to + h * 16, 32, x);
-            }
-        }
-    }
-    // D1 and D3, scaled, and their part of dg
     float dq[32], dkr[32], dkc[32];
-    tc_ld32(tl + c1 + half * 32, dq);
-    tc_ld32(tl + c1 + 64 + half * 32, dkr);
-    tc_ld32(tl + c3 + half * 32, dkc);
-    tc_wait_ld();
     {
         float u[32], x[32];
+        tc_ld32(tl + c1 + half * 32, dq);
+        tc_ld32(tl + c1 + cSmall + half * 32, x);
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) dq[i] += x[i];
+        tc_ld32(tl + c1 + 64 + half * 32, dkr);
+        tc_ld32(tl + c1 + cSmall + 64 + half * 32, x);
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) dkr[i] += x[i];
+        tc_ld32(tl + c3 + half * 32, dkc);
+        tc_ld32(tl + c3 + cSmall + half * 32, x);
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) dkc[i] += x[i];
         if (live) column_of<NP, DKP>(tiles + Sh::oQ, Sh::plane, dk, half * 32, x);
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
@@ -657,9 +678,24 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
         for (int i = 0; i < 32; ++i) x[i] = live ? x[i] * dkc[i] : 0.f;
         sh->V[warp & 3][half * 32 + lane] = reduce_columns(x, lane);
     }
+    tc_fence_before();
+    bar_sync(4, 256);  // the parts of dg are there, and the columns behind cSmall read
+    tc_fence_after();
+    // K^T (half 0) and Q^T: this thread's key channel, all steps
+    {
+        const unsigned char* tile = tiles + (half ? Sh::oQ : Sh::oK);
+        const uint32_t to = tl + (half ? cQT : cKT);
+        if ((warp & 3) * 32 < DKP) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float x[32];
+                column_of<NP, DKP>(tile, Sh::plane, dk, h * 32, x);
+                put_terms<NP, NP == 3>(to + h * 16, 32, x);
+            }
+        }
+    }
     tc_wait_st();
     ready(3);
-    bar_sync(4, 256);  // the parts of dg are there
     if (warp == 7) {  // dg, two steps a lane; then a, b and the sums for A and bias
         double x[2], v[2], base = 0.0;
         for (int w = 0; w < 8; ++w) base += (double)sh->red[w];
