@@ -255,3 +255,85 @@ def test_steps_continue_a_chunked_pass():
     ry, rS = R.delta_ref(x)
     R.close(torch.cat(ys, 1), ry, "f32", R.ACC_FORWARD, "y")
     R.close(S, rS, "f32", R.ACC_FORWARD, "state")
+
+
+# ------------------------------------------------------------------ calls that are easy to get wrong
+def test_offsets_that_make_no_sense_stay_inside_their_arrays():
+    """Decreasing, negative and too large offsets are clamped: the call ends, and what lies around
+    its outputs is as it was (the outputs themselves are not defined)."""
+    n, hv, d = 200, 2, 32
+    x = f32(R.delta_inputs(14, 1, n, 1, hv, d, d, "bf16"))
+    d_ = to_gpu(x, "bf16")
+    around = torch.full((1, n + 128, hv, d), 5.0, device=DEV, dtype=torch.bfloat16)
+    for offsets in ([0, 300, -7, 150], [150, 100, 50, 0], [-100, -1, 2 ** 31 - 1, 3], [200, 200, 200, 200]):
+        off = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+        states = torch.full((5, hv, d, d), 9.0, device=DEV)
+        vs.delta_forward(*(d_[m] for m in ("q", "k", "v", "a", "b", "A", "bias")), seq_offsets=off,
+                         out=around[:, 64:64 + n], final_state=states[1:4])
+        torch.cuda.synchronize()
+        assert (around[:, :64] == 5.0).all() and (around[:, 64 + n:] == 5.0).all()
+        assert (states[0] == 9.0).all() and (states[4] == 9.0).all()
+        got = vs.delta_backward(*(d_[m] for m in ("q", "k", "v", "a", "b", "A", "bias")), seq_offsets=off, dy=d_["v"])
+        torch.cuda.synchronize()
+        assert got["dq"].shape == d_["q"].shape
+
+
+def test_two_calls_at_once_and_graphs_that_share_a_workspace():
+    xs = [to_gpu(f32(R.delta_inputs(seed, 1, 700, 2, 2, 64, 64, "bf16")), "bf16") for seed in (15, 16)]
+    args = [[d[n] for n in ("q", "k", "v", "a", "b", "A", "bias")] for d in xs]
+    want = [vs.delta_forward(*a) for a in args]
+    streams = [torch.cuda.Stream() for _ in args]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [vs.delta_forward(*a, stream=s) for a, s in zip(args, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
+    # one workspace, two captured calls, replayed in turn on one stream
+    workspace = torch.empty(32 << 20, dtype=torch.uint8, device=DEV)
+    held, graphs = [], []
+    for a in args:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            held.append(vs.delta_forward(*a, workspace=workspace))
+        graphs.append(graph)
+    for _ in range(3):
+        for graph in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(h, w) for h, w in zip(held, want))
+
+
+def test_image_strides_beyond_32_bits():
+    batch, n, h, d = 2, 66, 1, 16
+    x = f32(R.delta_inputs(17, batch, n, h, h, d, d, "bf16"))
+    dd = to_gpu(x, "bf16")
+    stride = 2 ** 31 + 64
+    far = torch.empty(stride + n * h * d, dtype=torch.bfloat16, device=DEV)
+    views = {}
+    for m in ("q", "v"):  # one buffer each in turn would be larger: q and v share it, at different places
+        at = 0 if m == "q" else n * h * d
+        views[m] = torch.as_strided(far, (batch, n, h, d), (stride - n * h * d, h * d, d, 1), at)
+        views[m].copy_(dd[m])
+    near = vs.delta_forward(*(dd[m] for m in ("q", "k", "v", "a", "b", "A", "bias")))
+    got = vs.delta_forward(views["q"], dd["k"], views["v"], dd["a"], dd["b"], dd["A"], dd["bias"])
+    assert torch.equal(near, got)
+
+
+def test_a_later_token_does_not_touch_an_earlier_chunk():
+    x = f32(R.delta_inputs(18, 1, 192, 1, 1, 32, 32, "f32"))
+    d = to_gpu(x, "f32")
+    args = lambda: [d[n] for n in ("q", "k", "v", "a", "b", "A", "bias")]  # noqa: E731
+    first = vs.delta_forward(*args())
+    for n in ("q", "k", "v"):
+        d[n][:, 130:] = float("inf")
+    second = vs.delta_forward(*args())
+    assert torch.equal(first[:, :128], second[:, :128])
+
+
+def test_one_head_shared_by_many_and_sizes_at_the_limits():
+    for hk, hv, dk, dv in ((1, 7, 128, 256), (1, 1, 4, 4), (3, 3, 64, 4), (1, 2, 128, 132)):
+        x = f32(R.delta_inputs(hv + dk, 1, 67, hk, hv, dk, dv, "f32"))
+        y, S = run(x, "f32", final_state=True)
+        ry, rS = R.delta_ref(x)
+        R.close(y, ry, "f32", R.ACC_FORWARD, f"y {hk} {hv} {dk} {dv}")
+        R.close(S, rS, "f32", R.ACC_FORWARD, "state")
