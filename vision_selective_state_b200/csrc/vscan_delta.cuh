@@ -196,7 +196,9 @@ __device__ __forceinline__ Frag4 load_b_t(const __nv_bfloat16* t, int pitch, int
 __device__ __forceinline__ uint32_t split_bf16(float& x, float& y)
 {
     const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
-    const float2 r = __fadd2_rn(make_float2(x, y), make_float2(-__uint_as_float(a & 0xffff0000u), -__uint_as_float(b & 0xffff0000u)));
+    // a packed subtraction, as a product with -1: a packed sum has no sign of its own for an operand
+    const float2 r = __ffma2_rn(make_float2(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u)),
+                                make_float2(-1.f, -1.f), make_float2(x, y));
     x = r.x;
     y = r.y;
     return __byte_perm(a, b, 0x7632);
@@ -746,13 +748,15 @@ __global__ void __launch_bounds__(DP_THREADS) delta_prep_kernel(const DeltaParam
 // The chain KS -> W -> dS -> S bounds the walk, so everything else is off it: eight
 // warps compute, one thread issues the products (the ones of the chain first), three
 // warps copy the next chunks' tiles in, and a computing thread never waits for
-// another one, only for products. y of a chunk is finished while the next one's KS runs. T and P are lower triangles: slice ks of their summed
+// another one, only for products. y of a chunk is finished while the next one waits for W. T and P are lower triangles: slice ks of their summed
 // index touches the columns from 16 ks on only.
 // Tensor-memory columns: S terms (over them dS, once step 1 is done), KS (W, then W's
 // terms for O), QS, X's terms (then those of e^{G_C - G} W), O.
 constexpr int DW_COMPUTE = 256, DW_HELP = 96, DW_THREADS = 384;  // warps 0-7, 9-11, all (warp 8 issues)
 // Registers a thread: 384 x 168 at launch, split 200 / 96: 256 x 200 + 128 x 96 = 63488 of 64512.
 constexpr int DW_REGS_COMPUTE = 200, DW_REGS_HELP = 96;
+
+constexpr int WALK_FRONT = 2048;  // bytes in front of the stages, of WalkShared
 
 template <typename T, int DKP>
 struct WalkShape {
@@ -772,10 +776,11 @@ struct WalkShape {
     {
         return (oV(pplanes) + (NP == 1 ? DL_C * vpitch * (int)sizeof(T) : 0) + 1023) / 1024 * 1024;
     }
+    static constexpr int out = NP == 1 ? DL_C * vpitch * (int)sizeof(T) : 0;  // behind the stages: y's (dV's) way out
     // at least half of the SM's shared memory: one CTA an SM, which owns all tensor memory
     static __host__ __device__ constexpr size_t smem(int pplanes)
     {
-        const size_t n = 1024 + 1024 + (size_t)STAGES * stage(pplanes);
+        const size_t n = 1024 + WALK_FRONT + (size_t)STAGES * stage(pplanes) + out;
         return n < 120 * 1024 ? 120 * 1024 : n;
     }
     // tensor-memory columns of one term of half a row of S (DKP / 2 values)
@@ -852,11 +857,14 @@ __device__ __forceinline__ void stage_two(__nv_bfloat16* p, int pitch, float x, 
     p[pitch] = __high2bfloat16(h);
 }
 template <typename T>
-__device__ __forceinline__ void walk_store(T* dst, long long tok, const int* rows, T* mine, int pitch, int have, int lane,
-                                           const float (&x)[32])
+__device__ __forceinline__ void walk_stage(T* mine, int pitch, const float (&x)[32])
 {
 #pragma unroll
     for (int i = 0; i < 32; i += 2) stage_two(mine + i * pitch, pitch, x[i], x[i + 1]);
+}
+template <typename T>
+__device__ __forceinline__ void walk_flush(T* dst, long long tok, const int* rows, const T* mine, int pitch, int have, int lane)
+{
     __syncwarp();
     constexpr int V = 16 / sizeof(T), vecs = 32 / V, per = 32 / vecs;  // pieces of a row, rows at a time
     const int c = lane % vecs * V;
@@ -867,6 +875,14 @@ __device__ __forceinline__ void walk_store(T* dst, long long tok, const int* row
             const int r = i + lane / vecs, row = rows[r];
             if (row >= 0) *reinterpret_cast<uint4*>(dst + row * tok + c) = *reinterpret_cast<const uint4*>(src + r * pitch);
         }
+    __syncwarp();
+}
+template <typename T>
+__device__ __forceinline__ void walk_store(T* dst, long long tok, const int* rows, T* mine, int pitch, int have, int lane,
+                                           const float (&x)[32])
+{
+    walk_stage(mine, pitch, x);
+    walk_flush(dst, tok, rows, mine, pitch, have, lane);
 }
 
 // NT bf16 terms of 32 values of a row, term n in the 16 columns from addr + n * step on. Three
@@ -937,8 +953,9 @@ struct WalkShared {
     unsigned long long full[2], empty[2], done[5];
     uint32_t tmem;
     int dead;
-    alignas(16) int rows[3][DL_C];  // token rows of chunk c in slot c mod 3
+    alignas(16) int rows[4][DL_C];  // token rows of chunk c in slot c mod 4
 };
+static_assert(sizeof(WalkShared) <= WALK_FRONT, "shared memory in front of the stages");
 
 struct WalkBars {
     uint32_t full, empty, done;  // shared addresses; 8 bytes apart
@@ -985,11 +1002,12 @@ __device__ __forceinline__ void walk_copy(WalkShared* w, const WalkBars& bar, in
 {
     for (int n = 0; n < chunks; ++n) {
         const int st = STAGES == 2 ? n & 1 : 0;
-        // chunk n - 3, the last user of this slot, is done: the wait for chunk n - 1 - STAGES saw to it
-        if (tid < DL_C) w->rows[n % 3][tid] = row_of(n, tid);
+        // chunk n - 4, the last user of this slot, has left: its y goes before chunk n - 3 is done, for
+        // which the last round waited
+        if (tid < DL_C) w->rows[n % 4][tid] = row_of(n, tid);
         bar_sync(7, DW_HELP);
         if (n >= STAGES) mbar_wait(bar.empty + 8 * st, ((n - STAGES) / STAGES) & 1, &w->dead);
-        const uint32_t bytes = in(n, st, w->rows[n % 3]);
+        const uint32_t bytes = in(n, st, w->rows[n % 4]);
         cp_async_commit();
         cp_async_wait<0>();
         tc_fence_smem();
@@ -1016,7 +1034,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_scan_kernel(const DeltaPa
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + (1024 - (__cvta_generic_to_shared(smem_raw) & 1023)) % 1024;
     WalkShared* ws = reinterpret_cast<WalkShared*>(smem);
-    unsigned char* stages = smem + 1024;
+    unsigned char* stages = smem + WALK_FRONT;
     constexpr int STAGE = Sh::stage(PP);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int head = blockIdx.y, b = blockIdx.z;
@@ -1138,10 +1156,33 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_scan_kernel(const DeltaPa
             put_state<HS, Sh::SC>(tl + cS + half * 3 * Sh::SC, S);
             walk_ready(1);
         }
+        // y of chunk c, which waits in `o` (its part from the entering state) and O: a chunk later, while the
+        // chain waits for W and then for dS, so that it delays little
+        float o[SAVE ? 1 : 32];
+        T* corner = reinterpret_cast<T*>(stages + STAGES * STAGE) + half * 32 * Sh::vpitch + row;
+        auto put_y = [&](int c) {
+            float x[32];
+            mbar_wait(bar.done + 32, c & 1, &ws->dead);
+            tc_fence_after();
+            tc_ld32(tl + cO + half * 32, x);
+            tc_wait_ld();
+            if constexpr (!SAVE) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] += o[i];
+                if constexpr (NP == 1)
+                    walk_stage(corner, Sh::vpitch, x);
+                else
+                    walk_put(y + lane, p.y_tok, ws->rows[c % 4] + half * 32, live, x);
+            }
+        };
+        auto flush_y = [&](int c) {
+            if constexpr (!SAVE && NP == 1)
+                walk_flush(y, p.y_tok, ws->rows[c % 4] + half * 32, corner, Sh::vpitch, p.dv - vc + lane, lane);
+        };
         for (int c = 0; c < chunks; ++c) {
             const int st = STAGES == 2 ? c & 1 : 0;
             const uint32_t par = c & 1;
-            T* vd = reinterpret_cast<T*>(stages + st * STAGE + Sh::oV(PP)) + half * 32 * Sh::vpitch + row;
+            const T* vd = reinterpret_cast<const T*>(stages + st * STAGE + Sh::oV(PP)) + half * 32 * Sh::vpitch + row;
             const float* vec = reinterpret_cast<const float*>(stages + st * STAGE) + half * 32;
             const size_t rec = (size_t)(s.slot + c) * p.heads_v + head;
             if (SAVE && live) {  // the state entering the chunk, for the gradients
@@ -1149,7 +1190,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_scan_kernel(const DeltaPa
 #pragma unroll
                 for (int i = 0; i < HS; ++i) o[(size_t)(half * HS + i) * p.dv] = S[i];
             }
-            float x[32], o[SAVE ? 1 : 32];
+            float x[32];
             mbar_wait(bar.full + 8 * st, (c / STAGES) & 1, &ws->dead);
             {
                 float u[32];
@@ -1157,7 +1198,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_scan_kernel(const DeltaPa
 #pragma unroll
                     for (int i = 0; i < 32; ++i) u[i] = to_float(vd[i * Sh::vpitch]);
                 } else {
-                    walk_fetch(u, v, p.v_tok, ws->rows[c % 3] + half * 32, live);
+                    walk_fetch(u, v, p.v_tok, ws->rows[c % 4] + half * 32, live);
                 }
                 mbar_wait(bar.done, par, &ws->dead);
                 tc_fence_after();
@@ -1169,6 +1210,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_scan_kernel(const DeltaPa
             put_terms<3>(tl + cX + half * 48, 16, x);
             walk_ready(2);
             if constexpr (!SAVE) {
+                if (c > 0) put_y(c - 1);
                 mbar_wait(bar.done + 8, par, &ws->dead);
                 tc_fence_after();
                 tc_ld32(tl + cQS + half * 32, o);
@@ -1205,6 +1247,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_scan_kernel(const DeltaPa
                 }
                 walk_ready(4);
             }
+            if (c > 0) flush_y(c - 1);
             const float eC = vec[3 * DL_C - half * 32];
             mbar_wait(bar.done + 24, par, &ws->dead);
             tc_fence_after();
@@ -1215,23 +1258,15 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_scan_kernel(const DeltaPa
 #pragma unroll
                 for (int e = 0; e < 32; ++e) S[i + e] = eC * S[i + e] + x[e];
             }
+            mbar_arrive(bar.empty + 8 * st);
             if (c + 1 < chunks) {
                 put_state<HS, Sh::SC>(tl + cS + half * 3 * Sh::SC, S);
                 walk_ready(1);
             }
-            if constexpr (!SAVE) {
-                mbar_wait(bar.done + 32, par, &ws->dead);
-                tc_fence_after();
-                tc_ld32(tl + cO + half * 32, x);
-                tc_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] += o[i];
-                if constexpr (NP == 1)
-                    walk_store(y, p.y_tok, ws->rows[c % 3] + half * 32, vd, Sh::vpitch, p.dv - vc + lane, lane, x);
-                else
-                    walk_put(y + lane, p.y_tok, ws->rows[c % 3] + half * 32, live, x);
-            }
-            mbar_arrive(bar.empty + 8 * st);
+        }
+        if (!SAVE && chunks > 0) {
+            put_y(chunks - 1);
+            flush_y(chunks - 1);
         }
         if (p.s_out && live)
 #pragma unroll

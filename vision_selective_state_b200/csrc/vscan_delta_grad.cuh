@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaP
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + (1024 - (__cvta_generic_to_shared(smem_raw) & 1023)) % 1024;
     WalkShared* ws = reinterpret_cast<WalkShared*>(smem);
-    unsigned char* stages = smem + 1024;
+    unsigned char* stages = smem + WALK_FRONT;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int head = blockIdx.y, b = blockIdx.z;
     const int slice = blockIdx.x * 128;
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaP
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] = to_float(vd[i * Sh::vpitch]);
             } else {
-                walk_fetch(o, dy, p.y_tok, ws->rows[n % 3] + half * 32, live);
+                walk_fetch(o, dy, p.y_tok, ws->rows[n % 4] + half * 32, live);
             }
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] = o[i];
@@ -212,13 +212,11 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaP
             tc_fence_after();
             tc_ld32(tl + c1 + half * 32, x);
             tc_wait_ld();
-            if (live) {
-                float* ox = p.wdX + (rec * DL_C + half * 32) * p.dv + vc;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) ox[(size_t)i * p.dv] = x[i];
+            for (int i = 0; i < 32; ++i) {
+                o[i] = x[i];
+                x[i] *= vec[2 * DL_C + i];  // dV
             }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] *= vec[2 * DL_C + i];  // dV
             {
                 float u[32];
 #pragma unroll
@@ -226,12 +224,17 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaP
                 put_terms<3>(tl + cW + half * 48, 16, u);
             }
             walk_ready(5);
+            if (live) {
+                float* ox = p.wdX + (rec * DL_C + half * 32) * p.dv + vc;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) ox[(size_t)i * p.dv] = o[i];
+            }
             if (dvalue) {
                 if constexpr (NP == 1)
-                    walk_store(dvalue, (long long)p.heads_v * p.dv, ws->rows[n % 3] + half * 32, vd, Sh::vpitch, p.dv - vc + lane,
+                    walk_store(dvalue, (long long)p.heads_v * p.dv, ws->rows[n % 4] + half * 32, vd, Sh::vpitch, p.dv - vc + lane,
                                lane, x);
                 else
-                    walk_put(dvalue + lane, (long long)p.heads_v * p.dv, ws->rows[n % 3] + half * 32, live, x);
+                    walk_put(dvalue + lane, (long long)p.heads_v * p.dv, ws->rows[n % 4] + half * 32, live, x);
             }
             const float eC = vec[3 * DL_C - half * 32];
             mbar_wait(bar.done + 16, par, &ws->dead);

@@ -140,6 +140,11 @@ def _fields(q, k, v, a, b, A, bias, y, direction, seq_offsets, scale, beta_scale
         *_row_strides("b", b, b.is_contiguous()), *head_strides("y", y, y.is_contiguous()))
 
 
+def fresh(t):
+    """An uninitialised dense tensor like t."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
 def _status(status, index):
     if status is None:
         return 0
@@ -161,10 +166,10 @@ def _state_shape(q, v, seq_offsets):
     return (q.shape[0] if seq_offsets is None else seq_offsets.numel() - 1, v.shape[2], q.shape[3], v.shape[3])
 
 
-def _scratch(query, handle, fields, index):
+def _scratch(query, handle, fields, q):
     need = ctypes.c_uint64()
     check(query.fn(handle, _pack(*fields, 0, 0, 0), ctypes.byref(need)))
-    return torch.empty(need.value, dtype=torch.uint8, device=f"cuda:{index}")
+    return q.new_empty(need.value, dtype=torch.uint8)
 
 
 def delta_forward(q, k, v, a, b, A, bias=None, *, route=None, direction=0, seq_offsets=None, scale=None,
@@ -181,16 +186,16 @@ def delta_forward(q, k, v, a, b, A, bias=None, *, route=None, direction=0, seq_o
     status: as in forward().
     """
     if out is None:
-        out = (torch.zeros if _partial(route, seq_offsets) else torch.empty)(v.shape, dtype=v.dtype, device=v.device)
+        out = v.new_zeros(v.shape) if _partial(route, seq_offsets) else fresh(v)
     if final_state is True:
-        final_state = torch.empty(_state_shape(q, v, seq_offsets), dtype=torch.float32, device=q.device)
+        final_state = q.new_empty(_state_shape(q, v, seq_offsets), dtype=torch.float32)
     elif final_state is False:
         final_state = None
     index, fields = _fields(q, k, v, a, b, A, bias, out, direction, seq_offsets, scale, beta_scale, initial_state,
                             final_state)
     handle = _route_handle(route)
     if workspace is None:
-        workspace = _scratch(_abi.delta_workspace_size, handle, fields, index)
+        workspace = _scratch(_abi.delta_workspace_size, handle, fields, q)
     args = _pack(*fields, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _status(status, index))
     with on_device(index):
         check(_abi.delta_forward.fn(handle, args, stream_handle(stream, index, out, final_state, workspace)))
@@ -218,14 +223,14 @@ def delta_backward(q, k, v, a, b, A, bias=None, *, dy, route=None, direction=0, 
     for name in GRADIENTS if want is None else want:
         t = like[name]
         if t is not None:
-            out[name] = torch.empty(t.shape, dtype=t.dtype, device=t.device)
+            out[name] = fresh(t)
             setattr(grads, name, out[name].data_ptr())
     if d_final_state is not None:
         check_dense("d_final_state", d_final_state, _state_shape(q, v, seq_offsets), torch.float32, index)
         grads.d_final_state = d_final_state.data_ptr()
     handle = _route_handle(route)
     if workspace is None:
-        workspace = _scratch(_abi.delta_backward_workspace_size, handle, fields, index)
+        workspace = _scratch(_abi.delta_backward_workspace_size, handle, fields, q)
     grads.workspace, grads.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     args = _pack(*fields, 0, 0, _status(status, index))
     with on_device(index):
@@ -248,7 +253,7 @@ def delta_step(q, k, v, a, b, A, bias=None, *, state, state_out=None, scale=None
     batch, hk, dk = shape
     hv, dv = wide[1:]
     if out is None:
-        out = torch.empty(wide, dtype=dtype, device=v.device)
+        out = fresh(v)
     if state_out is None:
         state_out = state
     check_tensor("k", k, shape, dtype, index)

@@ -16,7 +16,7 @@ import torch
 
 from . import _abi
 from ._abi import VscanQkNormGrads, check
-from .delta import check_dense, check_tensor, device_index, head_strides, on_device, stream_handle
+from .delta import check_dense, check_tensor, device_index, fresh, head_strides, on_device, stream_handle
 
 NORMS = {"l2": 0, "rms": 1}
 
@@ -65,7 +65,7 @@ def qk_norm(q, k, wq=None, wk=None, *, norm="rms", eps=1e-6, inv_freq=None, posi
     """Normalised ("l2": unit length, "rms": unit mean square), weighted and rotated (yq, yk)
     (vscan_qknorm_forward). out: a pair of tensors to write to; (q, k) itself works in place."""
     if out is None:
-        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device), torch.empty(k.shape, dtype=k.dtype, device=k.device))
+        out = (fresh(q), fresh(k))
     index, args = _marshal(q, k, wq, wk, *out, norm, eps, inv_freq, positions)
     with on_device(index):
         check(_abi.qknorm_forward.fn(args, stream_handle(stream, index, *out)))
@@ -87,13 +87,13 @@ def qk_norm_backward(q, k, wq=None, wk=None, *, dyq, dyk, norm="rms", eps=1e-6, 
     for name in want:
         t = like[name]
         if t is not None:
-            out[name] = torch.empty(t.shape, dtype=t.dtype, device=t.device)
+            out[name] = fresh(t)
             setattr(grads, name, out[name].data_ptr())
     workspace = None
     if "dwq" in out or "dwk" in out:
         need = ctypes.c_uint64()
         check(_abi.qknorm_backward_workspace_size.fn(args, ctypes.byref(need)))
-        workspace = torch.empty(need.value, dtype=torch.uint8, device=q.device)
+        workspace = q.new_empty(need.value, dtype=torch.uint8)
         grads.workspace, grads.workspace_bytes = workspace.data_ptr(), need.value
     with on_device(index):
         check(_abi.qknorm_backward.fn(args, ctypes.byref(grads), stream_handle(stream, index, workspace, *out.values())))
