@@ -199,7 +199,7 @@ cudaError_t launch_prep(const DeltaParams& p, cudaStream_t stream)
 {
     if (p.slots == 0 || p.tokens == 0) return cudaSuccess;
     static int done[kAttrDevices];
-    constexpr size_t smem = vscan::PrepShape<T, DKP>::smem(PP);
+    constexpr size_t smem = vscan::PrepShape<T, DKP>::smem;
     cudaError_t e = set_smem_once(vscan::delta_prep_kernel<T, DKP, PP>, (int)smem, done, kAttrDevices);
     if (e != cudaSuccess) return e;
     vscan::delta_prep_kernel<T, DKP, PP><<<dim3((unsigned)p.slots, p.heads_v), vscan::DP_THREADS, smem, stream>>>(p);

@@ -376,9 +376,10 @@ __device__ __forceinline__ void copy_rows(const int* rows, int tid, F copy)
 // entry subtracted from all later ones at once), merged twice:
 //   [A 0; C B]^-1 = [A^-1 0; -B^-1 C A^-1 B^-1].
 // L and T's blocks lie transposed as well, so that four rows of a left factor are one
-// 16-byte read. The record is assembled in shared memory, in the walks' swizzled
-// layout, and leaves in two bulk copies; blocks above the diagonal hold nothing, and
-// nothing reads them.
+// 16-byte read. The decays and T are assembled in shared memory, in the walks' swizzled
+// layout, and leave in one bulk copy; P goes out directly, which leaves shared memory
+// for three CTAs an SM instead of two (bf16). Blocks above the diagonal hold nothing,
+// and nothing reads them.
 constexpr int DP_THREADS = 256;
 constexpr int DP_LP = 68, DP_TP = 36;  // row pitches of L^T and of the 32 x 32 blocks of T
 
@@ -391,12 +392,8 @@ struct PrepShape {
     static constexpr int image = DL_VECS * 4 + 3 * DL_PLANE * 2;          // then decays and T's planes,
     static constexpr int later = image + DL_C * DP_TP * 4;                // and T by rows
     static constexpr int front = (tiles > later ? tiles : later);
-    static __host__ __device__ constexpr int oP() { return front; }
-    static __host__ __device__ constexpr int oL(int pplanes) { return front + pplanes * DL_PLANE * 2; }
-    static __host__ __device__ constexpr int oTt(int pplanes) { return oL(pplanes) + DL_C * DP_LP * 4; }
-    static __host__ __device__ constexpr int oM(int pplanes) { return oTt(pplanes) + DL_C * DP_TP * 4; }
-    static __host__ __device__ constexpr int oGates(int pplanes) { return oM(pplanes) + 32 * DP_TP * 4; }
-    static __host__ __device__ constexpr size_t smem(int pplanes) { return oGates(pplanes) + DL_C * (8 + 4 * 7); }
+    static constexpr int oL = front, oTt = oL + DL_C * DP_LP * 4, oM = oTt + DL_C * DP_TP * 4, oGates = oM + 32 * DP_TP * 4;
+    static constexpr size_t smem = oGates + DL_C * (8 + 4 * 7);
 };
 
 // A value's three bf16 terms, one in each plane of T's image; `at` is its plane_at.
@@ -459,11 +456,10 @@ __global__ void __launch_bounds__(DP_THREADS) delta_prep_kernel(const DeltaParam
     float* vec = reinterpret_cast<float*>(smem);
     __nv_bfloat16* imgT = reinterpret_cast<__nv_bfloat16*>(vec + DL_VECS);
     float* Tr = reinterpret_cast<float*>(smem + Sh::image);                 // T_ij at [i][j mod 32]
-    __nv_bfloat16* imgP = reinterpret_cast<__nv_bfloat16*>(smem + Sh::oP());
-    float* Lt = reinterpret_cast<float*>(smem + Sh::oL(PP));         // L_ij at [j][i]
-    float* Tt = reinterpret_cast<float*>(smem + Sh::oTt(PP));        // T_ij at [j][i mod 32]
-    float* M = reinterpret_cast<float*>(smem + Sh::oM(PP));
-    float2* G = reinterpret_cast<float2*>(smem + Sh::oGates(PP));           // running sum, rounded and rest
+    float* Lt = reinterpret_cast<float*>(smem + Sh::oL);         // L_ij at [j][i]
+    float* Tt = reinterpret_cast<float*>(smem + Sh::oTt);        // T_ij at [j][i mod 32]
+    float* M = reinterpret_cast<float*>(smem + Sh::oM);
+    float2* G = reinterpret_cast<float2*>(smem + Sh::oGates);           // running sum, rounded and rest
     float* beta = reinterpret_cast<float*>(G + DL_C);
     float *onward = beta + DL_C, *upto = onward + DL_C;                     // [64]; [4][64], row block 0 unused
     int* rows = reinterpret_cast<int*>(upto + 4 * DL_C);
@@ -491,6 +487,7 @@ __global__ void __launch_bounds__(DP_THREADS) delta_prep_kernel(const DeltaParam
     const size_t rec = (size_t)blockIdx.x * p.heads_v + head;
 
     unsigned char* out = p.wrec + rec * delta_record_bytes<T, DKP>(PP);
+    __nv_bfloat16* imgP = reinterpret_cast<__nv_bfloat16*>(out + Sh::image);
     double g[2];
     if (warp == 0) {  // running sum of the log decay: two steps a lane, then a scan over the lanes
         const float A = p.A[head], bias = p.bias ? p.bias[head] : 0.f;
@@ -622,15 +619,7 @@ __global__ void __launch_bounds__(DP_THREADS) delta_prep_kernel(const DeltaParam
             }
         }
     }
-    if (group) {
-        tc_fence_smem();
-        bar_sync(2, 128);
-        if (tid == 128) {
-            bulk_out(out + Sh::image, imgP, PP * DL_PLANE * 2);
-            bulk_out_read();
-        }
-        return;
-    }
+    if (group) return;
     if (warp == 0) {
         const double last = __shfl_sync(0xffffffffu, g[1], 31);
 #pragma unroll
