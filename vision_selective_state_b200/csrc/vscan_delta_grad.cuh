@@ -413,6 +413,40 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
     tiles += (1024 - (__cvta_generic_to_shared(tiles) & 1023)) % 1024;
     const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(tiles));
     const uint32_t done = static_cast<uint32_t>(__cvta_generic_to_shared(&sh->done));
+    // A slab of everything else passes through registers, fetched ahead: a state is NS pieces of
+    // four channels a thread, W, dX and dO four each (a row's sixteen pieces are in half a warp).
+    constexpr int NS = DKP / 16;
+    using Raw = typename GradRaw<T>::type;
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int pr = tid >> 4, pc = (tid & 15) * 4;  // first row of this thread's pieces, 16 apart, and their columns
+    float4 s0[NS], ds[NS], w[4], x[4];
+    Raw o[4];
+    auto fetch_state = [&](float4 (&v)[NS], const float* src, int slab) {
+        const bool in = slab + pc < p.dv;
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+            v[i] = in ? __ldg(reinterpret_cast<const float4*>(src + (size_t)(pr + 16 * i) * p.dv + slab + pc)) : zero;
+    };
+    auto fetch = [&](int slab) {
+        fetch_state(s0, wS, slab);
+        const bool in = slab + pc < p.dv;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = pr + 16 * i;
+            w[i] = in ? __ldg(reinterpret_cast<const float4*>(wW + (size_t)r * p.dv + slab + pc)) : zero;
+            x[i] = in ? __ldg(reinterpret_cast<const float4*>(wdX + (size_t)r * p.dv + slab + pc)) : zero;
+        }
+    };
+    auto fetch_dy = [&](int slab) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = sh->rows[pr + 16 * i];
+            o[i] = Raw{};
+            if (slab + pc < p.dv && row >= 0) o[i] = __ldg(reinterpret_cast<const Raw*>(dy + row * p.y_tok + slab + pc));
+        }
+    };
+    if (warp < 8) fetch(0);
+
     if (warp == 0) tc_alloc(static_cast<uint32_t>(__cvta_generic_to_shared(&sh->tmem)));
     if (tid == 0) {
         mbar_init(done, 1);
@@ -487,6 +521,56 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
             tc_commit(done);
         }
         __syncwarp();
+        // dg, two steps a lane; then a, b and the sums for A and bias
+        double x[2], v[2], base = 0.0;
+        for (int w = 0; w < 8; ++w) base += (double)sh->red[w];
+        base *= (double)vec[3 * DL_C];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = 2 * lane + i;
+            x[i] = v[i] = 0.0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                x[i] += sh->hrow[q >> 1][q & 1][r] - sh->hcol[q][r] + (double)sh->U[q][r];
+                v[i] += (double)sh->V[q][r];
+            }
+        }
+        double sum = x[0] + x[1], before = v[0] + v[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double other = __shfl_down_sync(0xffffffffu, sum, o), prior = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane + o < 32) sum += other;
+            if (lane >= o) before += prior;
+        }
+        before -= v[0] + v[1];
+        const double dg[2] = {base + sum + before, base + (sum - x[0]) + (before + v[0])};
+        const float A = p.A[head], bias = p.bias ? p.bias[head] : 0.f;
+        double sA = 0.0, sb = 0.0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = 2 * lane + i;
+            if (t0 + r >= s.len) continue;
+            const int row = sh->rows[r];
+            const float a = row >= 0 ? to_float(reinterpret_cast<const T*>(p.a)[img * p.a_img + row * p.a_tok + head]) : 0.f;
+            const float da = (float)dg[i] * A * delta_sigmoid(a + bias);
+            sA += dg[i] * (double)delta_softplus(a + bias);
+            sb += (double)da;
+            if (row >= 0) {
+                const size_t o = (size_t)(img * p.tokens + row) * p.heads_v + head;
+                const float bb = to_float(reinterpret_cast<const T*>(p.b)[img * p.b_img + row * p.b_tok + head]);
+                if (p.da) store_elem(reinterpret_cast<T*>(p.da) + o, da);
+                if (p.db) store_elem(reinterpret_cast<T*>(p.db) + o, sh->xw[r] * delta_sigmoid(-bb));
+            }
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            sA += __shfl_xor_sync(0xffffffffu, sA, o);
+            sb += __shfl_xor_sync(0xffffffffu, sb, o);
+        }
+        if (lane == 0) {
+            p.wpart[2 * rec] = (float)sA;
+            p.wpart[2 * rec + 1] = (float)sb;
+        }
         __syncthreads();
         return;
     }
@@ -496,34 +580,7 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
         bar_arrive(id, DG_THREADS);
     };
 
-    // A slab of everything else passes through registers, fetched ahead: a state is NS pieces of
-    // four channels a thread, W, dX and dO four each (a row's sixteen pieces are in half a warp).
-    constexpr int NS = DKP / 16;
-    using Raw = typename GradRaw<T>::type;
-    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int pr = tid >> 4, pc = (tid & 15) * 4;  // first row of this thread's pieces, 16 apart, and their columns
-    float4 s0[NS], ds[NS], w[4], x[4];
-    Raw o[4];
-    auto fetch_state = [&](float4 (&v)[NS], const float* src, int slab) {
-        const bool in = slab + pc < p.dv;
-#pragma unroll
-        for (int i = 0; i < NS; ++i)
-            v[i] = in ? __ldg(reinterpret_cast<const float4*>(src + (size_t)(pr + 16 * i) * p.dv + slab + pc)) : zero;
-    };
-    auto fetch = [&](int slab) {
-        fetch_state(s0, wS, slab);
-        const bool in = slab + pc < p.dv;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = pr + 16 * i, row = sh->rows[r];
-            w[i] = in ? __ldg(reinterpret_cast<const float4*>(wW + (size_t)r * p.dv + slab + pc)) : zero;
-            x[i] = in ? __ldg(reinterpret_cast<const float4*>(wdX + (size_t)r * p.dv + slab + pc)) : zero;
-            o[i] = Raw{};
-            if (in && row >= 0) o[i] = __ldg(reinterpret_cast<const Raw*>(dy + row * p.y_tok + slab + pc));
-        }
-    };
-    fetch(0);
-
+    fetch_dy(0);
     // K and Q
     {
         const T* k = reinterpret_cast<const T*>(p.k) + img * p.k_img + (long long)hk * p.dk;
@@ -536,6 +593,21 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
         for (int i = tid; i < 2 * TC_TILE / 16; i += 256)
             *reinterpret_cast<uint4*>(tiles + Sh::oX + 2 * TC_TILE + (i >> 9) * 2 * TC_TILE + (i & 511) * 16) = make_uint4(0, 0, 0, 0);
 
+    // what E (P, in its planes) and M (L) are multiplied with for dg: this thread's half row, fetched ahead as well
+    const int part = (warp >> 1) & 1, step = (warp & 1) * 32 + lane, j0 = half * 32;
+    uint4 factor[12];
+    auto fetch_factors = [&]() {
+        if (part == 0) {
+            const __nv_bfloat16* wP = record_P<T, DKP>(p, rec);
+#pragma unroll
+            for (int q = 0; q < 12; ++q)
+                factor[q] = __ldg(reinterpret_cast<const uint4*>(wP + (q >> 2) * DL_PLANE + plane_at(step, j0 + (q & 3) * 8)));
+        } else {
+            const uint4* wL = reinterpret_cast<const uint4*>(p.wL + rec * DL_PLANE + step * DL_C + j0);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) factor[q] = __ldg(wL + q);
+        }
+    };
     float dots = 0.f;
     float xw[4] = {};
     for (int slab = 0; slab < p.dv; slab += 64) {
@@ -565,7 +637,12 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
 #pragma unroll
         for (int i = 0; i < NS; ++i) put_planes(tiles + Sh::oS, Sh::plane, pr + 16 * i, pc, ds[i]);
         ready(2);
-        if (slab + 64 < p.dv) fetch(slab + 64);
+        if (slab + 64 < p.dv) {
+            fetch(slab + 64);
+            fetch_dy(slab + 64);
+        } else {
+            fetch_factors();
+        }
         mbar_wait(done, phase, &sh->dead);
         phase ^= 1;
     }
@@ -582,7 +659,7 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
 
     // E and M: rows 0-63 of D2 and rows 64-127, columns 32 half .. of this thread's step i
     {
-        const int part = (warp >> 1) & 1, i = (warp & 1) * 32 + lane, j0 = half * 32;
+        const int i = step;
         float e[32], f[32];
         tc_ld32(tl + c2 + j0, e);
         tc_ld32(tl + c2 + cSmall + j0, f);
@@ -590,29 +667,22 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
 #pragma unroll
         for (int k = 0; k < 32; ++k) e[k] += f[k];
         if (part == 0) {  // P, whole again
-            const __nv_bfloat16* wP = record_P<T, DKP>(p, rec);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float z[8] = {};
+            for (int k = 0; k < 32; ++k) {
+                float z = 0.f;
 #pragma unroll
                 for (int n = 2; n >= 0; --n) {
-                    const uint4 u = __ldg(reinterpret_cast<const uint4*>(wP + n * DL_PLANE + plane_at(i, j0 + q * 8)));
-                    const uint32_t a[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        z[2 * k] += __uint_as_float(a[k] << 16);
-                        z[2 * k + 1] += __uint_as_float(a[k] & 0xffff0000u);
-                    }
+                    const uint4& u = factor[n * 4 + (k >> 3)];
+                    const uint32_t a = (k >> 1 & 3) == 0 ? u.x : (k >> 1 & 3) == 1 ? u.y : (k >> 1 & 3) == 2 ? u.z : u.w;
+                    z += __uint_as_float(k & 1 ? a & 0xffff0000u : a << 16);
                 }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) f[q * 8 + k] = z[k];
+                f[k] = z;
             }
         } else {
-            const float4* wL = reinterpret_cast<const float4*>(p.wL + rec * DL_PLANE + i * DL_C + j0);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const float4 u = __ldg(wL + q);
-                f[4 * q] = -u.x; f[4 * q + 1] = -u.y; f[4 * q + 2] = -u.z; f[4 * q + 3] = -u.w;
+            for (int k = 0; k < 32; ++k) {
+                const uint4& u = factor[k >> 2];
+                f[k] = -__uint_as_float((k & 3) == 0 ? u.x : (k & 3) == 1 ? u.y : (k & 3) == 2 ? u.z : u.w);
             }
         }
         // a step's own product carries no decay: it is no part of dg. Blocks above the diagonal
@@ -632,12 +702,12 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
         sh->hcol[warp & 3][j0 + lane] = col;
         const float2* G = reinterpret_cast<const float2*>(vec + 4 * DL_C);
         const float2 gi = G[i];
-        const float factor = part == 0 ? p.scale : -1.f;
+        const float sign = part == 0 ? p.scale : -1.f;
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
             const float2 gj = G[j0 + k];
             const float d = decay_between<NP == 1>(gi, gj);
-            e[k] = j0 + k <= i - part ? factor * (d * e[k]) : 0.f;
+            e[k] = j0 + k <= i - part ? sign * (d * e[k]) : 0.f;
         }
         unsigned char* o = tiles + Sh::oX + part * TC_TILE;
 #pragma unroll
@@ -699,57 +769,6 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
     }
     tc_wait_st();
     ready(3);
-    if (warp == 7) {  // dg, two steps a lane; then a, b and the sums for A and bias
-        double x[2], v[2], base = 0.0;
-        for (int w = 0; w < 8; ++w) base += (double)sh->red[w];
-        base *= (double)vec[3 * DL_C];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = 2 * lane + i;
-            x[i] = v[i] = 0.0;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                x[i] += sh->hrow[q >> 1][q & 1][r] - sh->hcol[q][r] + (double)sh->U[q][r];
-                v[i] += (double)sh->V[q][r];
-            }
-        }
-        double sum = x[0] + x[1], before = v[0] + v[1];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double other = __shfl_down_sync(0xffffffffu, sum, o), prior = __shfl_up_sync(0xffffffffu, before, o);
-            if (lane + o < 32) sum += other;
-            if (lane >= o) before += prior;
-        }
-        before -= v[0] + v[1];
-        const double dg[2] = {base + sum + before, base + (sum - x[0]) + (before + v[0])};
-        const float A = p.A[head], bias = p.bias ? p.bias[head] : 0.f;
-        double sA = 0.0, sb = 0.0;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = 2 * lane + i;
-            if (t0 + r >= s.len) continue;
-            const int row = sh->rows[r];
-            const float a = row >= 0 ? to_float(reinterpret_cast<const T*>(p.a)[img * p.a_img + row * p.a_tok + head]) : 0.f;
-            const float da = (float)dg[i] * A * delta_sigmoid(a + bias);
-            sA += dg[i] * (double)delta_softplus(a + bias);
-            sb += (double)da;
-            if (row >= 0) {
-                const size_t o = (size_t)(img * p.tokens + row) * p.heads_v + head;
-                const float bb = to_float(reinterpret_cast<const T*>(p.b)[img * p.b_img + row * p.b_tok + head]);
-                if (p.da) store_elem(reinterpret_cast<T*>(p.da) + o, da);
-                if (p.db) store_elem(reinterpret_cast<T*>(p.db) + o, sh->xw[r] * delta_sigmoid(-bb));
-            }
-        }
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            sA += __shfl_xor_sync(0xffffffffu, sA, o);
-            sb += __shfl_xor_sync(0xffffffffu, sb, o);
-        }
-        if (lane == 0) {
-            p.wpart[2 * rec] = (float)sA;
-            p.wpart[2 * rec + 1] = (float)sb;
-        }
-    }
     mbar_wait(done, phase, &sh->dead);
     tc_fence_after();
     {
