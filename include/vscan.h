@@ -425,7 +425,8 @@ vscan_status vscan_status_from_device_word(int32_t word);
  * beta <= 1 keep the update contractive. States are float32; the products run on
  * bf16 tensor cores with every float32 operand split into three bf16 terms, so
  * states and float32 results keep float32 accuracy. Values must be finite: a
- * non-finite value in one token can reach other tokens of its chunk of 64 steps.
+ * non-finite value in one token can reach the other tokens of its chunk of 64 steps
+ * (never an earlier chunk).
  */
 typedef struct vscan_delta_args {
     int32_t batch;       /* images, >= 0; with seq_offsets: packed sequences         */
@@ -479,9 +480,10 @@ typedef struct vscan_delta_args {
 
 /*
  * Device scratch bytes vscan_delta_forward needs (host only): for every chunk of
- * 64 steps and value head the triangular inverse, the masked q k^T product and
- * the decays (about 41 KiB in bf16, 49 KiB in float32). Packed sequences count
- * tokens / 64 + batch + 1 chunks whatever their lengths.
+ * 64 steps and value head a record of the triangular inverse, the masked q k^T
+ * product and the decays, 42 KiB in bf16; in float32 with the chunk's split q and k,
+ * 98 KiB (dim_k <= 64) or 146 KiB. Packed sequences count tokens / 64 + batch + 1
+ * chunks whatever their lengths.
  */
 vscan_status vscan_delta_workspace_size(const vscan_route* route, const vscan_delta_args* args, uint64_t* bytes);
 
@@ -537,8 +539,9 @@ vscan_status vscan_delta_backward_workspace_size(const vscan_route* route, const
  * args->workspace are not used; y's strides are dy's); dy is dL/dy, 16-byte
  * aligned. Runs the forward recurrence once more, then the chunks in reverse, then
  * every chunk's token gradients; enqueued on stream (five launches, one more with
- * shared key heads); allocates nothing; never synchronizes. Rows that no step
- * visits (ATROUS2, packed sequences) get gradients of 0. All sums have a fixed
+ * shared key heads; clears where rows may stay without a step); allocates nothing;
+ * never synchronizes. Rows that no step visits (ATROUS2, packed sequences) get
+ * gradients of 0. All sums have a fixed
  * order: equal calls give equal bits.
  * Errors: as vscan_delta_forward; INVALID_ARGUMENT for dy or grads NULL.
  */
