@@ -294,11 +294,19 @@ __device__ __forceinline__ void copy_rows(const int* rows, int tid, F copy)
 //   [A 0; C B]^-1 = [A^-1 0; -B^-1 C A^-1 B^-1].
 // L and T's blocks lie transposed as well, so that four rows of a left factor are one
 // 16-byte read. The decays and T are assembled in shared memory, in the walks' swizzled
-// layout, and leave in one bulk copy; P goes out directly, which leaves shared memory
-// for three CTAs an SM instead of two (bf16). Blocks above the diagonal hold nothing,
-// and nothing reads them.
+// layout, and leave in one bulk copy; P goes out directly. What shared memory holds is
+// packed so that four CTAs share an SM (bf16): L^T's rows begin at their diagonal block,
+// the part of T^T that nothing reads has no place, and the merges' first factors lie in
+// T's own rows. Blocks above the diagonal hold nothing, and nothing reads them.
 constexpr int DP_THREADS = 256;
-constexpr int DP_LP = 68, DP_TP = 36;  // row pitches of L^T and of the 32 x 32 blocks of T
+constexpr int DP_TP = 36;  // row pitch of the 32 x 32 blocks of T
+// L^T: rows of block b hold the steps from 16 b on.
+__host__ __device__ constexpr int prep_lt_pitch(int b) { return 68 - 16 * b; }
+__host__ __device__ constexpr int prep_lt(int j)  // L_ij at prep_lt(j) + i
+{
+    return (j >> 4) * (1088 - 128 * ((j >> 4) - 1)) + (j & 15) * prep_lt_pitch(j >> 4) - (j & ~15);
+}
+static_assert(prep_lt(16) + 16 == prep_lt(15) + 68 && prep_lt(48) + 48 == prep_lt(47) + 68, "rows follow one another");
 
 template <typename T, int DKP>
 struct PrepShape {
@@ -309,7 +317,7 @@ struct PrepShape {
     static constexpr int image = DL_VECS * 4 + 3 * DL_PLANE * 2;          // then decays and T's planes,
     static constexpr int later = image + DL_C * DP_TP * 4;                // and T by rows
     static constexpr int front = (tiles > later ? tiles : later);
-    static constexpr int oL = front, oTt = oL + DL_C * DP_LP * 4, oM = oTt + DL_C * DP_TP * 4, oGates = oM + 32 * DP_TP * 4;
+    static constexpr int oL = front, oTt = oL + (prep_lt(63) + 68) * 4, oGates = oTt + (DL_C - 16) * DP_TP * 4;
     static constexpr size_t smem = oGates + DL_C * (8 + 4 * 7);
 };
 
@@ -363,7 +371,7 @@ __device__ __forceinline__ void prep_load(__nv_bfloat16* dst, unsigned char* ima
 }
 
 template <typename T, int DKP, int PP>  // PP planes of P
-__global__ void __launch_bounds__(DP_THREADS) delta_prep_kernel(const DeltaParams p)
+__global__ void __launch_bounds__(DP_THREADS, DeltaIo<T>::planes == 1 ? 4 : 3) delta_prep_kernel(const DeltaParams p)
 {
     using Sh = PrepShape<T, DKP>;
     constexpr int NP = Sh::NP, PITCH = Sh::pitch, PLANE = Sh::plane;
@@ -373,9 +381,8 @@ __global__ void __launch_bounds__(DP_THREADS) delta_prep_kernel(const DeltaParam
     float* vec = reinterpret_cast<float*>(smem);
     __nv_bfloat16* imgT = reinterpret_cast<__nv_bfloat16*>(vec + DL_VECS);
     float* Tr = reinterpret_cast<float*>(smem + Sh::image);                 // T_ij at [i][j mod 32]
-    float* Lt = reinterpret_cast<float*>(smem + Sh::oL);         // L_ij at [j][i]
-    float* Tt = reinterpret_cast<float*>(smem + Sh::oTt);        // T_ij at [j][i mod 32]
-    float* M = reinterpret_cast<float*>(smem + Sh::oM);
+    float* Lt = reinterpret_cast<float*>(smem + Sh::oL);                // L_ij at prep_lt(j) + i
+    float* Tt = reinterpret_cast<float*>(smem + Sh::oTt) - 16 * DP_TP;  // T_ij at [j][i mod 32], j from 16 on
     float2* G = reinterpret_cast<float2*>(smem + Sh::oGates);           // running sum, rounded and rest
     float* beta = reinterpret_cast<float*>(G + DL_C);
     float *onward = beta + DL_C, *upto = onward + DL_C;                     // [64]; [4][64], row block 0 unused
@@ -496,8 +503,8 @@ __global__ void __launch_bounds__(DP_THREADS) delta_prep_kernel(const DeltaParam
             } else {
                 if (PP == 3 && p.wL) *reinterpret_cast<float2*>(p.wL + rec * DL_PLANE + i * DL_C + j) = make_float2(v0, v1);
                 const float be = half ? beta1 : beta0;
-                Lt[j * DP_LP + i] = be * v0;
-                Lt[(j + 1) * DP_LP + i] = be * v1;
+                Lt[prep_lt(j) + i] = be * v0;
+                Lt[prep_lt(j + 1) + i] = be * v1;
             }
         };
         beta0 = beta[r0];
@@ -554,19 +561,20 @@ __global__ void __launch_bounds__(DP_THREADS) delta_prep_kernel(const DeltaParam
         float x[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = i == lane ? 1.f : 0.f;
-        const float* L = Lt + m0 * DP_LP + m0;
+        const float* L = Lt + prep_lt(m0) + m0;
+        const int pitch = prep_lt_pitch(m0 >> 4);
 #pragma unroll
         for (int j = 0; j < 15; ++j) {
             float l[16];
 #pragma unroll
-            for (int q = (j + 1) / 4; q < 4; ++q) *reinterpret_cast<float4*>(l + 4 * q) = *reinterpret_cast<const float4*>(L + j * DP_LP + 4 * q);
+            for (int q = (j + 1) / 4; q < 4; ++q) *reinterpret_cast<float4*>(l + 4 * q) = *reinterpret_cast<const float4*>(L + j * pitch + 4 * q);
 #pragma unroll
             for (int i = j + 1; i < 16; ++i) x[i] -= l[i] * x[j];
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             Tr[(m0 + i) * DP_TP + (m0 & 31) + lane] = x[i];
-            Tt[(m0 + lane) * DP_TP + (m0 & 31) + i] = x[i];
+            if (m0) Tt[(m0 + lane) * DP_TP + (m0 & 31) + i] = x[i];
             image_put(imgT, (m0 + i) * 64 + ((((m0 + lane) >> 3) ^ (i & 7)) << 3) + (lane & 7), x[i]);
         }
     }
@@ -574,10 +582,12 @@ __global__ void __launch_bounds__(DP_THREADS) delta_prep_kernel(const DeltaParam
     {  // 16 x 16 blocks below the diagonal of both 32 x 32 ones: four rows of a column a thread
         const int b0 = (tid >> 6) * 32, col = tid & 15, r = (tid >> 4 & 3) * 4;
         float m[4] = {}, o[4] = {};
-        float* Mb = M + (tid >> 6) * 16 * DP_TP;
+        float* Mb = Tr + (b0 + 16) * DP_TP;  // where o goes in the end
+        const float* L = Lt + prep_lt(b0) + b0 + 16 + r;
+        const int pitch = prep_lt_pitch(b0 >> 4);
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-            const float4 l = *reinterpret_cast<const float4*>(Lt + (b0 + k) * DP_LP + b0 + 16 + r);
+            const float4 l = *reinterpret_cast<const float4*>(L + k * pitch);
             const float x = Tr[(b0 + k) * DP_TP + col];
             m[0] += l.x * x; m[1] += l.y * x; m[2] += l.z * x; m[3] += l.w * x;
         }
@@ -591,28 +601,35 @@ __global__ void __launch_bounds__(DP_THREADS) delta_prep_kernel(const DeltaParam
             o[0] -= l.x * x; o[1] -= l.y * x; o[2] -= l.z * x; o[3] -= l.w * x;
         }
         bar_sync(1, 128);
-        *reinterpret_cast<float4*>(Tt + (b0 + col) * DP_TP + 16 + r) = make_float4(o[0], o[1], o[2], o[3]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            Tr[(b0 + 16 + r + i) * DP_TP + col] = o[i];
-            image_put(imgT, plane_at(b0 + 16 + r + i, b0 + col), o[i]);
+        for (int i = 0; i < 4; ++i) image_put(imgT, plane_at(b0 + 16 + r + i, b0 + col), o[i]);
+        // The next products read the first block by rows and the second one by columns, above
+        // the diagonal too.
+        if (b0) {
+            *reinterpret_cast<float4*>(Tt + (32 + col) * DP_TP + 16 + r) = make_float4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<float4*>(Tt + (48 + col) * DP_TP + r) = make_float4(0.f, 0.f, 0.f, 0.f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                Tr[(16 + r + i) * DP_TP + col] = o[i];
+                Tr[(r + i) * DP_TP + 16 + col] = 0.f;
+            }
         }
-        // above the diagonal of the 32 x 32 blocks, which the next products read
-#pragma unroll
-        for (int i = 0; i < 4; ++i) Tr[(b0 + r + i) * DP_TP + 16 + col] = 0.f;
-        *reinterpret_cast<float4*>(Tt + (b0 + 16 + col) * DP_TP + r) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     bar_sync(1, 128);
     {  // the 32 x 32 block below the diagonal: four rows of two columns a thread
         const int col = (tid & 15) * 2, r = (tid >> 4) * 4;
         float m[4][2] = {}, o[4][2] = {};
+        float* M = Tr + 32 * DP_TP;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
 #pragma unroll 8
-        for (int k = 0; k < 32; ++k) {
-            const float4 l = *reinterpret_cast<const float4*>(Lt + k * DP_LP + 32 + r);
-            const float2 x = *reinterpret_cast<const float2*>(Tr + k * DP_TP + col);
-            m[0][0] += l.x * x.x; m[1][0] += l.y * x.x; m[2][0] += l.z * x.x; m[3][0] += l.w * x.x;
-            m[0][1] += l.x * x.y; m[1][1] += l.y * x.y; m[2][1] += l.z * x.y; m[3][1] += l.w * x.y;
-        }
+            for (int k = 0; k < 16; ++k) {
+                const float4 l = *reinterpret_cast<const float4*>(Lt + prep_lt(h * 16) + k * prep_lt_pitch(h) + 32 + r);
+                const float2 x = *reinterpret_cast<const float2*>(Tr + (h * 16 + k) * DP_TP + col);
+                m[0][0] += l.x * x.x; m[1][0] += l.y * x.x; m[2][0] += l.z * x.x; m[3][0] += l.w * x.x;
+                m[0][1] += l.x * x.y; m[1][1] += l.y * x.y; m[2][1] += l.z * x.y; m[3][1] += l.w * x.y;
+            }
 #pragma unroll
         for (int i = 0; i < 4; ++i) *reinterpret_cast<float2*>(M + (r + i) * DP_TP + col) = make_float2(m[i][0], m[i][1]);
         bar_sync(1, 128);
@@ -762,13 +779,13 @@ __device__ __forceinline__ void stage_two(__nv_bfloat16* p, int pitch, float x, 
     p[0] = __low2bfloat16(h);
     p[pitch] = __high2bfloat16(h);
 }
-template <typename T>
-__device__ __forceinline__ void walk_stage(T* mine, int pitch, const float (&x)[32])
+template <typename T, int N>
+__device__ __forceinline__ void walk_stage(T* mine, int pitch, const float (&x)[N])
 {
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) stage_two(mine + i * pitch, pitch, x[i], x[i + 1]);
+    for (int i = 0; i < N; i += 2) stage_two(mine + i * pitch, pitch, x[i], x[i + 1]);
 }
-template <typename T>
+template <int N = 32, typename T>
 __device__ __forceinline__ void walk_flush(T* dst, long long tok, const int* rows, const T* mine, int pitch, int have, int lane)
 {
     __syncwarp();
@@ -777,18 +794,18 @@ __device__ __forceinline__ void walk_flush(T* dst, long long tok, const int* row
     const T* src = mine - lane + c;
     if (c < have)
 #pragma unroll
-        for (int i = 0; i < 32; i += per) {
+        for (int i = 0; i < N; i += per) {
             const int r = i + lane / vecs, row = rows[r];
             if (row >= 0) *reinterpret_cast<uint4*>(dst + row * tok + c) = *reinterpret_cast<const uint4*>(src + r * pitch);
         }
     __syncwarp();
 }
-template <typename T>
+template <typename T, int N>
 __device__ __forceinline__ void walk_store(T* dst, long long tok, const int* rows, T* mine, int pitch, int have, int lane,
-                                           const float (&x)[32])
+                                           const float (&x)[N])
 {
     walk_stage(mine, pitch, x);
-    walk_flush(dst, tok, rows, mine, pitch, have, lane);
+    walk_flush<N>(dst, tok, rows, mine, pitch, have, lane);
 }
 
 // NT bf16 terms of 32 values of a row, term n in the 16 columns from addr + n * step on. Three

@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaP
 // ---- per-chunk gradients -------------------------------------------------------------
 // One CTA per chunk and value head. As in the walks the products stand
 // transposed, with the key channel as the row of the 128-row tile, so that a thread
-// holds half the steps of one key channel:
+// holds a quarter of the steps of one key channel:
 //
 //   D1[dk][i | i] = S0 [dO | dV]^T      D2[i | i][j] = [dO | dV] W^T      D3[dk][j] = dS W^T
 //   (dq | dkr)^T = (scale e^G | -e^G) D1 + K^T [E | M]^T       dkc^T = e^{G_C - G} D3 + Q^T E + K^T M
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaP
 // [i][j], where the same tile is E (M) and its transpose; K^T and Q^T lie in tensor memory.
 // Bound by the products and by splitting the operands (S0 and dS are 32,768 values a chunk
 // and head at dk = dv = 128).
-constexpr int DG_THREADS = 288;  // eight warps and one that issues the products
+constexpr int DG_COMPUTE = 512, DG_THREADS = 544;  // sixteen warps and one that issues the products
 
 template <typename T> struct GradRaw;  // four values of dy
 template <> struct GradRaw<__nv_bfloat16> { using type = uint2; };
@@ -288,7 +288,8 @@ struct GradShape {
     static constexpr int oK = 0, oQ = NP * plane, oS = 2 * NP * plane, oW = oS + 3 * plane;
     static constexpr int oX = oW + 3 * TC_TILE;   // three pairs of tiles: dO's and dV's terms; later E's and M's
     static constexpr int oEnd = oX + 6 * TC_TILE;
-    static constexpr int front = 9216;  // GradShared
+    static constexpr int oSums = oW + 2 * TC_TILE;  // GradSums, once W is read
+    static constexpr int front = 3072;  // GradShared
     static constexpr size_t smem = 1024 + front + oEnd;
 };
 
@@ -297,14 +298,17 @@ struct GradShared {
     uint32_t tmem;
     int dead;
     alignas(16) int rows[DL_C];
-    double hrow[2][2][DL_C];  // row sums of H: E's and M's part, halves of the columns
-    double hcol[4][DL_C];     // column sums, by quarters of the 128 rows of D2
-    float U[4][DL_C], V[4][DL_C];  // by quarters of the key channels
-    float xw[DL_C];           // dX.w
-    float red[8];             // <dS, S0>
+    float xw[DL_C];                // dX.w
+    float red[DG_COMPUTE / 32];    // <dS, S0>
     alignas(16) float vec[DL_VECS];
 };
-static_assert(sizeof(GradShared) <= 9216, "shared memory in front of the tiles");
+struct GradSums {
+    double hrow[2][4][DL_C];       // row sums of H: E's and M's part, quarters of the columns
+    double hcol[4][DL_C];          // column sums, by quarters of the 128 rows of D2
+    float U[4][DL_C], V[4][DL_C];  // by quarters of the key channels
+};
+static_assert(sizeof(GradShared) <= 3072, "shared memory in front of the tiles");
+static_assert(sizeof(GradSums) <= TC_TILE, "in the place of W's third plane");
 
 // Sum over the warp of each of 32 values; lane l gets the l-th.
 __device__ __forceinline__ float reduce_columns(float (&v)[32], int lane)
@@ -334,12 +338,12 @@ __device__ __forceinline__ void put_planes(unsigned char* dst, int plane, int r,
     }
 }
 
-// 32 values of a row, NP bf16 terms, from a column of a [64][DKP] tile of K or Q.
-template <int NP, int DKP>
-__device__ __forceinline__ void column_of(const unsigned char* tile, int plane, int col, int first, float (&v)[32])
+// N values of a row, NP bf16 terms, from a column of a [64][DKP] tile of K or Q.
+template <int NP, int DKP, int N>
+__device__ __forceinline__ void column_of(const unsigned char* tile, int plane, int col, int first, float (&v)[N])
 {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < N; ++i) {
         float x = 0.f;
         const unsigned char* at = tile + tc_swizzle(first + i, col >> 3) + (col & 7) * 2;
 #pragma unroll
@@ -356,7 +360,7 @@ __device__ __forceinline__ void grad_load(unsigned char* dst, const __nv_bfloat1
     const int c = tid % vecs;
     const bool in = c * 8 < have;
     const __nv_bfloat16* at = in ? src + c * 8 : src;
-    copy_rows<vecs, 256>(rows, tid, [&](int r, int row) {
+    copy_rows<vecs, DG_COMPUTE>(rows, tid, [&](int r, int row) {
         const bool ok = in && row >= 0;
         copy16(dst + tc_swizzle(r, c), at + (ok ? row * tok : 0), ok);
     });
@@ -366,7 +370,7 @@ __device__ __forceinline__ void grad_load(unsigned char* dst, const float* src, 
 {
     constexpr int vecs = DKP / 4;
     const int c = tid % vecs * 4;
-    copy_rows<vecs, 256>(rows, tid, [&](int r, int row) {
+    copy_rows<vecs, DG_COMPUTE>(rows, tid, [&](int r, int row) {
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (row >= 0 && c < have) x = __ldg(reinterpret_cast<const float4*>(src + c + row * tok));
         put_planes(dst + (c >> 6) * TC_TILE, DKP / 64 * TC_TILE, r, c & 63, x);
@@ -382,7 +386,7 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
     // (one accumulator over several slabs would be truncated by each of them), and K^T and Q^T follow there
     constexpr int c1 = 0, c2 = 128, c3 = 192, cSmall = 256, cKT = 256, cQT = cKT + NP * 32;
     extern __shared__ unsigned char smem_raw[];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = warp >> 2;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quarter = warp >> 2;
     const int head = blockIdx.y, hk = head / p.group;
 
     int b;
@@ -411,41 +415,42 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
     GradShared* sh = reinterpret_cast<GradShared*>(smem_raw);
     unsigned char* tiles = smem_raw + Sh::front;
     tiles += (1024 - (__cvta_generic_to_shared(tiles) & 1023)) % 1024;
+    GradSums* sums = reinterpret_cast<GradSums*>(tiles + Sh::oSums);
     const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(tiles));
     const uint32_t done = static_cast<uint32_t>(__cvta_generic_to_shared(&sh->done));
     // A slab of everything else passes through registers, fetched ahead: a state is NS pieces of
-    // four channels a thread, W, dX and dO four each (a row's sixteen pieces are in half a warp).
-    constexpr int NS = DKP / 16;
+    // four channels a thread, W, dX and dO NW each (a row's sixteen pieces are in half a warp).
+    constexpr int STEP = DG_COMPUTE / 16, NS = DKP / STEP, NW = DL_C / STEP;
     using Raw = typename GradRaw<T>::type;
     const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int pr = tid >> 4, pc = (tid & 15) * 4;  // first row of this thread's pieces, 16 apart, and their columns
-    float4 s0[NS], ds[NS], w[4], x[4];
-    Raw o[4];
+    const int pr = tid >> 4, pc = (tid & 15) * 4;  // first row of this thread's pieces, STEP apart, and their columns
+    float4 s0[NS], ds[NS], w[NW], x[NW];
+    Raw o[NW];
     auto fetch_state = [&](float4 (&v)[NS], const float* src, int slab) {
         const bool in = slab + pc < p.dv;
 #pragma unroll
         for (int i = 0; i < NS; ++i)
-            v[i] = in ? __ldg(reinterpret_cast<const float4*>(src + (size_t)(pr + 16 * i) * p.dv + slab + pc)) : zero;
+            v[i] = in ? __ldg(reinterpret_cast<const float4*>(src + (size_t)(pr + STEP * i) * p.dv + slab + pc)) : zero;
     };
     auto fetch = [&](int slab) {
         fetch_state(s0, wS, slab);
         const bool in = slab + pc < p.dv;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = pr + 16 * i;
+        for (int i = 0; i < NW; ++i) {
+            const int r = pr + STEP * i;
             w[i] = in ? __ldg(reinterpret_cast<const float4*>(wW + (size_t)r * p.dv + slab + pc)) : zero;
             x[i] = in ? __ldg(reinterpret_cast<const float4*>(wdX + (size_t)r * p.dv + slab + pc)) : zero;
         }
     };
     auto fetch_dy = [&](int slab) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = sh->rows[pr + 16 * i];
+        for (int i = 0; i < NW; ++i) {
+            const int row = sh->rows[pr + STEP * i];
             o[i] = Raw{};
             if (slab + pc < p.dv && row >= 0) o[i] = __ldg(reinterpret_cast<const Raw*>(dy + row * p.y_tok + slab + pc));
         }
     };
-    if (warp < 8) fetch(0);
+    if (warp < DG_COMPUTE / 32) fetch(0);
 
     if (warp == 0) tc_alloc(static_cast<uint32_t>(__cvta_generic_to_shared(&sh->tmem)));
     if (tid == 0) {
@@ -464,7 +469,7 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
     const uint64_t aS = tc_desc(at + Sh::oS), aX = tc_desc(at + Sh::oX), bW = tc_desc(at + Sh::oW);
     auto aK = [&](int x, int ks) { return tm + cKT + x * 32 + ks * 8; };
 
-    if (warp == 8) {  // issues the products
+    if (warp == DG_COMPUTE / 32) {  // issues the products
         for (int slab = 0; slab < p.dv; slab += 64) {
             const bool more = slab > 0;
             bar_sync(1, DG_THREADS);
@@ -523,7 +528,7 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
         __syncwarp();
         // dg, two steps a lane; then a, b and the sums for A and bias
         double x[2], v[2], base = 0.0;
-        for (int w = 0; w < 8; ++w) base += (double)sh->red[w];
+        for (int w = 0; w < DG_COMPUTE / 32; ++w) base += (double)sh->red[w];
         base *= (double)vec[3 * DL_C];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -531,8 +536,8 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
             x[i] = v[i] = 0.0;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                x[i] += sh->hrow[q >> 1][q & 1][r] - sh->hcol[q][r] + (double)sh->U[q][r];
-                v[i] += (double)sh->V[q][r];
+                x[i] += sums->hrow[0][q][r] + sums->hrow[1][q][r] - sums->hcol[q][r] + (double)sums->U[q][r];
+                v[i] += (double)sums->V[q][r];
             }
         }
         double sum = x[0] + x[1], before = v[0] + v[1];
@@ -590,33 +595,33 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
         cp_async_commit();
     }
     if (NP == 1)  // an exact dO has no second and third term
-        for (int i = tid; i < 2 * TC_TILE / 16; i += 256)
+        for (int i = tid; i < 2 * TC_TILE / 16; i += DG_COMPUTE)
             *reinterpret_cast<uint4*>(tiles + Sh::oX + 2 * TC_TILE + (i >> 9) * 2 * TC_TILE + (i & 511) * 16) = make_uint4(0, 0, 0, 0);
 
-    // what E (P, in its planes) and M (L) are multiplied with for dg: this thread's half row, fetched ahead as well
-    const int part = (warp >> 1) & 1, step = (warp & 1) * 32 + lane, j0 = half * 32;
-    uint4 factor[12];
+    // what E (P, in its planes) and M (L) are multiplied with for dg: this thread's quarter of a row, fetched ahead as well
+    const int part = (warp >> 1) & 1, step = (warp & 1) * 32 + lane, j0 = quarter * 16;
+    uint4 factor[6];
     auto fetch_factors = [&]() {
         if (part == 0) {
             const __nv_bfloat16* wP = record_P<T, DKP>(p, rec);
 #pragma unroll
-            for (int q = 0; q < 12; ++q)
-                factor[q] = __ldg(reinterpret_cast<const uint4*>(wP + (q >> 2) * DL_PLANE + plane_at(step, j0 + (q & 3) * 8)));
+            for (int q = 0; q < 6; ++q)
+                factor[q] = __ldg(reinterpret_cast<const uint4*>(wP + (q >> 1) * DL_PLANE + plane_at(step, j0 + (q & 1) * 8)));
         } else {
             const uint4* wL = reinterpret_cast<const uint4*>(p.wL + rec * DL_PLANE + step * DL_C + j0);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) factor[q] = __ldg(wL + q);
+            for (int q = 0; q < 4; ++q) factor[q] = __ldg(wL + q);
         }
     };
     float dots = 0.f;
-    float xw[4] = {};
+    float xw[NW] = {};
     for (int slab = 0; slab < p.dv; slab += 64) {
         const bool more = slab > 0;
 #pragma unroll
-        for (int i = 0; i < NS; ++i) put_planes(tiles + Sh::oS, Sh::plane, pr + 16 * i, pc, s0[i]);
+        for (int i = 0; i < NS; ++i) put_planes(tiles + Sh::oS, Sh::plane, pr + STEP * i, pc, s0[i]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = pr + 16 * i;
+        for (int i = 0; i < NW; ++i) {
+            const int r = pr + STEP * i;
             xw[i] += w[i].x * x[i].x + w[i].y * x[i].y + w[i].z * x[i].z + w[i].w * x[i].w;
             put_planes(tiles + Sh::oW, TC_TILE, r, pc, w[i]);
             const float beta = vec[2 * DL_C + r];
@@ -635,7 +640,7 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
         mbar_wait(done, phase, &sh->dead);
         phase ^= 1;
 #pragma unroll
-        for (int i = 0; i < NS; ++i) put_planes(tiles + Sh::oS, Sh::plane, pr + 16 * i, pc, ds[i]);
+        for (int i = 0; i < NS; ++i) put_planes(tiles + Sh::oS, Sh::plane, pr + STEP * i, pc, ds[i]);
         ready(2);
         if (slab + 64 < p.dv) {
             fetch(slab + 64);
@@ -647,32 +652,32 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
         phase ^= 1;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < NW; ++i) {
 #pragma unroll
         for (int q = 1; q < 16; q <<= 1) xw[i] += __shfl_xor_sync(0xffffffffu, xw[i], q);
-        if ((lane & 15) == 0) sh->xw[pr + 16 * i] = xw[i];
+        if ((lane & 15) == 0) sh->xw[pr + STEP * i] = xw[i];
     }
     tc_fence_after();
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) dots += __shfl_xor_sync(0xffffffffu, dots, o);
     if (lane == 0) sh->red[warp] = dots;
 
-    // E and M: rows 0-63 of D2 and rows 64-127, columns 32 half .. of this thread's step i
+    // E and M: rows 0-63 of D2 and rows 64-127, columns 16 quarter .. of this thread's step i
     {
         const int i = step;
-        float e[32], f[32];
-        tc_ld32(tl + c2 + j0, e);
-        tc_ld32(tl + c2 + cSmall + j0, f);
+        float e[16], f[16];
+        tc_ld16(tl + c2 + j0, e);
+        tc_ld16(tl + c2 + cSmall + j0, f);
         tc_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 32; ++k) e[k] += f[k];
+        for (int k = 0; k < 16; ++k) e[k] += f[k];
         if (part == 0) {  // P, whole again
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
+            for (int k = 0; k < 16; ++k) {
                 float z = 0.f;
 #pragma unroll
                 for (int n = 2; n >= 0; --n) {
-                    const uint4& u = factor[n * 4 + (k >> 3)];
+                    const uint4& u = factor[n * 2 + (k >> 3)];
                     const uint32_t a = (k >> 1 & 3) == 0 ? u.x : (k >> 1 & 3) == 1 ? u.y : (k >> 1 & 3) == 2 ? u.z : u.w;
                     z += __uint_as_float(k & 1 ? a & 0xffff0000u : a << 16);
                 }
@@ -680,7 +685,7 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
             }
         } else {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
+            for (int k = 0; k < 16; ++k) {
                 const uint4& u = factor[k >> 2];
                 f[k] = -__uint_as_float((k & 3) == 0 ? u.x : (k & 3) == 1 ? u.y : (k & 3) == 2 ? u.z : u.w);
             }
@@ -688,83 +693,80 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
         // a step's own product carries no decay: it is no part of dg. Blocks above the diagonal
         // hold nothing: selected, not multiplied by zero
         double sum = 0.0, col = 0.0;
-        float* h = reinterpret_cast<float*>(tiles + Sh::oS) + warp * (32 * 33);  // this warp's [row][column], over the states
+        float* h = reinterpret_cast<float*>(tiles + Sh::oS) + warp * (32 * 17);  // this warp's [row][column], over the states
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
+        for (int k = 0; k < 16; ++k) {
             f[k] = j0 + k < i ? e[k] * f[k] : 0.f;
-            h[lane * 33 + k] = f[k];
+            h[lane * 17 + k] = f[k];
             sum += (double)f[k];
         }
-        sh->hrow[part][half][i] = sum;
+        sums->hrow[part][quarter][i] = sum;
         __syncwarp();
 #pragma unroll 8
-        for (int k = 0; k < 32; ++k) col += (double)h[k * 33 + lane];
-        sh->hcol[warp & 3][j0 + lane] = col;
+        for (int k = 0; k < 16; ++k) col += (double)h[((lane & 16) + k) * 17 + (lane & 15)];  // half the rows a lane
+        col += __shfl_xor_sync(0xffffffffu, col, 16);
+        if (lane < 16) sums->hcol[warp & 3][j0 + lane] = col;
         const float2* G = reinterpret_cast<const float2*>(vec + 4 * DL_C);
         const float2 gi = G[i];
         const float sign = part == 0 ? p.scale : -1.f;
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
+        for (int k = 0; k < 16; ++k) {
             const float2 gj = G[j0 + k];
             const float d = decay_between<NP == 1>(gi, gj);
             e[k] = j0 + k <= i - part ? sign * (d * e[k]) : 0.f;
         }
         unsigned char* o = tiles + Sh::oX + part * TC_TILE;
 #pragma unroll
-        for (int k = 0; k < 32; k += 4) put_planes(o, 2 * TC_TILE, i, j0 + k, make_float4(e[k], e[k + 1], e[k + 2], e[k + 3]));
+        for (int k = 0; k < 16; k += 4) put_planes(o, 2 * TC_TILE, i, j0 + k, make_float4(e[k], e[k + 1], e[k + 2], e[k + 3]));
     }
     // D1 and D3, scaled, and their part of dg
     const int dk = (warp & 3) * 32 + lane;
     const bool live = dk < DKP;  // DKP = 64: the upper two warps of each four idle here
-    float dq[32], dkr[32], dkc[32];
+    float dq[16], dkr[16], dkc[16];
     {
-        float u[32], x[32];
-        tc_ld32(tl + c1 + half * 32, dq);
-        tc_ld32(tl + c1 + cSmall + half * 32, x);
+        float u[32], x[16];  // U's and V's parts
+        tc_ld16(tl + c1 + j0, dq);
+        tc_ld16(tl + c1 + cSmall + j0, x);
         tc_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) dq[i] += x[i];
-        tc_ld32(tl + c1 + 64 + half * 32, dkr);
-        tc_ld32(tl + c1 + cSmall + 64 + half * 32, x);
+        for (int i = 0; i < 16; ++i) dq[i] += x[i];
+        tc_ld16(tl + c1 + 64 + j0, dkr);
+        tc_ld16(tl + c1 + cSmall + 64 + j0, x);
         tc_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) dkr[i] += x[i];
-        tc_ld32(tl + c3 + half * 32, dkc);
-        tc_ld32(tl + c3 + cSmall + half * 32, x);
+        for (int i = 0; i < 16; ++i) dkr[i] += x[i];
+        tc_ld16(tl + c3 + j0, dkc);
+        tc_ld16(tl + c3 + cSmall + j0, x);
         tc_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) dkc[i] += x[i];
-        if (live) column_of<NP, DKP>(tiles + Sh::oQ, Sh::plane, dk, half * 32, x);
+        for (int i = 0; i < 16; ++i) dkc[i] += x[i];
+        if (live) column_of<NP, DKP>(tiles + Sh::oQ, Sh::plane, dk, j0, x);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const float eG = vec[half * 32 + i];
+        for (int i = 0; i < 16; ++i) {
+            const float eG = vec[j0 + i];
             dq[i] *= p.scale * eG;
             dkr[i] *= -eG;
-            dkc[i] *= vec[DL_C + half * 32 + i];
+            dkc[i] *= vec[DL_C + j0 + i];
             u[i] = live ? x[i] * dq[i] : 0.f;
         }
-        if (live) column_of<NP, DKP>(tiles + Sh::oK, Sh::plane, dk, half * 32, x);
+        if (live) column_of<NP, DKP>(tiles + Sh::oK, Sh::plane, dk, j0, x);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) u[i] += live ? x[i] * dkr[i] : 0.f;
-        sh->U[warp & 3][half * 32 + lane] = reduce_columns(u, lane);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = live ? x[i] * dkc[i] : 0.f;
-        sh->V[warp & 3][half * 32 + lane] = reduce_columns(x, lane);
+        for (int i = 0; i < 16; ++i) {
+            u[i] += live ? x[i] * dkr[i] : 0.f;
+            u[16 + i] = live ? x[i] * dkc[i] : 0.f;
+        }
+        (lane < 16 ? sums->U : sums->V)[warp & 3][j0 + (lane & 15)] = reduce_columns(u, lane);
     }
     tc_fence_before();
-    bar_sync(4, 256);  // the parts of dg are there, and the columns behind cSmall read
+    bar_sync(4, DG_COMPUTE);  // the parts of dg are there, and the columns behind cSmall read
     tc_fence_after();
-    // K^T (half 0) and Q^T: this thread's key channel, all steps
+    // K^T and Q^T: this thread's key channel, half the steps of one of them
     {
-        const unsigned char* tile = tiles + (half ? Sh::oQ : Sh::oK);
-        const uint32_t to = tl + (half ? cQT : cKT);
+        const int which = quarter & 1, h = quarter >> 1;
         if ((warp & 3) * 32 < DKP) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float x[32];
-                column_of<NP, DKP>(tile, Sh::plane, dk, h * 32, x);
-                put_terms<NP, NP == 3>(to + h * 16, 32, x);
-            }
+            float x[32];
+            column_of<NP, DKP>(tiles + (which ? Sh::oQ : Sh::oK), Sh::plane, dk, h * 32, x);
+            put_terms<NP, NP == 3>(tl + (which ? cQT : cKT) + h * 16, 32, x);
         }
     }
     tc_wait_st();
@@ -772,27 +774,27 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
     mbar_wait(done, phase, &sh->dead);
     tc_fence_after();
     {
-        float x[32];
-        tc_ld32(tl + c1 + half * 32, x);
+        float x[16];
+        tc_ld16(tl + c1 + j0, x);
         tc_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) dq[i] += x[i];
-        tc_ld32(tl + c1 + 64 + half * 32, x);
+        for (int i = 0; i < 16; ++i) dq[i] += x[i];
+        tc_ld16(tl + c1 + 64 + j0, x);
         tc_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) dkr[i] += x[i];
-        tc_ld32(tl + c3 + half * 32, x);
+        for (int i = 0; i < 16; ++i) dkr[i] += x[i];
+        tc_ld16(tl + c3 + j0, x);
         tc_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) dkc[i] += dkr[i] + x[i];
+        for (int i = 0; i < 16; ++i) dkc[i] += dkr[i] + x[i];
     }
     // rows out, over the states' place
-    const int* rows = sh->rows + half * 32;
+    const int* rows = sh->rows + j0;
     const size_t first = (size_t)img * p.tokens;
     if ((warp & 3) * 32 < DKP) {
         const int have = p.dk - (warp & 3) * 32;
         if (p.wdq) {
-            float* mine = reinterpret_cast<float*>(tiles + Sh::oS) + warp * (32 * 36) + lane;
+            float* mine = reinterpret_cast<float*>(tiles + Sh::oS) + warp * (16 * 36) + lane;
             const long long tok = (long long)p.heads_v * p.dk;
             const size_t o = (first * p.heads_v + head) * p.dk + (warp & 3) * 32;
             walk_store(p.wdq + o, tok, rows, mine, 36, have, lane, dq);
@@ -800,7 +802,7 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
             walk_store(p.wdk + o, tok, rows, mine, 36, have, lane, dkc);
         } else {
             constexpr int pitch = 32 + 16 / (int)sizeof(T);
-            T* mine = reinterpret_cast<T*>(tiles + Sh::oS) + warp * (32 * pitch) + lane;
+            T* mine = reinterpret_cast<T*>(tiles + Sh::oS) + warp * (16 * pitch) + lane;
             const long long tok = (long long)p.heads_k * p.dk;
             const size_t o = (first * p.heads_k + hk) * p.dk + (warp & 3) * 32;
             if (p.dq) walk_store(reinterpret_cast<T*>(p.dq) + o, tok, rows, mine, pitch, have, lane, dq);
