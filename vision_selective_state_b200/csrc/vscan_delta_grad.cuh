@@ -434,6 +434,7 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
     };
     auto fetch = [&](int slab) {
         fetch_state(s0, wS, slab);
+        fetch_state(ds, wdS, slab);
         const bool in = slab + pc < p.dv;
 #pragma unroll
         for (int i = 0; i < NW; ++i) {
@@ -470,6 +471,18 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
     auto aK = [&](int x, int ks) { return tm + cKT + x * 32 + ks * 8; };
 
     if (warp == DG_COMPUTE / 32) {  // issues the products
+        // what dg, da and db need of a and b, two steps a lane, ahead of the sums
+        const float A = p.A[head], bias = p.bias ? p.bias[head] : 0.f;
+        float soft[2], slope[2], open[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = sh->rows[2 * lane + i];
+            const float a = (row >= 0 ? to_float(reinterpret_cast<const T*>(p.a)[img * p.a_img + row * p.a_tok + head]) : 0.f) + bias;
+            const float bb = row >= 0 ? to_float(reinterpret_cast<const T*>(p.b)[img * p.b_img + row * p.b_tok + head]) : 0.f;
+            soft[i] = delta_softplus(a);
+            slope[i] = A * delta_sigmoid(a);
+            open[i] = delta_sigmoid(-bb);
+        }
         for (int slab = 0; slab < p.dv; slab += 64) {
             const bool more = slab > 0;
             bar_sync(1, DG_THREADS);
@@ -549,22 +562,19 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
         }
         before -= v[0] + v[1];
         const double dg[2] = {base + sum + before, base + (sum - x[0]) + (before + v[0])};
-        const float A = p.A[head], bias = p.bias ? p.bias[head] : 0.f;
         double sA = 0.0, sb = 0.0;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int r = 2 * lane + i;
             if (t0 + r >= s.len) continue;
             const int row = sh->rows[r];
-            const float a = row >= 0 ? to_float(reinterpret_cast<const T*>(p.a)[img * p.a_img + row * p.a_tok + head]) : 0.f;
-            const float da = (float)dg[i] * A * delta_sigmoid(a + bias);
-            sA += dg[i] * (double)delta_softplus(a + bias);
+            const float da = (float)dg[i] * slope[i];
+            sA += dg[i] * (double)soft[i];
             sb += (double)da;
             if (row >= 0) {
                 const size_t o = (size_t)(img * p.tokens + row) * p.heads_v + head;
-                const float bb = to_float(reinterpret_cast<const T*>(p.b)[img * p.b_img + row * p.b_tok + head]);
                 if (p.da) store_elem(reinterpret_cast<T*>(p.da) + o, da);
-                if (p.db) store_elem(reinterpret_cast<T*>(p.db) + o, sh->xw[r] * delta_sigmoid(-bb));
+                if (p.db) store_elem(reinterpret_cast<T*>(p.db) + o, sh->xw[r] * open[i]);
             }
         }
 #pragma unroll
@@ -634,7 +644,6 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
         if (!more) cp_async_wait<0>();
         ready(1);
         // the gradient of the state leaving the chunk, over the one entering it once D1 has read that
-        fetch_state(ds, wdS, slab);
 #pragma unroll
         for (int i = 0; i < NS; ++i) dots += ds[i].x * s0[i].x + ds[i].y * s0[i].y + ds[i].z * s0[i].z + ds[i].w * s0[i].w;
         mbar_wait(done, phase, &sh->dead);
