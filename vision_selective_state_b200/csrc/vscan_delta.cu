@@ -15,6 +15,7 @@ using vscan_host::cuda_fail;
 using vscan_host::fail;
 using vscan_host::NvtxRange;
 using vscan_host::round256;
+using vscan_host::launch_after;
 using vscan_host::set_smem_once;
 using vscan::DeltaParams;
 using vscan::DL_C;
@@ -202,8 +203,8 @@ cudaError_t launch_prep(const DeltaParams& p, cudaStream_t stream)
     constexpr size_t smem = vscan::PrepShape<T, DKP>::smem;
     cudaError_t e = set_smem_once(vscan::delta_prep_kernel<T, DKP, PP>, (int)smem, done, kAttrDevices);
     if (e != cudaSuccess) return e;
-    vscan::delta_prep_kernel<T, DKP, PP><<<dim3((unsigned)p.slots, p.heads_v), vscan::DP_THREADS, smem, stream>>>(p);
-    return cudaGetLastError();
+    return launch_after(false, vscan::delta_prep_kernel<T, DKP, PP>, dim3((unsigned)p.slots, p.heads_v), vscan::DP_THREADS, smem,
+                        stream, p);
 }
 
 dim3 walk_grid(const DeltaParams& p) { return dim3((p.dv + 127) / 128, p.heads_v, p.batch); }
@@ -216,8 +217,8 @@ cudaError_t launch_scan(const DeltaParams& p, cudaStream_t stream)
     constexpr size_t smem = Sh::smem(Sh::PP);
     const cudaError_t e = set_smem_once(vscan::delta_scan_kernel<T, DKP, SAVE>, (int)smem, done, kAttrDevices);
     if (e != cudaSuccess) return e;
-    vscan::delta_scan_kernel<T, DKP, SAVE><<<walk_grid(p), vscan::DW_THREADS, smem, stream>>>(p);
-    return cudaGetLastError();
+    return launch_after(p.slots > 0 && p.tokens > 0, vscan::delta_scan_kernel<T, DKP, SAVE>, walk_grid(p), vscan::DW_THREADS, smem,
+                        stream, p);
 }
 
 template <typename T, int DKP>
@@ -233,27 +234,26 @@ cudaError_t run_backward(const DeltaParams& p, cudaStream_t stream)
 {
     static int done_r[kAttrDevices], done_g[kAttrDevices];
     cudaError_t e;
-    if (p.tokens > 0 && p.slots > 0) {
+    const bool any = p.tokens > 0 && p.slots > 0;
+    if (any) {
         if ((e = launch_prep<T, DKP, 3>(p, stream)) != cudaSuccess) return e;
         if ((e = launch_scan<T, DKP, true>(p, stream)) != cudaSuccess) return e;
     }
     constexpr size_t walk = vscan::WalkShape<T, DKP>::smem(3);
     if ((e = set_smem_once(vscan::delta_rscan_kernel<T, DKP>, (int)walk, done_r, kAttrDevices)) != cudaSuccess) return e;
-    vscan::delta_rscan_kernel<T, DKP><<<walk_grid(p), vscan::DW_THREADS, walk, stream>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (p.tokens > 0 && p.slots > 0) {
+    if ((e = launch_after(any, vscan::delta_rscan_kernel<T, DKP>, walk_grid(p), vscan::DW_THREADS, walk, stream, p)) != cudaSuccess) return e;
+    if (any) {
         constexpr size_t smem = vscan::GradShape<T, DKP>::smem;
         if ((e = set_smem_once(vscan::delta_grad_kernel<T, DKP>, (int)smem, done_g, kAttrDevices)) != cudaSuccess) return e;
-        vscan::delta_grad_kernel<T, DKP><<<dim3((unsigned)p.slots, p.heads_v), vscan::DG_THREADS, smem, stream>>>(p);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        e = launch_after(true, vscan::delta_grad_kernel<T, DKP>, dim3((unsigned)p.slots, p.heads_v), vscan::DG_THREADS, smem, stream, p);
+        if (e != cudaSuccess) return e;
         if (p.wdq && (p.dq || p.dkey)) {
             const long long vecs = (long long)(p.offsets ? 1 : p.batch) * p.tokens * p.heads_k * (p.dk / 4);
-            vscan::delta_group_kernel<T><<<dim3((unsigned)((vecs + 255) / 256), 2), 256, 0, stream>>>(p, vecs);
-            if ((e = cudaGetLastError()) != cudaSuccess) return e;
+            e = launch_after(true, vscan::delta_group_kernel<T>, dim3((unsigned)((vecs + 255) / 256), 2), 256, 0, stream, p, vecs);
+            if (e != cudaSuccess) return e;
         }
     }
-    if (p.dA || p.dbias) vscan::delta_param_grad_kernel<<<p.heads_v, 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    return p.dA || p.dbias ? launch_after(true, vscan::delta_param_grad_kernel, dim3(p.heads_v), 256, 0, stream, p) : cudaSuccess;
 }
 
 // f(width) with the I/O type and the padded key width as template arguments.

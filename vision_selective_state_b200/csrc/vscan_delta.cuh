@@ -389,6 +389,7 @@ __global__ void __launch_bounds__(DP_THREADS, DeltaIo<T>::planes == 1 ? 4 : 3) d
     int* rows = reinterpret_cast<int*>(upto + 4 * DL_C);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, head = blockIdx.y;
     const int group = warp >> 2, m0 = (warp & 3) * 16;
+    start_next();
 
     // the sequence of this slot
     int b;
@@ -914,6 +915,7 @@ __device__ __forceinline__ void walk_end(WalkShared* w, uint32_t tm, int* status
     tc_wait_st();
     tc_fence_before();
     __syncthreads();
+    start_next();
     if (threadIdx.x == 0 && status && w->dead) atomicOr(status, DEV_STATUS_TIMEOUT);
     if (threadIdx.x < 32) tc_free(tm);
 }
@@ -967,6 +969,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_scan_kernel(const DeltaPa
     const size_t sbase = ((size_t)b * p.heads_v + head) * p.dk * p.dv;
     const WalkBars bar(ws);
     const uint32_t tm = walk_begin(ws, bar);
+    wait_previous();
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(DW_REGS_HELP));

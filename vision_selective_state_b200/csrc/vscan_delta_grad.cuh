@@ -58,6 +58,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaP
     const size_t sbase = ((size_t)b * p.heads_v + head) * p.dk * p.dv;
     const WalkBars bar(ws);
     const uint32_t tm = walk_begin(ws, bar);
+    wait_previous();
     // n counts the chunks in the order of the walk, from the last to the first
 
     if (warp >= 8) {
@@ -388,6 +389,7 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
     extern __shared__ unsigned char smem_raw[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quarter = warp >> 2;
     const int head = blockIdx.y, hk = head / p.group;
+    wait_previous();
 
     int b;
     if (p.offsets) {
@@ -797,6 +799,7 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
 #pragma unroll
         for (int i = 0; i < 16; ++i) dkc[i] += dkr[i] + x[i];
     }
+    start_next();
     // rows out, over the states' place
     const int* rows = sh->rows + j0;
     const size_t first = (size_t)img * p.tokens;
@@ -830,6 +833,7 @@ __global__ void __launch_bounds__(256) delta_param_grad_kernel(const DeltaParams
 {
     __shared__ double part[2][8];
     const int head = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    wait_previous();
     double sA = 0.0, sb = 0.0;
     for (long long i = tid; i < p.slots; i += 256) {
         const float2 x = *reinterpret_cast<const float2*>(p.wpart + 2 * ((size_t)i * p.heads_v + head));
@@ -855,6 +859,8 @@ __global__ void __launch_bounds__(256) delta_param_grad_kernel(const DeltaParams
 template <typename T>
 __global__ void __launch_bounds__(256) delta_group_kernel(const DeltaParams p, long long vecs)
 {
+    wait_previous();
+    start_next();
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;  // four channels of one row and key head
     if (i >= vecs) return;
     const int per = p.dk / 4;

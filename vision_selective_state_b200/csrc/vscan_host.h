@@ -53,4 +53,23 @@ cudaError_t set_smem_once(Kernel* fn, int bytes, int* done_by_device, int max_de
     return e;
 }
 
+// Launch a kernel; with `after`, one that follows another of the same call on the stream: its blocks
+// may come before that one has ended (programmatic dependent launch) and have to wait for its end
+// themselves. Saves the launch latency between the kernels of small calls.
+template <typename... P>
+cudaError_t launch_after(bool after, void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, P... args)
+{
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t config{};
+    config.gridDim = grid;
+    config.blockDim = dim3(threads);
+    config.dynamicSmemBytes = smem;
+    config.stream = stream;
+    config.attrs = &attr;
+    config.numAttrs = after ? 1 : 0;
+    return cudaLaunchKernelEx(&config, kernel, args...);
+}
+
 }  // namespace vscan_host

@@ -14,6 +14,7 @@ using vscan::QkNormParams;
 using vscan_host::aligned16;
 using vscan_host::cuda_fail;
 using vscan_host::fail;
+using vscan_host::launch_after;
 using vscan_host::NvtxRange;
 
 constexpr int kMaxBlocks = 148 * 4;  // of q and as many of k: eight CTAs of 256 threads an SM
@@ -215,9 +216,8 @@ vscan_status vscan_qknorm_backward(const vscan_qknorm_args* args, const vscan_qk
     p.part = weights ? static_cast<float*>(grads->workspace) : nullptr;
     e = launch<true>(args, p, v, s);
     if (e == cudaSuccess && weights) {
-        vscan::qk_norm_weight_kernel<<<dim3((args->dim + 31) / 32, 2), vscan::QN_SUM_THREADS, 0, s>>>(p.part, p.blocks, args->dim,
-                                                                                             grads->dwq, grads->dwk);
-        e = cudaGetLastError();
+        e = launch_after(true, vscan::qk_norm_weight_kernel, dim3((args->dim + 31) / 32, 2), vscan::QN_SUM_THREADS, 0, s,
+                         (const float*)p.part, p.blocks, (int)args->dim, grads->dwq, grads->dwk);
     }
     return e == cudaSuccess ? VSCAN_OK : cuda_fail(e, "vscan_qknorm_backward");
 }

@@ -24,6 +24,7 @@
 #include <stdint.h>
 
 #include "vscan_common.cuh"
+#include "vscan_tc.cuh"
 
 namespace vscan {
 
@@ -329,6 +330,7 @@ __global__ void __launch_bounds__(QN_THREADS, BACK ? 3 : 4) qk_norm_kernel(const
                 const int base = e < V ? lo[u] : hi[u];
                 if (lane < p.lanes && base >= 0) wsum[warp * p.d + base + (e < V ? e : e - V)] = a;
             }
+        start_next();
         __syncthreads();
         for (int i = tid; i < p.d; i += QN_THREADS) {
             float a = 0.f;
@@ -344,6 +346,7 @@ __global__ void __launch_bounds__(QN_SUM_THREADS) qk_norm_weight_kernel(const fl
 {
     __shared__ double sum[QN_SUM_THREADS / 32][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = blockIdx.x * 32 + lane;
+    wait_previous();
     float* dst = blockIdx.y ? dwk : dwq;
     double a = 0.0;
     if (i < d && dst) {

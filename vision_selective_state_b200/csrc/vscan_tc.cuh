@@ -113,6 +113,13 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r)
                  : "memory");
 }
 
+// ---- launches that follow one another ------------------------------------------------
+// A call's kernels each start while the one before ends (launch_after): start_next lets the next
+// one's blocks come as soon as all of this one's have got that far, and wait_previous, which
+// every block executes before it reads what the one before wrote or returns, waits for its end.
+__device__ __forceinline__ void start_next() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+
 // ---- barriers ------------------------------------------------------------------------
 __device__ __forceinline__ void mbar_init(uint32_t mbar, int count)
 {
