@@ -47,7 +47,8 @@
 namespace vscan {
 
 constexpr int DL_C = 64;          // steps per chunk
-// Floats per chunk in the workspace: e^{G_i}, e^{G_C - G_i}, beta_i, {e^{G_C}}, and G_i rounded and the rest of it.
+// Floats per chunk in the workspace: e^{G_i}, e^{G_C - G_i}, beta_i, {e^{G_C}}, G_i rounded and the rest of it (two
+// each), -beta_i e^{G_i}.
 constexpr int DL_VECS = 8 * DL_C;  // 2048 bytes, so that the planes behind them keep their alignment
 constexpr int DL_PLANE = DL_C * DL_C;
 
@@ -550,7 +551,9 @@ __global__ void __launch_bounds__(DP_THREADS, DeltaIo<T>::planes == 1 ? 4 : 3) d
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int r = 2 * lane + i;
-            vec[r] = exp_diff(g[i]);
+            const float e = exp_diff(g[i]);
+            vec[r] = e;
+            vec[6 * DL_C + r] = -beta[r] * e;
             vec[DL_C + r] = exp_diff(last - g[i]);
             vec[2 * DL_C + r] = beta[r];
         }
@@ -837,6 +840,41 @@ __device__ __forceinline__ float upper_terms(float x)
 {
     const float h = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
     return h + __uint_as_float(__float_as_uint(x - h) & 0xffff0000u);
+}
+
+// x * s and x * s + z, two values at a time; s in shared memory.
+__device__ __forceinline__ void scale_row(float (&x)[32], const float* s)
+{
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+        const float2 r = __fmul2_rn(make_float2(x[i], x[i + 1]), *reinterpret_cast<const float2*>(s + i));
+        x[i] = r.x;
+        x[i + 1] = r.y;
+    }
+}
+__device__ __forceinline__ void scale_add_row(float (&x)[32], const float* s, const float (&z)[32])
+{
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+        const float2 r = __ffma2_rn(make_float2(x[i], x[i + 1]), *reinterpret_cast<const float2*>(s + i), make_float2(z[i], z[i + 1]));
+        x[i] = r.x;
+        x[i + 1] = r.y;
+    }
+}
+// S = e S + half a row in the tensor-memory columns from `from` on.
+template <int HS>
+__device__ __forceinline__ void advance_state(float (&S)[HS], float e, uint32_t from)
+{
+    float x[HS];
+#pragma unroll
+    for (int i = 0; i < HS; i += 32) tc_ld32(from + i, x + i);
+    tc_wait_ld();
+#pragma unroll
+    for (int i = 0; i < HS; i += 2) {
+        const float2 r = __ffma2_rn(make_float2(S[i], S[i + 1]), make_float2(e, e), make_float2(x[i], x[i + 1]));
+        S[i] = r.x;
+        S[i + 1] = r.y;
+    }
 }
 
 // S's (dS's) terms: half a row's lie side by side, three of SC columns.
@@ -1129,9 +1167,9 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_scan_kernel(const DeltaPa
                 mbar_wait(bar.done, par, &ws->dead);
                 tc_fence_after();
                 tc_ld32(tl + cKS + half * 32, x);
+                scale_row(u, vec + 2 * DL_C);
                 tc_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = vec[2 * DL_C + i] * (u[i] - vec[i] * x[i]);  // X^T = beta (V - e^G K S)^T
+                scale_add_row(x, vec + 6 * DL_C, u);  // X^T = beta (V - e^G K S)^T
             }
             put_terms<3>(tl + cX + half * 48, 16, x);
             walk_ready(2);
@@ -1151,7 +1189,8 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_scan_kernel(const DeltaPa
             {
                 float w[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) w[i] = x[i] * vec[DL_C + i];
+                for (int i = 0; i < 32; ++i) w[i] = x[i];
+                scale_row(w, vec + DL_C);
                 put_terms<3>(tl + cX + half * 48, 16, w);
                 walk_ready(3);
             }
@@ -1177,13 +1216,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_scan_kernel(const DeltaPa
             const float eC = vec[3 * DL_C - half * 32];
             mbar_wait(bar.done + 24, par, &ws->dead);
             tc_fence_after();
-#pragma unroll
-            for (int i = 0; i < HS; i += 32) {
-                tc_ld32(tl + cDS + (DKP == 128 ? half * 3 * Sh::SC : half * 32) + i, x);
-                tc_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) S[i + e] = eC * S[i + e] + x[e];
-            }
+            advance_state(S, eC, tl + cDS + half * (DKP == 128 ? 3 * Sh::SC : 32));
             mbar_arrive(bar.empty + 8 * st);
             if (c + 1 < chunks) {
                 put_state<HS, Sh::SC>(tl + cS + half * 3 * Sh::SC, S);

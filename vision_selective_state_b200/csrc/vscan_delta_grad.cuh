@@ -201,8 +201,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaP
                 tc_ld32(tl + c1 + half * 32, x);
                 tc_ld32(tl + c2 + half * 32, z);
                 tc_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = vec[DL_C + i] * x[i] + z[i];
+                scale_add_row(x, vec + DL_C, z);
             }
             put_terms<3>(tl + cW + half * 48, 16, x);
             walk_ready(3);
@@ -214,16 +213,9 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaP
             tc_ld32(tl + c1 + half * 32, x);
             tc_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                o[i] = x[i];
-                x[i] *= vec[2 * DL_C + i];  // dV
-            }
-            {
-                float u[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) u[i] = x[i] * -vec[i];
-                put_terms<3>(tl + cW + half * 48, 16, u);
-            }
+            for (int i = 0; i < 32; ++i) o[i] = x[i];
+            scale_row(x, vec + 6 * DL_C);
+            put_terms<3>(tl + cW + half * 48, 16, x);  // -e^G dV
             walk_ready(5);
             if (live) {
                 float* ox = p.wdX + (rec * DL_C + half * 32) * p.dv + vc;
@@ -231,6 +223,9 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaP
                 for (int i = 0; i < 32; ++i) ox[(size_t)i * p.dv] = o[i];
             }
             if (dvalue) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = o[i];
+                scale_row(x, vec + 2 * DL_C);
                 if constexpr (NP == 1)
                     walk_store(dvalue, (long long)p.heads_v * p.dv, ws->rows[n % 4] + half * 32, vd, Sh::vpitch, p.dv - vc + lane,
                                lane, x);
@@ -240,13 +235,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaP
             const float eC = vec[3 * DL_C - half * 32];
             mbar_wait(bar.done + 16, par, &ws->dead);
             tc_fence_after();
-#pragma unroll
-            for (int i = 0; i < HS; i += 32) {
-                tc_ld32(tl + cDS + (DKP == 128 ? half * 3 * Sh::SC : half * 32) + i, x);
-                tc_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) S[i + e] = eC * S[i + e] + x[e];
-            }
+            advance_state(S, eC, tl + cDS + half * (DKP == 128 ? 3 * Sh::SC : 32));
             mbar_arrive(bar.empty + 8 * st);
             if (n + 1 < chunks) {
                 put_state<HS, Sh::SC>(tl + cS + half * 3 * Sh::SC, S);
