@@ -213,6 +213,17 @@ def test_the_binding_refuses_what_it_cannot_marshal():
         vs.qk_norm(q.double(), q.double())
 
 
+def test_the_binding_refuses_an_expanded_axis():
+    from vision_selective_state_b200.delta import _row_strides, head_strides
+    x, row = torch.zeros(1, 1, 2, 16), torch.zeros(1, 1, 2)
+    for shape in ((3, 1, 2, 16), (1, 3, 2, 16), (3, 5, 2, 16)):
+        with pytest.raises(ValueError, match="stride of 0"):
+            head_strides("q", x.expand(shape), False)
+        with pytest.raises(ValueError, match="stride of 0"):
+            _row_strides("a", row.expand(shape[:3]), False)
+    assert head_strides("q", x.expand(1, 1, 2, 16), False) == (32, 32)
+
+
 # ------------------------------------------------------------------ the float64 forms themselves
 def test_the_reference_step_on_a_worked_example():
     """One head of width one: S = 2, decay 1/2, beta 1/2, k = 1, v = 3: S' = 1 + (3 - 1) / 2 = 2, y = 2 q."""

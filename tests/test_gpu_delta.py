@@ -337,3 +337,24 @@ def test_one_head_shared_by_many_and_sizes_at_the_limits():
         ry, rS = R.delta_ref(x)
         R.close(y, ry, "f32", R.ACC_FORWARD, f"y {hk} {hv} {dk} {dv}")
         R.close(S, rS, "f32", R.ACC_FORWARD, "state")
+
+
+def test_expanded_inputs_and_foreign_workspaces_are_refused():
+    x = to_gpu(f32(R.delta_inputs(3, 2, 5, 1, 1, 16, 16, "f32")), "f32")
+    names = ("q", "k", "v", "a", "b", "A", "bias")
+    for name in ("q", "k", "v", "a", "b"):
+        for axis in (0, 1):
+            one = x[name].narrow(axis, 0, 1).expand(x[name].shape)
+            with pytest.raises(ValueError, match="stride of 0"):
+                vs.delta_forward(*(one if n == name else x[n] for n in names))
+    step = [x[n] if n in ("A", "bias") else x[n][:, 0].contiguous() for n in names]
+    state = torch.zeros(2, 1, 16, 16, device=DEV)
+    step[0] = step[0][:1].expand(step[0].shape)
+    with pytest.raises(ValueError, match="stride of 0"):
+        vs.delta_step(*step, state=state)
+    with pytest.raises(ValueError, match="stride of 0"):
+        vs.qk_norm(x["q"], x["k"][:1].expand(x["k"].shape))
+    with pytest.raises(ValueError, match="workspace"):
+        vs.delta_forward(*(x[n] for n in names), workspace=torch.zeros(1 << 20, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="workspace"):
+        vs.delta_backward(*(x[n] for n in names), dy=x["v"], workspace=torch.zeros(1 << 20, dtype=torch.uint8))

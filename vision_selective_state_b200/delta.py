@@ -13,7 +13,8 @@ beta = beta_scale sigmoid(b),
     states  : [batch, heads_v, dim_k, dim_v] float32
 
 q, k, v, a, b and y share one dtype: torch.float32 or torch.bfloat16. Token and image strides
-are free (slices of a wider projection output); the heads of one token are contiguous. As in
+are free (slices of a wider projection output) but not 0 (an expanded axis is refused); the
+heads of one token are contiguous. As in
 the rest of the package, the binding only marshals tensors; the arithmetic runs in libvscan.so.
 """
 import contextlib
@@ -25,7 +26,9 @@ from . import _abi
 from ._abi import BF16, F32, ROUTES, VscanDeltaGrads, check
 
 CODES = {torch.float32: F32, torch.bfloat16: BF16}
+_f32 = torch.float32
 _here = contextlib.nullcontext()
+_dense = (0,) * 12  # strides of six dense tensors
 _pack = _abi.delta_forward.pack
 
 
@@ -65,6 +68,16 @@ def check_dense(name, t, shape, dtype, index):
         raise ValueError(f"{name} must be contiguous")
 
 
+def fits(dtype, index, *pairs):
+    """Whether every (tensor, shape) has the dtype, device and shape asked for: one look at what
+    check_tensor would refuse one by one. The smallest calls take less time on the device
+    than their checks do here."""
+    for t, shape in pairs:
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+            return False
+    return True
+
+
 def device_index(q):
     """Index of the tensors' device, and the dtype's code."""
     code = CODES.get(q.dtype)
@@ -76,6 +89,13 @@ def device_index(q):
     return index, code
 
 
+def _spaced(name, t):
+    """Refuse a broadcast axis: the ABI reads a stride of 0 as dense."""
+    for size, stride in zip(t.shape[:2], t.stride()):
+        if stride == 0 and size > 1:
+            raise ValueError(f"{name} repeats one row (a stride of 0): make it contiguous")
+
+
 def head_strides(name, t, dense):
     """(token, image) strides of a [batch, tokens, heads, dim] tensor with contiguous heads;
     a size-1 axis has no meaningful stride and takes the dense value (0)."""
@@ -85,6 +105,7 @@ def head_strides(name, t, dense):
     sb, sn, sh, sd = t.stride()
     if (sd != 1 and d > 1) or (sh != d and h > 1):
         raise ValueError(f"the heads of one token of {name} must be contiguous")
+    _spaced(name, t)
     tok = sn if n > 1 else h * d
     return tok, (sb if b > 1 else n * tok)
 
@@ -96,6 +117,7 @@ def _row_strides(name, t, dense):
     b, n, h = t.shape
     if t.stride(2) != 1 and h > 1:
         raise ValueError(f"the heads of one token of {name} must be contiguous")
+    _spaced(name, t)
     tok = t.stride(1) if n > 1 else h
     return tok, (t.stride(0) if b > 1 else n * tok)
 
@@ -166,10 +188,15 @@ def _state_shape(q, v, seq_offsets):
     return (q.shape[0] if seq_offsets is None else seq_offsets.numel() - 1, v.shape[2], q.shape[3], v.shape[3])
 
 
-def _scratch(query, handle, fields, q):
-    need = ctypes.c_uint64()
-    check(query.fn(handle, _pack(*fields, 0, 0, 0), ctypes.byref(need)))
-    return q.new_empty(need.value, dtype=torch.uint8)
+def _scratch(given, query, handle, fields, q, index):
+    """(workspace, its address, its bytes)."""
+    if given is None:
+        need = ctypes.c_uint64()
+        check(query.fn(handle, _pack(*fields, 0, 0, 0), ctypes.byref(need)))
+        given = q.new_empty(need.value, dtype=torch.uint8)
+    elif given.get_device() != index or not given.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on cuda:{index}")
+    return given, given.data_ptr(), given.numel() * given.element_size()
 
 
 def delta_forward(q, k, v, a, b, A, bias=None, *, route=None, direction=0, seq_offsets=None, scale=None,
@@ -194,9 +221,8 @@ def delta_forward(q, k, v, a, b, A, bias=None, *, route=None, direction=0, seq_o
     index, fields = _fields(q, k, v, a, b, A, bias, out, direction, seq_offsets, scale, beta_scale, initial_state,
                             final_state)
     handle = _route_handle(route)
-    if workspace is None:
-        workspace = _scratch(_abi.delta_workspace_size, handle, fields, q)
-    args = _pack(*fields, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _status(status, index))
+    workspace, *scratch = _scratch(workspace, _abi.delta_workspace_size, handle, fields, q, index)
+    args = _pack(*fields, *scratch, _status(status, index))
     with on_device(index):
         check(_abi.delta_forward.fn(handle, args, stream_handle(stream, index, out, final_state, workspace)))
     return out if final_state is None else (out, final_state)
@@ -229,9 +255,8 @@ def delta_backward(q, k, v, a, b, A, bias=None, *, dy, route=None, direction=0, 
         check_dense("d_final_state", d_final_state, _state_shape(q, v, seq_offsets), torch.float32, index)
         grads.d_final_state = d_final_state.data_ptr()
     handle = _route_handle(route)
-    if workspace is None:
-        workspace = _scratch(_abi.delta_backward_workspace_size, handle, fields, q)
-    grads.workspace, grads.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    workspace, grads.workspace, grads.workspace_bytes = _scratch(workspace, _abi.delta_backward_workspace_size, handle,
+                                                                 fields, q, index)
     args = _pack(*fields, 0, 0, _status(status, index))
     with on_device(index):
         check(_abi.delta_backward.fn(handle, args, dy.data_ptr(), ctypes.byref(grads),
@@ -252,29 +277,37 @@ def delta_step(q, k, v, a, b, A, bias=None, *, state, state_out=None, scale=None
     dtype, shape, wide = q.dtype, q.shape, v.shape
     batch, hk, dk = shape
     hv, dv = wide[1:]
+    heads, table = (batch, hv), (batch, hv, dk, dv)
+    if not fits(dtype, index, (k, shape), (v, (batch, hv, dv)), (a, heads), (b, heads)):
+        check_tensor("k", k, shape, dtype, index)
+        check_tensor("v", v, (batch, hv, dv), dtype, index)
+        check_tensor("a", a, heads, dtype, index)
+        check_tensor("b", b, heads, dtype, index)
     if out is None:
         out = fresh(v)
+    else:
+        check_tensor("y", out, wide, dtype, index)
     if state_out is None:
         state_out = state
-    check_tensor("k", k, shape, dtype, index)
-    check_tensor("v", v, (batch, hv, dv), dtype, index)
-    check_tensor("a", a, (batch, hv), dtype, index)
-    check_tensor("b", b, (batch, hv), dtype, index)
-    check_tensor("y", out, wide, dtype, index)
-    check_dense("A", A, (hv,), torch.float32, index)
-    if bias is not None:
-        check_dense("bias", bias, (hv,), torch.float32, index)
-    check_dense("state", state, (batch, hv, dk, dv), torch.float32, index)
-    if state_out is not state:
-        check_dense("state_out", state_out, (batch, hv, dk, dv), torch.float32, index)
-    strides = []
-    for name, t in (("q", q), ("k", k), ("v", v), ("a", a), ("b", b), ("y", out)):
-        if t.is_contiguous():
-            strides += (0, 0)
-        elif t.dim() == 3:
-            strides += (0, head_strides(name, t.unsqueeze(1), False)[1])
-        else:
-            strides += (0, _row_strides(name, t.unsqueeze(1), False)[1])
+    shift = A if bias is None else bias
+    if not (fits(_f32, index, (A, (hv,)), (shift, (hv,)), (state, table), (state_out, table)) and A.is_contiguous()
+            and shift.is_contiguous() and state.is_contiguous() and state_out.is_contiguous()):
+        check_dense("A", A, (hv,), _f32, index)
+        check_dense("bias", shift, (hv,), _f32, index)
+        check_dense("state", state, table, _f32, index)
+        check_dense("state_out", state_out, table, _f32, index)
+    if (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and a.is_contiguous() and b.is_contiguous()
+            and out.is_contiguous()):
+        strides = _dense
+    else:
+        strides = []
+        for name, t in (("q", q), ("k", k), ("v", v), ("a", a), ("b", b), ("y", out)):
+            if t.is_contiguous():
+                strides += (0, 0)
+            elif t.dim() == 3:
+                strides += (0, head_strides(name, t.unsqueeze(1), False)[1])
+            else:
+                strides += (0, _row_strides(name, t.unsqueeze(1), False)[1])
     args = _pack(batch, 1, hk, hv, dk, dv, code, 0, q.data_ptr(), k.data_ptr(), v.data_ptr(), a.data_ptr(), b.data_ptr(),
                  out.data_ptr(), A.data_ptr(), 0 if bias is None else bias.data_ptr(), state.data_ptr(),
                  state_out.data_ptr(), 0, dk ** -0.5 if scale is None else scale, beta_scale, *strides, 0, 0, 0)
