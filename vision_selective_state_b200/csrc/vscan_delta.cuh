@@ -1167,9 +1167,9 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_scan_kernel(const DeltaPa
                 mbar_wait(bar.done, par, &ws->dead);
                 tc_fence_after();
                 tc_ld32(tl + cKS + half * 32, x);
-                scale_row(u, vec + 2 * DL_C);
                 tc_wait_ld();
-                scale_add_row(x, vec + 6 * DL_C, u);  // X^T = beta (V - e^G K S)^T
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = vec[2 * DL_C + i] * (u[i] - vec[i] * x[i]);  // X^T = beta (V - e^G K S)^T
             }
             put_terms<3>(tl + cX + half * 48, 16, x);
             walk_ready(2);
