@@ -28,11 +28,11 @@
 // terms of each (2^-17 before a rounding of 2^-9). The state itself is float32
 // throughout, in registers, and is only ever added to with rounding.
 //
-// Measured on one B200 (medians of ten or more calls): 64 images of 4097 tokens, 6 heads of
-// 128 x 128, bf16: triangles 583 us, walk 813 us; 16 images of 56x56, 3 heads of 64 x 64:
-// 58 and 152 us; one float32 image of 197 tokens, 6 heads of 64 x 64: 13 and 23 us. The
-// backward pass of 16 images of 4097 tokens, 6 heads of 128 x 128: triangles 166 us, walk
-// 295 us, reverse walk 363 us, per-chunk gradients 841 us.
+// Measured on one B200 (one kernel at a time): 64 images of 4097 tokens, 6 heads of 128 x 128,
+// bf16: triangles 545 us, walk 768 us; 16 images of 56x56, 3 heads of 64 x 64: 52 and 150 us; one
+// float32 image of 197 tokens, 6 heads of 64 x 64: 13 and 23 us. The backward pass of 16 images of
+// 4097 tokens, 6 heads of 128 x 128: triangles 157 us, walk 281 us, reverse walk 336 us, per-chunk
+// gradients 828 us.
 #pragma once
 
 #include <cuda_bf16.h>

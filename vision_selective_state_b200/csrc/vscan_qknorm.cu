@@ -17,7 +17,11 @@ using vscan_host::fail;
 using vscan_host::launch_after;
 using vscan_host::NvtxRange;
 
-constexpr int kMaxBlocks = 148 * 4;  // of q and as many of k: eight CTAs of 256 threads an SM
+// CTAs of q and as many of k. Forward two rounds of the four CTAs of 256 threads that an SM holds,
+// backward one round (a CTA's sums for the weights' gradients are paid once): 64 images of 4097 tokens,
+// 6 + 6 heads of 128, bf16: 307 us (one round: 318); gradients of 16 images of 3136 tokens, heads of 72:
+// 141 us (two rounds: 163; three quarters of a round: 168).
+int most_blocks(bool back) { return 148 * (back ? 2 : 4); }
 
 vscan_status check_stride(const char* name, int64_t tok, int64_t img, int64_t width, int vec)
 {
@@ -80,28 +84,28 @@ int unit_width(const vscan_qknorm_args* a)
 // CTAs: one for each position and group of images. Images share a position's angles; they are
 // spread over groups until every CTA slot has several items (so that the last round costs
 // little), as long as an item keeps 32 rows of the smaller side.
-int groups_of(const vscan_qknorm_args* a)
+int groups_of(const vscan_qknorm_args* a, bool back)
 {
     if (a->pairs && a->pos_per_image) return std::max(a->batch, 1);
     const long long heads = std::min(a->heads_q, a->heads_k);
-    const long long want = (6LL * kMaxBlocks + a->tokens - 1) / std::max(a->tokens, 1);
-    const long long most = std::max(1LL, std::max(a->batch * heads / 32, (long long)kMaxBlocks / std::max(a->tokens, 1)));
+    const long long want = (6LL * most_blocks(back) + a->tokens - 1) / std::max(a->tokens, 1);
+    const long long most = std::max(1LL, std::max(a->batch * heads / 32, (long long)most_blocks(back) / std::max(a->tokens, 1)));
     return (int)std::max(1LL, std::min(std::min(want, most), (long long)a->batch));
 }
 
-int blocks_of(const vscan_qknorm_args* a)
+int blocks_of(const vscan_qknorm_args* a, bool back)
 {
-    return (int)std::min<long long>((long long)a->tokens * groups_of(a), kMaxBlocks);
+    return (int)std::min<long long>((long long)a->tokens * groups_of(a, back), most_blocks(back));
 }
 
-QkNormParams make_params(const vscan_qknorm_args* a, int v)
+QkNormParams make_params(const vscan_qknorm_args* a, int v, bool back)
 {
     QkNormParams p{};
     p.batch = a->batch; p.tokens = a->tokens;
     p.d = a->dim; p.pairs = a->pairs; p.axes = a->axes;
     p.rms = a->norm == VSCAN_NORM_RMS;
     p.pos_img = a->pos_per_image ? a->tokens * a->axes : 0;
-    p.groups = groups_of(a);
+    p.groups = groups_of(a, back);
     p.units = a->pairs / v + ((a->dim - 2 * a->pairs) / v + 1) / 2;
     p.lanes = 1;
     while (p.lanes < 32 && p.lanes < p.units) p.lanes *= 2;
@@ -118,7 +122,7 @@ QkNormParams make_params(const vscan_qknorm_args* a, int v)
     stride(a->k_tok_stride, a->k_batch_stride, a->heads_k, k.x_tok, k.x_img);
     stride(a->yq_tok_stride, a->yq_batch_stride, a->heads_q, q.y_tok, q.y_img);
     stride(a->yk_tok_stride, a->yk_batch_stride, a->heads_k, k.y_tok, k.y_img);
-    p.blocks = blocks_of(a);
+    p.blocks = blocks_of(a, back);
     return p;
 }
 
@@ -170,7 +174,7 @@ vscan_status vscan_qknorm_forward(const vscan_qknorm_args* args, void* stream)
         return fail(VSCAN_ERR_ALIGNMENT, "q, k, yq and yk must be 16-byte aligned");
     NvtxRange range("vscan_qknorm_forward");
     const int v = unit_width(args);
-    const cudaError_t e = launch<false>(args, make_params(args, v), v, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch<false>(args, make_params(args, v, false), v, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? VSCAN_OK : cuda_fail(e, "vscan_qknorm_forward");
 }
 
@@ -179,7 +183,7 @@ vscan_status vscan_qknorm_backward_workspace_size(const vscan_qknorm_args* args,
     if (!bytes) return fail(VSCAN_ERR_INVALID_ARGUMENT, "bytes is NULL");
     const vscan_status st = check_shape(args);
     if (st != VSCAN_OK) return st;
-    *bytes = empty(args) ? 0 : (uint64_t)blocks_of(args) * 2 * args->dim * 4;
+    *bytes = empty(args) ? 0 : (uint64_t)blocks_of(args, true) * 2 * args->dim * 4;
     return VSCAN_OK;
 }
 
@@ -205,7 +209,7 @@ vscan_status vscan_qknorm_backward(const vscan_qknorm_args* args, const vscan_qk
         !aligned16(grads->dq) || !aligned16(grads->dk))
         return fail(VSCAN_ERR_ALIGNMENT, "q, k, dyq, dyk, dq and dk must be 16-byte aligned");
     const int v = unit_width(args);
-    QkNormParams p = make_params(args, v);
+    QkNormParams p = make_params(args, v, true);
     const uint64_t need = (uint64_t)p.blocks * 2 * args->dim * 4;
     if (weights && (!grads->workspace || grads->workspace_bytes < need))
         return fail(VSCAN_ERR_WORKSPACE, "workspace of %llu bytes, %llu needed", (unsigned long long)grads->workspace_bytes,
