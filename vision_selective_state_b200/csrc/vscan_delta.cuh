@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(DP_THREADS, DeltaIo<T>::planes == 1 ? 4 : 3) d
     __syncthreads();  // K and Q are read: their place is the record's now
     {
         const int r0 = m0 + (lane >> 2), tc = (lane & 3) * 2;
-        float beta0, beta1;
+        const float beta0 = beta[r0], beta1 = beta[r0 + 8];
         // one pair of columns of one row, decayed: to P's planes, or to L
         auto put = [&](int i, int half, int nt, float v0, float v1) {
             const int j = nt * 8 + tc;
@@ -509,8 +509,6 @@ __global__ void __launch_bounds__(DP_THREADS, DeltaIo<T>::planes == 1 ? 4 : 3) d
                 Lt[prep_lt(j + 1) + i] = be * v1;
             }
         };
-        beta0 = beta[r0];
-        beta1 = beta[r0 + 8];
         const float f0 = onward[r0], f1 = onward[r0 + 8];
         float diag[2][4];  // the block on the diagonal, moved to fixed registers: its code is there once
 #pragma unroll

@@ -134,7 +134,8 @@ __device__ __forceinline__ void qn_shared(const float* s, float (&v)[V])
     }
 }
 
-// v *= s, or a row of factors; x = a c - b d and y = a d + b c with nb = -b: two values an instruction.
+// Two values an instruction, where there are two: v *= s; s += x y; a turn of pairs, x = a c + m d and
+// y = b c + n d with (m, n) = (-b, a), or back with (b, -a).
 template <int V>
 __device__ __forceinline__ void qn_scale(float (&v)[V], const float (&s)[V])
 {
@@ -150,22 +151,32 @@ __device__ __forceinline__ void qn_scale(float (&v)[V], const float (&s)[V])
     }
 }
 template <int V>
-__device__ __forceinline__ void qn_turn(float (&a)[V], float (&b)[V], const float (&nb)[V], const float (&c)[V], const float (&d)[V])
+__device__ __forceinline__ void qn_add(float (&s)[V], const float (&x)[V], const float (&y)[V])
 {
     if constexpr (V == 1) {
-        const float y = a[0] * c[0] + nb[0] * d[0];
-        b[0] = a[0] * d[0] + b[0] * c[0];
-        a[0] = y;
+        s[0] += x[0] * y[0];
     } else {
 #pragma unroll
         for (int e = 0; e < V; e += 2) {
-            const float2 a2 = make_float2(a[e], a[e + 1]), b2 = make_float2(b[e], b[e + 1]), n2 = make_float2(nb[e], nb[e + 1]);
-            const float2 c2 = make_float2(c[e], c[e + 1]), d2 = make_float2(d[e], d[e + 1]);
-            const float2 x = __ffma2_rn(n2, d2, __fmul2_rn(a2, c2)), y = __ffma2_rn(a2, d2, __fmul2_rn(b2, c2));
-            a[e] = x.x; a[e + 1] = x.y;
-            b[e] = y.x; b[e + 1] = y.y;
+            const float2 z = __ffma2_rn(make_float2(x[e], x[e + 1]), make_float2(y[e], y[e + 1]), make_float2(s[e], s[e + 1]));
+            s[e] = z.x;
+            s[e + 1] = z.y;
         }
     }
+}
+template <bool BACK, int V>
+__device__ __forceinline__ void qn_turn(float (&a)[V], float (&b)[V], const float (&c)[V], const float (&d)[V])
+{
+    float m[V], n[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        m[e] = BACK ? b[e] : -b[e];
+        n[e] = BACK ? -a[e] : a[e];
+    }
+    qn_scale(a, c);
+    qn_scale(b, c);
+    qn_add(a, m, d);
+    qn_add(b, n, d);
 }
 
 // Cosine and sine of every pair's angle at one position, by the whole CTA.
@@ -269,11 +280,15 @@ __global__ void __launch_bounds__(QN_THREADS, BACK ? 3 : 4) qk_norm_kernel(const
             }
 #pragma unroll
             for (int k = 0; k < R; ++k) {
-                float sq = 0.f;
+                float squares[2] = {};
 #pragma unroll
                 for (int u = 0; u < U; ++u)
 #pragma unroll
-                    for (int e = 0; e < 2 * V; ++e) sq += x[k][u][e] * x[k][u][e];
+                    for (int e = 0; e < 2 * V; e += 2) {
+                        const float x2[2] = {x[k][u][e], x[k][u][e + 1]};
+                        qn_add(squares, x2, x2);
+                    }
+                float sq = squares[0] + squares[1];
                 for (int o = p.lanes >> 1; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
                 const float square = (p.rms ? sq / p.d : sq) + p.eps;
                 float r = rsqrtf(square);  // good to 2 units of the last place: enough for what leaves in bf16
@@ -283,7 +298,7 @@ __global__ void __launch_bounds__(QN_THREADS, BACK ? 3 : 4) qk_norm_kernel(const
                     T* dst = reinterpret_cast<T*>(side.y) + yat[k];
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
-                        float a[V], b[V], nb[V], c[V], d[V];
+                        float a[V], b[V], c[V], d[V];
 #pragma unroll
                         for (int e = 0; e < V; ++e) {
                             a[e] = x[k][u][e];
@@ -301,9 +316,7 @@ __global__ void __launch_bounds__(QN_THREADS, BACK ? 3 : 4) qk_norm_kernel(const
                         if (lo[u] >= 0 && lo[u] < p.pairs) {  // turned
                             qn_shared<V>(cosine + lo[u], c);
                             qn_shared<V>(sine + lo[u], d);
-#pragma unroll
-                            for (int e = 0; e < V; ++e) nb[e] = -b[e];
-                            qn_turn(a, b, nb, c, d);
+                            qn_turn<false>(a, b, c, d);
                         }
                         if (live[k] && lo[u] >= 0) qn_store<T, V>(dst + lo[u], a);
                         if (live[k] && hi[u] >= 0) qn_store<T, V>(dst + hi[u], b);
@@ -321,33 +334,32 @@ __global__ void __launch_bounds__(QN_THREADS, BACK ? 3 : 4) qk_norm_kernel(const
                         if (lo[u] >= 0 && lo[u] < p.pairs) {  // turned back
                             qn_shared<V>(cosine + lo[u], c);
                             qn_shared<V>(sine + lo[u], d);
-#pragma unroll
-                            for (int e = 0; e < V; ++e) {
-                                const float y = a[e] * c[e] + b[e] * d[e];
-                                b[e] = b[e] * c[e] - a[e] * d[e];
-                                a[e] = y;
-                            }
+                            qn_turn<true>(a, b, c, d);
                         }
+                        float dn[2 * V], n[2 * V];
 #pragma unroll
-                        for (int e = 0; e < V; ++e) {
-                            acc[u][e] += a[e] * (x[k][u][e] * r);
-                            acc[u][V + e] += b[e] * (x[k][u][V + e] * r);
+                        for (int e = 0; e < 2 * V; ++e) {
+                            dn[e] = e < V ? a[e] : b[e - V];
+                            n[e] = r;
                         }
+                        qn_scale(n, x[k][u]);
+                        qn_add(acc[u], dn, n);
                         if (weighted) {
                             qn_shared<V>(weight + max(lo[u], 0), c);
                             qn_shared<V>(weight + max(hi[u], 0), d);
 #pragma unroll
-                            for (int e = 0; e < V; ++e) {
-                                a[e] *= c[e];
-                                b[e] *= d[e];
-                            }
+                            for (int e = 0; e < 2 * V; ++e) n[e] = e < V ? c[e] : d[e - V];
+                            qn_scale(dn, n);
                         }
+                        float part[2] = {};
 #pragma unroll
-                        for (int e = 0; e < V; ++e) {
-                            inner += a[e] * x[k][u][e] + b[e] * x[k][u][V + e];
-                            dy[k][u][e] = a[e];
-                            dy[k][u][V + e] = b[e];
+                        for (int e = 0; e < 2 * V; e += 2) {
+                            const float u2[2] = {dn[e], dn[e + 1]}, x2[2] = {x[k][u][e], x[k][u][e + 1]};
+                            qn_add(part, u2, x2);
                         }
+                        inner += part[0] + part[1];
+#pragma unroll
+                        for (int e = 0; e < 2 * V; ++e) dy[k][u][e] = dn[e];
                     }
                     for (int o = p.lanes >> 1; o > 0; o >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, o);
                     const float f = (p.rms ? inner / p.d : inner) * r * r;
@@ -355,11 +367,20 @@ __global__ void __launch_bounds__(QN_THREADS, BACK ? 3 : 4) qk_norm_kernel(const
                         T* dst = reinterpret_cast<T*>(side.y) + dense[k];
 #pragma unroll
                         for (int u = 0; u < U; ++u) {
-                            float a[V], b[V];
+                            float out[2 * V], s[2 * V], a[V], b[V];
+#pragma unroll
+                            for (int e = 0; e < 2 * V; ++e) {
+                                out[e] = dy[k][u][e];
+                                s[e] = -f;
+                            }
+                            qn_add(out, x[k][u], s);
+#pragma unroll
+                            for (int e = 0; e < 2 * V; ++e) s[e] = r;
+                            qn_scale(out, s);
 #pragma unroll
                             for (int e = 0; e < V; ++e) {
-                                a[e] = r * (dy[k][u][e] - x[k][u][e] * f);
-                                b[e] = r * (dy[k][u][V + e] - x[k][u][V + e] * f);
+                                a[e] = out[e];
+                                b[e] = out[V + e];
                             }
                             if (live[k] && lo[u] >= 0) qn_store<T, V>(dst + lo[u], a);
                             if (live[k] && hi[u] >= 0) qn_store<T, V>(dst + hi[u], b);
