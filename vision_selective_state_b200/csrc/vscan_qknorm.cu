@@ -19,8 +19,8 @@ using vscan_host::NvtxRange;
 
 // CTAs of q and as many of k. Forward two rounds of the four CTAs of 256 threads that an SM holds,
 // backward one round (a CTA's sums for the weights' gradients are paid once): 64 images of 4097 tokens,
-// 6 + 6 heads of 128, bf16: 307 us (one round: 318); gradients of 16 images of 3136 tokens, heads of 72:
-// 141 us (two rounds: 163; three quarters of a round: 168).
+// 6 + 6 heads of 128, bf16: 306 us (one round: 318); gradients of 16 images of 3136 tokens, heads of 72:
+// 135 us (262 CTAs a side: 154; 370: 147; 740: 155).
 int most_blocks(bool back) { return 148 * (back ? 2 : 4); }
 
 vscan_status check_stride(const char* name, int64_t tok, int64_t img, int64_t width, int vec)
