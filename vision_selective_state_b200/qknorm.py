@@ -17,10 +17,9 @@ import torch
 
 from . import _abi
 from ._abi import VscanQkNormGrads, check
-from .delta import check_dense, check_tensor, device_index, fits, fresh, head_strides, on_device, stream_handle
+from .delta import check_dense, check_tensor, device_index, fresh, head_strides, on_device, stream_handle
 
 NORMS = {"l2": 0, "rms": 1}
-_dense = (0,) * 8  # strides of four dense tensors
 
 
 def _marshal(q, k, wq, wk, yq, yk, norm, eps, inv_freq, positions):
@@ -33,10 +32,9 @@ def _marshal(q, k, wq, wk, yq, yk, norm, eps, inv_freq, positions):
     dtype = q.dtype
     batch, tokens, hq, d = q.shape
     hk = k.shape[2]
-    if not fits(dtype, index, (k, (batch, tokens, hk, d)), (yq, q.shape), (yk, k.shape)):
-        check_tensor("k", k, (batch, tokens, hk, d), dtype, index)
-        check_tensor("yq (dyq)", yq, q.shape, dtype, index)
-        check_tensor("yk (dyk)", yk, k.shape, dtype, index)
+    check_tensor("k", k, (batch, tokens, hk, d), dtype, index)
+    check_tensor("yq (dyq)", yq, q.shape, dtype, index)
+    check_tensor("yk (dyk)", yk, k.shape, dtype, index)
     if wq is not None:
         check_dense("wq", wq, (d,), torch.float32, index)
     if wk is not None:
@@ -48,25 +46,20 @@ def _marshal(q, k, wq, wk, yq, yk, norm, eps, inv_freq, positions):
         pairs = inv_freq.numel()
         check_dense("inv_freq", inv_freq, (pairs,), torch.float32, index)
         shape = positions.shape
-        for per_image, lead in enumerate(((tokens,), (batch, tokens))):
-            if shape == lead:
-                break
-            if shape[:-1] == lead and shape[-1] in (1, 2):
-                axes = shape[-1]
+        for lead in ((tokens,), (batch, tokens)):
+            if shape == lead or (shape[:-1] == lead and shape[-1] in (1, 2)):
+                axes, per_image = (1 if shape == lead else shape[-1]), len(lead) - 1
                 break
         else:
             raise ValueError(f"positions shape {tuple(shape)} is not [tokens(, axes)] or [batch, tokens(, axes)]")
         check_dense("positions", positions, shape, torch.int32, index)
-    if q.is_contiguous() and k.is_contiguous() and yq.is_contiguous() and yk.is_contiguous():
-        strides = _dense
-    else:
-        strides = (*head_strides("q", q, q.is_contiguous()), *head_strides("k", k, k.is_contiguous()),
-                   *head_strides("yq", yq, yq.is_contiguous()), *head_strides("yk", yk, yk.is_contiguous()))
     return index, _abi.qknorm_forward.pack(
         batch, tokens, hq, hk, d, pairs, axes, code, NORMS[norm], eps,
         q.data_ptr(), k.data_ptr(), yq.data_ptr(), yk.data_ptr(), 0 if wq is None else wq.data_ptr(),
         0 if wk is None else wk.data_ptr(), inv_freq.data_ptr() if pairs else 0, positions.data_ptr() if pairs else 0,
-        per_image, 0, *strides)
+        per_image, 0,
+        *head_strides("q", q, q.is_contiguous()), *head_strides("k", k, k.is_contiguous()),
+        *head_strides("yq", yq, yq.is_contiguous()), *head_strides("yk", yk, yk.is_contiguous()))
 
 
 def qk_norm(q, k, wq=None, wk=None, *, norm="rms", eps=1e-6, inv_freq=None, positions=None, out=None, stream=None):
