@@ -283,7 +283,7 @@ struct GradShape {
     static constexpr int oX = oW + 3 * TC_TILE;   // three pairs of tiles: dO's and dV's terms; later E's and M's
     static constexpr int oEnd = oX + 6 * TC_TILE;
     static constexpr int oSums = oW + 2 * TC_TILE;  // GradSums, once W is read
-    static constexpr int front = 3072;  // GradShared
+    static constexpr int front = 4096;  // GradShared
     static constexpr size_t smem = 1024 + front + oEnd;
 };
 
@@ -301,7 +301,7 @@ struct GradSums {
     double hcol[4][DL_C];          // column sums, by quarters of the 128 rows of D2
     float U[4][DL_C], V[4][DL_C];  // by quarters of the key channels
 };
-static_assert(sizeof(GradShared) <= 3072, "shared memory in front of the tiles");
+static_assert(sizeof(GradShared) <= 4096, "shared memory in front of the tiles");
 static_assert(sizeof(GradSums) <= TC_TILE, "in the place of W's third plane");
 
 // Sum over the warp of each of 32 values; lane l gets the l-th.
