@@ -927,14 +927,16 @@ struct WalkBars {
     }
 };
 
-// Tensor memory and barriers of a walk; all threads.
-__device__ __forceinline__ uint32_t walk_begin(WalkShared* w, const WalkBars& bar)
+// Tensor memory and barriers of a walk; all threads. A stage is free again after `releases` arrivals:
+// the computing threads', who have then waited for every product of theirs that reads it, and one more
+// where the issuing warp waits for a product that they do not wait for.
+__device__ __forceinline__ uint32_t walk_begin(WalkShared* w, const WalkBars& bar, int releases)
 {
     if (threadIdx.x < 32) tc_alloc(static_cast<uint32_t>(__cvta_generic_to_shared(&w->tmem)));
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar.full + 8 * i, DW_HELP);  // the copying threads, each with the bytes of its bulk copies
-            mbar_init(bar.empty + 8 * i, DW_COMPUTE);
+            mbar_init(bar.empty + 8 * i, releases);
         }
         for (int i = 0; i < 5; ++i) mbar_init(bar.done + 8 * i, 1);
         w->dead = 0;
@@ -1004,7 +1006,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_scan_kernel(const DeltaPa
     const int chunks = (s.len + DL_C - 1) / DL_C;
     const size_t sbase = ((size_t)b * p.heads_v + head) * p.dk * p.dv;
     const WalkBars bar(ws);
-    const uint32_t tm = walk_begin(ws, bar);
+    const uint32_t tm = walk_begin(ws, bar, DW_COMPUTE + (SAVE ? 0 : 1));
     wait_previous();
 
     if (warp >= 8) {
@@ -1071,8 +1073,10 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_scan_kernel(const DeltaPa
                         tc_commit(bar.done + 32);
                     }
                     __syncwarp();
-                    // the next KS lies over W's terms: O has read them
+                    // O has read W's terms, over which the next KS lies, and P, over which the stage's next record
+                    // comes; the computing threads, which wait for O a chunk later, have not seen that
                     mbar_wait(bar.done + 32, par, &ws->dead);
+                    if (lane == 0) mbar_arrive(bar.empty + 8 * st);
                 }
             }
         } else {

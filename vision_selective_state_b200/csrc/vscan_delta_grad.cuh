@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaP
     const int chunks = (s.len + DL_C - 1) / DL_C;
     const size_t sbase = ((size_t)b * p.heads_v + head) * p.dk * p.dv;
     const WalkBars bar(ws);
-    const uint32_t tm = walk_begin(ws, bar);
+    const uint32_t tm = walk_begin(ws, bar, DW_COMPUTE);  // they wait for the last product
     wait_previous();
     // n counts the chunks in the order of the walk, from the last to the first
 
