@@ -606,7 +606,8 @@ typedef struct vscan_qknorm_args {
 /*
  * Normalise and rotate. One launch, enqueued on stream; no workspace; never
  * synchronizes. Errors: INVALID_ARGUMENT, SHAPE (pairs or axes that do not fit),
- * ALIGNMENT, UNSUPPORTED (dim above 256), CUDA.
+ * ALIGNMENT, UNSUPPORTED (dim above 256, batch x (heads_q + heads_k) or tokens x axes
+ * near 2^31), CUDA.
  */
 vscan_status vscan_qknorm_forward(const vscan_qknorm_args* args, void* stream);
 

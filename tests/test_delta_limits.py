@@ -1,0 +1,23 @@
+"""Sizes at the ends of 32-bit counters are refused on the host: no GPU needed, no kernel launched."""
+import ctypes
+
+import pytest
+
+abi = pytest.importorskip("vision_selective_state_b200._abi")
+
+INVALID, UNSUPPORTED = -1, -4
+
+
+@pytest.mark.parametrize("batch,heads_q,heads_k,ok", [
+    (1, 2 ** 31 - 2, 1, False), (1, 1, 2 ** 31 - 2, False), (2 ** 30 - 1, 1, 1, False), (1, 2 ** 31 - 1025, 1, False),
+    (1, 2 ** 31 - 1026, 1, True), (2 ** 30 - 513, 1, 1, True), (65536, 32768, 32767, False),
+])
+def test_rows_that_a_lane_counts_past_2_31(batch, heads_q, heads_k, ok):
+    """A lane of the norm steps through images x heads rows, up to 512 behind the last."""
+    a = abi.VscanQkNormArgs()
+    a.batch, a.tokens, a.heads_q, a.heads_k, a.dim, a.axes, a.dtype, a.eps = batch, 1, heads_q, heads_k, 4, 1, abi.F32, 1e-6
+    n, g = ctypes.c_uint64(), abi.VscanQkNormGrads()
+    assert abi.lib.vscan_qknorm_backward_workspace_size(ctypes.byref(a), ctypes.byref(n)) == (0 if ok else UNSUPPORTED)
+    # without pointers: refused for its size, or for the pointers that it lacks
+    assert abi.lib.vscan_qknorm_forward(ctypes.byref(a), None) == (INVALID if ok else UNSUPPORTED)
+    assert abi.lib.vscan_qknorm_backward(ctypes.byref(a), ctypes.byref(g), None) == (INVALID if ok else UNSUPPORTED)

@@ -47,8 +47,9 @@ vscan_status check_shape(const vscan_qknorm_args* a)
     if (a->dim % vec != 0)
         return fail(VSCAN_ERR_ALIGNMENT, "dim %d is not a multiple of %d (16-byte rows)", a->dim, vec);
     if (a->dim > 2 * vscan::QN_MAX_PAIRS) return fail(VSCAN_ERR_UNSUPPORTED, "dim %d > %d", a->dim, 2 * vscan::QN_MAX_PAIRS);
-    if ((int64_t)a->batch * ((int64_t)a->heads_q + a->heads_k) > 0x7fffffffLL)
-        return fail(VSCAN_ERR_UNSUPPORTED, "batch x heads must be below 2^31");
+    // rows of a position, which a lane counts in steps of at most 512, in 32 bits
+    if ((int64_t)a->batch * ((int64_t)a->heads_q + a->heads_k) > 0x7fffffffLL - 1024)
+        return fail(VSCAN_ERR_UNSUPPORTED, "batch x (heads_q + heads_k) must be below 2^31 - 1024");
     if (!(a->eps >= 0.f) || !std::isfinite(a->eps)) return fail(VSCAN_ERR_INVALID_ARGUMENT, "eps must be finite and >= 0");
     if (a->reserved != 0) return fail(VSCAN_ERR_INVALID_ARGUMENT, "args.reserved must be 0");
     if (a->pos_per_image != 0 && a->pos_per_image != 1)

@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(QN_THREADS, BACK ? 3 : 4) qk_norm_kernel(const
     }
     const long long work = (long long)p.tokens * p.groups;
     // a lane's rows are R * row_slots apart: so many images and heads
-    const int hop = R * row_slots, hop_at = hop / side.heads, hop_head = hop - hop_at * side.heads;
+    const int hop = R * row_slots /* <= 512 */, hop_at = hop / side.heads, hop_head = hop - hop_at * side.heads;
     for (long long item = blockIdx.x; item < work; item += gridDim.x) {
         const int token = (int)(item / p.groups), group = (int)(item - (long long)token * p.groups);
         __syncthreads();
