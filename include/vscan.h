@@ -496,8 +496,8 @@ vscan_status vscan_delta_workspace_size(const vscan_route* route, const vscan_de
  * calls need workspaces of their own.
  * Errors: INVALID_ARGUMENT, SHAPE (heads or direction that do not fit, a token
  * count that is not the route's), ALIGNMENT, UNSUPPORTED (pooled routes, head
- * widths above the limits, heads_v or batch above 65535, seq_offsets with a
- * route), WORKSPACE, CUDA.
+ * widths above the limits, heads_v or batch above 65535, tokens above 2^31 - 64,
+ * seq_offsets with a route), WORKSPACE, CUDA.
  */
 vscan_status vscan_delta_forward(const vscan_route* route, const vscan_delta_args* args, void* stream);
 

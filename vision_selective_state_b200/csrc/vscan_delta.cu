@@ -67,6 +67,8 @@ vscan_status check_shape(const vscan_route* r, const vscan_delta_args* a)
         return fail(VSCAN_ERR_ALIGNMENT, "dim_k %d and dim_v %d must be multiples of %d (16-byte rows)", a->dim_k, a->dim_v, vec);
     if (a->dim_k > kMaxDimK || a->dim_v > kMaxDimV)
         return fail(VSCAN_ERR_UNSUPPORTED, "dim_k %d > %d or dim_v %d > %d", a->dim_k, kMaxDimK, a->dim_v, kMaxDimV);
+    if (a->tokens > 0x7fffffff - (DL_C - 1))  // rounded up to chunks in 32 bits
+        return fail(VSCAN_ERR_UNSUPPORTED, "tokens %d > 2^31 - %d", a->tokens, DL_C);
     if (a->batch > kMaxGrid || a->heads_v > kMaxGrid)
         return fail(VSCAN_ERR_UNSUPPORTED, "batch %d or heads_v %d > %d", a->batch, a->heads_v, kMaxGrid);
     if (!std::isfinite(a->scale) || !std::isfinite(a->beta_scale))
