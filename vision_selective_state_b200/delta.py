@@ -16,6 +16,10 @@ q, k, v, a, b and y share one dtype: torch.float32 or torch.bfloat16. Token and 
 are free (slices of a wider projection output) but not 0 (an expanded axis is refused); the
 heads of one token are contiguous. As in
 the rest of the package, the binding only marshals tensors; the arithmetic runs in libvscan.so.
+
+A call runs on `stream`, or on the current one: its kernels, what it allocates and the rows that it
+clears. It waits for no other stream: with `stream` given, the caller orders it behind the work that
+makes its inputs, and what reads its results behind it.
 """
 import contextlib
 import ctypes
@@ -32,24 +36,26 @@ _dense = (0,) * 12  # strides of six dense tensors
 _pack = _abi.delta_forward.pack
 
 
-def on_device(index):
-    """Context in which the runtime's current device is the tensors' own."""
-    return _here if torch._C._cuda_getDevice() == index else torch.cuda.device(index)
-
-
-def stream_handle(stream, index, *scratch):
-    """The launch stream's handle. Tensors made here for a call on a stream other than the
-    current one are marked as used there, so that their memory is not handed out again early."""
-    current = torch._C._cuda_getCurrentRawStream(index)
+def launching(stream, index):
+    """Context of a call on the tensors' device and on `stream`, the current one if None. What a call
+    allocates and clears belongs to the stream that its kernels run on: memory of the current one may
+    still be read there, and a fill there comes at any time."""
     if stream is None:
-        return current
+        return _here if torch._C._cuda_getDevice() == index else torch.cuda.device(index)
     if stream.device.index != index:
         raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{index}")
-    if stream.cuda_stream != current:
-        for t in scratch:
+    return torch.cuda.stream(stream)
+
+
+def hand_over(stream, index, *tensors):
+    """A call's tensors are used on its stream and on the caller's: their memory is not handed out
+    again before both have passed the point where the last reference is dropped."""
+    here = torch.cuda.current_stream(index)
+    if here.cuda_stream != stream.cuda_stream:
+        for t in tensors:
             if t is not None:
                 t.record_stream(stream)
-    return stream.cuda_stream
+                t.record_stream(here)
 
 
 def check_tensor(name, t, shape, dtype, index):
@@ -122,9 +128,8 @@ def _row_strides(name, t, dense):
     return tok, (t.stride(0) if b > 1 else n * tok)
 
 
-def _fields(q, k, v, a, b, A, bias, y, direction, seq_offsets, scale, beta_scale, initial_state, final_state):
-    """(device index, fields of vscan_delta_args up to the strides)."""
-    index, code = device_index(q)
+def _fields(index, code, q, k, v, a, b, A, bias, y, direction, seq_offsets, scale, beta_scale, initial_state, final_state):
+    """Fields of vscan_delta_args up to the strides."""
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q and k are [batch, tokens, heads_k, dim_k], v is [batch, tokens, heads_v, dim_v]")
     dtype, shape = q.dtype, q.shape
@@ -151,7 +156,7 @@ def _fields(q, k, v, a, b, A, bias, y, direction, seq_offsets, scale, beta_scale
         check_dense("initial_state", initial_state, (rows, hv, dk, dv), torch.float32, index)
     if final_state is not None:
         check_dense("final_state", final_state, (rows, hv, dk, dv), torch.float32, index)
-    return index, (
+    return (
         rows, tokens, hk, hv, dk, dv, code, direction,
         q.data_ptr(), k.data_ptr(), v.data_ptr(), a.data_ptr(), b.data_ptr(), y.data_ptr(), A.data_ptr(),
         0 if bias is None else bias.data_ptr(), 0 if initial_state is None else initial_state.data_ptr(),
@@ -212,19 +217,22 @@ def delta_forward(q, k, v, a, b, A, bias=None, *, route=None, direction=0, seq_o
     tensor to write the state after the last token to (initial_state itself is allowed).
     status: as in forward().
     """
-    if out is None:
-        out = v.new_zeros(v.shape) if _partial(route, seq_offsets) else fresh(v)
-    if final_state is True:
-        final_state = q.new_empty(_state_shape(q, v, seq_offsets), dtype=torch.float32)
-    elif final_state is False:
-        final_state = None
-    index, fields = _fields(q, k, v, a, b, A, bias, out, direction, seq_offsets, scale, beta_scale, initial_state,
-                            final_state)
-    handle = _route_handle(route)
-    workspace, *scratch = _scratch(workspace, _abi.delta_workspace_size, handle, fields, q, index)
-    args = _pack(*fields, *scratch, _status(status, index))
-    with on_device(index):
-        check(_abi.delta_forward.fn(handle, args, stream_handle(stream, index, out, final_state, workspace)))
+    index, code = device_index(q)
+    with launching(stream, index):
+        if out is None:
+            out = v.new_zeros(v.shape) if _partial(route, seq_offsets) else fresh(v)
+        if final_state is True:
+            final_state = q.new_empty(_state_shape(q, v, seq_offsets), dtype=torch.float32)
+        elif final_state is False:
+            final_state = None
+        fields = _fields(index, code, q, k, v, a, b, A, bias, out, direction, seq_offsets, scale, beta_scale, initial_state,
+                         final_state)
+        handle = _route_handle(route)
+        scratch, *where = _scratch(workspace, _abi.delta_workspace_size, handle, fields, q, index)
+        args = _pack(*fields, *where, _status(status, index))
+        check(_abi.delta_forward.fn(handle, args, torch._C._cuda_getCurrentRawStream(index)))
+    if stream is not None:
+        hand_over(stream, index, out, final_state, workspace)
     return out if final_state is None else (out, final_state)
 
 
@@ -241,26 +249,30 @@ def delta_backward(q, k, v, a, b, A, bias=None, *, dy, route=None, direction=0, 
     d_initial_state (float32). `want` limits the keys computed. Tokens that no step visits get
     zeros. Equal calls give equal bits.
     """
-    index, fields = _fields(q, k, v, a, b, A, bias, dy, direction, seq_offsets, scale, beta_scale, initial_state, None)
     if want is not None and not set(want) <= set(GRADIENTS):
         raise ValueError(f"want holds unknown gradients {sorted(set(want) - set(GRADIENTS))}")
-    grads, out = VscanDeltaGrads(), {}
-    like = {"dq": q, "dk": k, "dv": v, "da": a, "db": b, "dA": A, "dbias": A, "d_initial_state": initial_state}
-    for name in GRADIENTS if want is None else want:
-        t = like[name]
-        if t is not None:
-            out[name] = fresh(t)
-            setattr(grads, name, out[name].data_ptr())
-    if d_final_state is not None:
-        check_dense("d_final_state", d_final_state, _state_shape(q, v, seq_offsets), torch.float32, index)
-        grads.d_final_state = d_final_state.data_ptr()
-    handle = _route_handle(route)
-    workspace, grads.workspace, grads.workspace_bytes = _scratch(workspace, _abi.delta_backward_workspace_size, handle,
-                                                                 fields, q, index)
-    args = _pack(*fields, 0, 0, _status(status, index))
-    with on_device(index):
+    index, code = device_index(q)
+    with launching(stream, index):
+        fields = _fields(index, code, q, k, v, a, b, A, bias, dy, direction, seq_offsets, scale, beta_scale, initial_state,
+                         None)
+        grads, out = VscanDeltaGrads(), {}
+        like = {"dq": q, "dk": k, "dv": v, "da": a, "db": b, "dA": A, "dbias": A, "d_initial_state": initial_state}
+        for name in GRADIENTS if want is None else want:
+            t = like[name]
+            if t is not None:
+                out[name] = fresh(t)
+                setattr(grads, name, out[name].data_ptr())
+        if d_final_state is not None:
+            check_dense("d_final_state", d_final_state, _state_shape(q, v, seq_offsets), torch.float32, index)
+            grads.d_final_state = d_final_state.data_ptr()
+        handle = _route_handle(route)
+        scratch, grads.workspace, grads.workspace_bytes = _scratch(workspace, _abi.delta_backward_workspace_size, handle,
+                                                                   fields, q, index)
+        args = _pack(*fields, 0, 0, _status(status, index))
         check(_abi.delta_backward.fn(handle, args, dy.data_ptr(), ctypes.byref(grads),
-                                     stream_handle(stream, index, workspace, *out.values())))
+                                     torch._C._cuda_getCurrentRawStream(index)))
+    if stream is not None:
+        hand_over(stream, index, workspace, *out.values())
     return out
 
 
@@ -283,9 +295,7 @@ def delta_step(q, k, v, a, b, A, bias=None, *, state, state_out=None, scale=None
         check_tensor("v", v, (batch, hv, dv), dtype, index)
         check_tensor("a", a, heads, dtype, index)
         check_tensor("b", b, heads, dtype, index)
-    if out is None:
-        out = fresh(v)
-    else:
+    if out is not None:
         check_tensor("y", out, wide, dtype, index)
     if state_out is None:
         state_out = state
@@ -296,21 +306,25 @@ def delta_step(q, k, v, a, b, A, bias=None, *, state, state_out=None, scale=None
         check_dense("bias", shift, (hv,), _f32, index)
         check_dense("state", state, table, _f32, index)
         check_dense("state_out", state_out, table, _f32, index)
-    if (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and a.is_contiguous() and b.is_contiguous()
-            and out.is_contiguous()):
-        strides = _dense
-    else:
-        strides = []
-        for name, t in (("q", q), ("k", k), ("v", v), ("a", a), ("b", b), ("y", out)):
-            if t.is_contiguous():
-                strides += (0, 0)
-            elif t.dim() == 3:
-                strides += (0, head_strides(name, t.unsqueeze(1), False)[1])
-            else:
-                strides += (0, _row_strides(name, t.unsqueeze(1), False)[1])
-    args = _pack(batch, 1, hk, hv, dk, dv, code, 0, q.data_ptr(), k.data_ptr(), v.data_ptr(), a.data_ptr(), b.data_ptr(),
-                 out.data_ptr(), A.data_ptr(), 0 if bias is None else bias.data_ptr(), state.data_ptr(),
-                 state_out.data_ptr(), 0, dk ** -0.5 if scale is None else scale, beta_scale, *strides, 0, 0, 0)
-    with on_device(index):
-        check(_abi.delta_step.fn(args, stream_handle(stream, index, out)))
+    with launching(stream, index):
+        if out is None:
+            out = fresh(v)
+        if (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and a.is_contiguous() and b.is_contiguous()
+                and out.is_contiguous()):
+            strides = _dense
+        else:
+            strides = []
+            for name, t in (("q", q), ("k", k), ("v", v), ("a", a), ("b", b), ("y", out)):
+                if t.is_contiguous():
+                    strides += (0, 0)
+                elif t.dim() == 3:
+                    strides += (0, head_strides(name, t.unsqueeze(1), False)[1])
+                else:
+                    strides += (0, _row_strides(name, t.unsqueeze(1), False)[1])
+        args = _pack(batch, 1, hk, hv, dk, dv, code, 0, q.data_ptr(), k.data_ptr(), v.data_ptr(), a.data_ptr(), b.data_ptr(),
+                     out.data_ptr(), A.data_ptr(), 0 if bias is None else bias.data_ptr(), state.data_ptr(),
+                     state_out.data_ptr(), 0, dk ** -0.5 if scale is None else scale, beta_scale, *strides, 0, 0, 0)
+        check(_abi.delta_step.fn(args, torch._C._cuda_getCurrentRawStream(index)))
+    if stream is not None:
+        hand_over(stream, index, out, state_out)
     return out, state_out

@@ -10,6 +10,9 @@ vscan_qknorm_* entry points.
                (a shape that fits two of them is read as the first);
                with two axes (grid row, grid column) the first half of the pairs turns by the
                first, the second half by the second
+
+stream is as in the delta rule's calls: the call runs, allocates and clears there, and waits for no
+other stream.
 """
 import ctypes
 
@@ -17,14 +20,13 @@ import torch
 
 from . import _abi
 from ._abi import VscanQkNormGrads, check
-from .delta import check_dense, check_tensor, device_index, fresh, head_strides, on_device, stream_handle
+from .delta import check_dense, check_tensor, device_index, fresh, hand_over, head_strides, launching
 
 NORMS = {"l2": 0, "rms": 1}
 
 
-def _marshal(q, k, wq, wk, yq, yk, norm, eps, inv_freq, positions):
-    """(device index, packed vscan_qknorm_args)."""
-    index, code = device_index(q)
+def _marshal(index, code, q, k, wq, wk, yq, yk, norm, eps, inv_freq, positions):
+    """Packed vscan_qknorm_args."""
     if norm not in NORMS:
         raise ValueError(f"norm must be one of {sorted(NORMS)}")
     if q.dim() != 4 or k.dim() != 4:
@@ -53,7 +55,7 @@ def _marshal(q, k, wq, wk, yq, yk, norm, eps, inv_freq, positions):
         else:
             raise ValueError(f"positions shape {tuple(shape)} is not [tokens(, axes)] or [batch, tokens(, axes)]")
         check_dense("positions", positions, shape, torch.int32, index)
-    return index, _abi.qknorm_forward.pack(
+    return _abi.qknorm_forward.pack(
         batch, tokens, hq, hk, d, pairs, axes, code, NORMS[norm], eps,
         q.data_ptr(), k.data_ptr(), yq.data_ptr(), yk.data_ptr(), 0 if wq is None else wq.data_ptr(),
         0 if wk is None else wk.data_ptr(), inv_freq.data_ptr() if pairs else 0, positions.data_ptr() if pairs else 0,
@@ -65,11 +67,14 @@ def _marshal(q, k, wq, wk, yq, yk, norm, eps, inv_freq, positions):
 def qk_norm(q, k, wq=None, wk=None, *, norm="rms", eps=1e-6, inv_freq=None, positions=None, out=None, stream=None):
     """Normalised ("l2": unit length, "rms": unit mean square), weighted and rotated (yq, yk)
     (vscan_qknorm_forward). out: a pair of tensors to write to; (q, k) itself works in place."""
-    if out is None:
-        out = (fresh(q), fresh(k))
-    index, args = _marshal(q, k, wq, wk, *out, norm, eps, inv_freq, positions)
-    with on_device(index):
-        check(_abi.qknorm_forward.fn(args, stream_handle(stream, index, *out)))
+    index, code = device_index(q)
+    with launching(stream, index):
+        if out is None:
+            out = (fresh(q), fresh(k))
+        args = _marshal(index, code, q, k, wq, wk, *out, norm, eps, inv_freq, positions)
+        check(_abi.qknorm_forward.fn(args, torch._C._cuda_getCurrentRawStream(index)))
+    if stream is not None:
+        hand_over(stream, index, *out)
     return tuple(out)
 
 
@@ -79,23 +84,25 @@ def qk_norm_backward(q, k, wq=None, wk=None, *, dyq, dyk, norm="rms", eps=1e-6, 
     q) and, where there is a weight, dwq and dwk (float32, summed over the tokens in a fixed
     order). dyq, dyk: dL/dyq and dL/dyk in the dtype of q, with free strides. `want` limits
     the keys computed."""
-    index, args = _marshal(q, k, wq, wk, dyq, dyk, norm, eps, inv_freq, positions)
     like = {"dq": q, "dk": k, "dwq": wq, "dwk": wk}
     if not set(want) <= set(like):
         raise ValueError(f"want holds unknown gradients {sorted(set(want) - set(like))}")
-    grads, out = VscanQkNormGrads(), {}
-    grads.dyq, grads.dyk = dyq.data_ptr(), dyk.data_ptr()
-    for name in want:
-        t = like[name]
-        if t is not None:
-            out[name] = fresh(t)
-            setattr(grads, name, out[name].data_ptr())
-    workspace = None
-    if "dwq" in out or "dwk" in out:
-        need = ctypes.c_uint64()
-        check(_abi.qknorm_backward_workspace_size.fn(args, ctypes.byref(need)))
-        workspace = q.new_empty(need.value, dtype=torch.uint8)
-        grads.workspace, grads.workspace_bytes = workspace.data_ptr(), need.value
-    with on_device(index):
-        check(_abi.qknorm_backward.fn(args, ctypes.byref(grads), stream_handle(stream, index, workspace, *out.values())))
+    index, code = device_index(q)
+    with launching(stream, index):
+        args = _marshal(index, code, q, k, wq, wk, dyq, dyk, norm, eps, inv_freq, positions)
+        grads, out = VscanQkNormGrads(), {}
+        grads.dyq, grads.dyk = dyq.data_ptr(), dyk.data_ptr()
+        for name in want:
+            t = like[name]
+            if t is not None:
+                out[name] = fresh(t)
+                setattr(grads, name, out[name].data_ptr())
+        if "dwq" in out or "dwk" in out:
+            need = ctypes.c_uint64()
+            check(_abi.qknorm_backward_workspace_size.fn(args, ctypes.byref(need)))
+            workspace = q.new_empty(need.value, dtype=torch.uint8)
+            grads.workspace, grads.workspace_bytes = workspace.data_ptr(), need.value
+        check(_abi.qknorm_backward.fn(args, ctypes.byref(grads), torch._C._cuda_getCurrentRawStream(index)))
+    if stream is not None:
+        hand_over(stream, index, *out.values())
     return out
