@@ -344,7 +344,18 @@ vscan_status vscan_delta_backward(const vscan_route* route, const vscan_delta_ar
     auto zero = [&](void* ptr, size_t bytes) {
         if (ptr && bytes && e == cudaSuccess) e = cudaMemsetAsync(ptr, 0, bytes, s);
     };
+    // every token row's gradients, for rows that no step visits
+    auto zero_rows = [&] {
+        const size_t el_bytes = vscan_host::elem_bytes(args->dtype);
+        const size_t rows = (size_t)(args->seq_offsets ? 1 : args->batch) * args->tokens;
+        zero(grads->dq, rows * args->heads_k * args->dim_k * el_bytes);
+        zero(grads->dk, rows * args->heads_k * args->dim_k * el_bytes);
+        zero(grads->dv, rows * args->heads_v * args->dim_v * el_bytes);
+        zero(grads->da, rows * args->heads_v * el_bytes);
+        zero(grads->db, rows * args->heads_v * el_bytes);
+    };
     if (none) {  // no step: the state's gradient passes through
+        zero_rows();  // packed rows without a sequence; otherwise there are none
         zero(grads->dA, (size_t)args->heads_v * 4);
         zero(grads->dbias, (size_t)args->heads_v * 4);
         const size_t bytes = (size_t)args->batch * args->heads_v * args->dim_k * args->dim_v * 4;
@@ -376,14 +387,7 @@ vscan_status vscan_delta_backward(const vscan_route* route, const vscan_delta_ar
     p.da = grads->da; p.db = grads->db;
     p.dA = grads->dA; p.dbias = grads->dbias;
     if (args->seq_offsets || (route && route->g.kind == vscan::RK_ATROUS2)) {
-        // rows without a step, and chunk slots without a chunk
-        const size_t el_bytes = vscan_host::elem_bytes(args->dtype);
-        const size_t rows = (size_t)(args->seq_offsets ? 1 : args->batch) * args->tokens;
-        zero(grads->dq, rows * args->heads_k * args->dim_k * el_bytes);
-        zero(grads->dk, rows * args->heads_k * args->dim_k * el_bytes);
-        zero(grads->dv, rows * args->heads_v * args->dim_v * el_bytes);
-        zero(grads->da, rows * args->heads_v * el_bytes);
-        zero(grads->db, rows * args->heads_v * el_bytes);
+        zero_rows();  // rows without a step, and chunk slots without a chunk
         zero(p.wpart, (size_t)p.slots * p.heads_v * 8);
         if (p.wdq) zero(p.wdq, l.grad_total - l.dq);
         if (e != cudaSuccess) return cuda_fail(e, "vscan_delta_backward");
