@@ -167,18 +167,22 @@ __device__ __forceinline__ void mbar_arrive(uint32_t mbar)
 // Named barriers: some threads only arrive, the others wait for them.
 __device__ __forceinline__ void bar_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;\n" ::"r"(id), "r"(threads) : "memory"); }
 __device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory"); }
-// Wait for a phase, at most about a second in all (each try sleeps for up to 1000 ns): after that `dead` is set, this and
-// every later wait of the CTA returns at once, and the kernel runs to its end with
-// invalid results instead of hanging.
+// Tries until `ready` says so, TC_WAIT_TRIES times at most. Then `dead` is set: the CTA's other waits give
+// up within 256 tries, every later one after its first, and the kernel runs to its end with invalid
+// results instead of hanging.
 constexpr int TC_WAIT_TRIES = 1 << 20;
-__device__ __forceinline__ void mbar_wait(uint32_t mbar, uint32_t parity, volatile int* dead)
+template <typename READY>
+__host__ __device__ __forceinline__ void tc_bounded_wait(READY ready, volatile int* dead)
 {
     int i = 0;
-    while (i < TC_WAIT_TRIES && !mbar_test(mbar, parity)) {
-        ++i;
-        if ((i & 255) == 0 && *dead) i = TC_WAIT_TRIES;
-    }
+    while (i < TC_WAIT_TRIES && !ready())  // looks at `dead` after the first try and every 256th
+        i = (i & 255) == 0 && *dead ? TC_WAIT_TRIES : i + 1;
     if (i == TC_WAIT_TRIES) *dead = 1;
+}
+// Wait for a phase, at most about a second in all: each try sleeps for up to 1000 ns.
+__device__ __forceinline__ void mbar_wait(uint32_t mbar, uint32_t parity, volatile int* dead)
+{
+    tc_bounded_wait([&] { return mbar_test(mbar, parity); }, dead);
     __syncwarp();
 }
 
