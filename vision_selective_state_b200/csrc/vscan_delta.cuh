@@ -955,7 +955,7 @@ __device__ __forceinline__ void walk_end(WalkShared* w, uint32_t tm, int* status
     __syncthreads();
     start_next();
     if (threadIdx.x == 0 && status && w->dead) atomicOr(status, DEV_STATUS_TIMEOUT);
-    if (threadIdx.x < 32) tc_free(tm);
+    if (threadIdx.x < 32) tc_free(tm, &w->dead);
 }
 
 // The copying warps' part: chunk n of `chunks` into stage n mod STAGES. `in` returns the bytes of

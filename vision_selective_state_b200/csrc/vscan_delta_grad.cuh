@@ -818,7 +818,7 @@ __global__ void __launch_bounds__(DG_THREADS, 1) delta_grad_kernel(const DeltaPa
     tc_fence_before();
     __syncthreads();
     if (tid == 0 && p.status && sh->dead) atomicOr(p.status, DEV_STATUS_TIMEOUT);
-    if (warp == 0) tc_free(tm);
+    if (warp == 0) tc_free(tm, &sh->dead);
 }
 
 // dA and dbias of one head: its chunks' sums added in a fixed order.

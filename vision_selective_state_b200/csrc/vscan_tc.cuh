@@ -73,8 +73,13 @@ __device__ __forceinline__ void tc_alloc(uint32_t smem_out)  // one warp; all 51
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_out) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
 }
-__device__ __forceinline__ void tc_free(uint32_t addr)
+// At the end of a kernel, by one warp, behind a barrier of the block. Where a wait gave up, products and copies
+// into shared memory may still be on their way: they get a millisecond to end before the block gives its memory back.
+__device__ __forceinline__ void tc_free(uint32_t addr, const volatile int* dead)
 {
+    if (*dead)
+#pragma unroll 1
+        for (int i = 0; i < 1000; ++i) __nanosleep(1000);
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(addr));
 }
 
