@@ -128,10 +128,22 @@ def _row_strides(name, t, dense):
     return tok, (t.stride(0) if b > 1 else n * tok)
 
 
-def _fields(index, code, q, k, v, a, b, A, bias, y, direction, seq_offsets, scale, beta_scale, initial_state, final_state):
-    """Fields of vscan_delta_args up to the strides."""
+def _rows(q, v, seq_offsets):
+    """Images, or packed sequences."""
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q and k are [batch, tokens, heads_k, dim_k], v is [batch, tokens, heads_v, dim_v]")
+    if seq_offsets is None:
+        return q.shape[0]
+    if q.shape[0] != 1:
+        raise ValueError("packed sequences have one row of tokens: batch must be 1")
+    if seq_offsets.dim() != 1 or seq_offsets.numel() < 1:
+        raise ValueError("seq_offsets must hold one more element than there are sequences")
+    return seq_offsets.numel() - 1
+
+
+def _fields(index, code, rows, q, k, v, a, b, A, bias, y, direction, seq_offsets, scale, beta_scale, initial_state,
+            final_state):
+    """Fields of vscan_delta_args up to the strides."""
     dtype, shape = q.dtype, q.shape
     batch, tokens, hk, dk = shape
     hv, dv = v.shape[2:]
@@ -140,18 +152,12 @@ def _fields(index, code, q, k, v, a, b, A, bias, y, direction, seq_offsets, scal
     check_tensor("v", v, (batch, tokens, hv, dv), dtype, index)
     check_tensor("a", a, heads, dtype, index)
     check_tensor("b", b, heads, dtype, index)
-    check_tensor("y", y, v.shape, dtype, index)
+    check_tensor("y (dy)", y, v.shape, dtype, index)
     check_dense("A", A, (hv,), torch.float32, index)
     if bias is not None:
         check_dense("bias", bias, (hv,), torch.float32, index)
-    rows = batch
     if seq_offsets is not None:
-        if batch != 1:
-            raise ValueError("packed sequences have one row of tokens: batch must be 1")
-        if seq_offsets.dim() != 1 or seq_offsets.numel() < 1:
-            raise ValueError("seq_offsets must hold one more element than there are sequences")
         check_dense("seq_offsets", seq_offsets, seq_offsets.shape, torch.int32, index)
-        rows = seq_offsets.numel() - 1
     if initial_state is not None:
         check_dense("initial_state", initial_state, (rows, hv, dk, dv), torch.float32, index)
     if final_state is not None:
@@ -161,7 +167,7 @@ def _fields(index, code, q, k, v, a, b, A, bias, y, direction, seq_offsets, scal
         q.data_ptr(), k.data_ptr(), v.data_ptr(), a.data_ptr(), b.data_ptr(), y.data_ptr(), A.data_ptr(),
         0 if bias is None else bias.data_ptr(), 0 if initial_state is None else initial_state.data_ptr(),
         0 if final_state is None else final_state.data_ptr(), 0 if seq_offsets is None else seq_offsets.data_ptr(),
-        dk ** -0.5 if scale is None else scale, beta_scale,
+        (dk and dk ** -0.5) if scale is None else scale, beta_scale,  # a width of 0 is refused by the library
         *head_strides("q", q, q.is_contiguous()), *head_strides("k", k, k.is_contiguous()),
         *head_strides("v", v, v.is_contiguous()), *_row_strides("a", a, a.is_contiguous()),
         *_row_strides("b", b, b.is_contiguous()), *head_strides("y", y, y.is_contiguous()))
@@ -189,8 +195,8 @@ def _partial(route, seq_offsets):
     return seq_offsets is not None or (route is not None and route.kind == ROUTES["atrous2"])
 
 
-def _state_shape(q, v, seq_offsets):
-    return (q.shape[0] if seq_offsets is None else seq_offsets.numel() - 1, v.shape[2], q.shape[3], v.shape[3])
+def _state_shape(rows, q, v):
+    return rows, v.shape[2], q.shape[3], v.shape[3]
 
 
 def _scratch(given, query, handle, fields, q, index):
@@ -218,15 +224,16 @@ def delta_forward(q, k, v, a, b, A, bias=None, *, route=None, direction=0, seq_o
     status: as in forward().
     """
     index, code = device_index(q)
+    rows = _rows(q, v, seq_offsets)
     with launching(stream, index):
         if out is None:
             out = v.new_zeros(v.shape) if _partial(route, seq_offsets) else fresh(v)
         if final_state is True:
-            final_state = q.new_empty(_state_shape(q, v, seq_offsets), dtype=torch.float32)
+            final_state = q.new_empty(_state_shape(rows, q, v), dtype=torch.float32)
         elif final_state is False:
             final_state = None
-        fields = _fields(index, code, q, k, v, a, b, A, bias, out, direction, seq_offsets, scale, beta_scale, initial_state,
-                         final_state)
+        fields = _fields(index, code, rows, q, k, v, a, b, A, bias, out, direction, seq_offsets, scale, beta_scale,
+                         initial_state, final_state)
         handle = _route_handle(route)
         scratch, *where = _scratch(workspace, _abi.delta_workspace_size, handle, fields, q, index)
         args = _pack(*fields, *where, _status(status, index))
@@ -252,9 +259,10 @@ def delta_backward(q, k, v, a, b, A, bias=None, *, dy, route=None, direction=0, 
     if want is not None and not set(want) <= set(GRADIENTS):
         raise ValueError(f"want holds unknown gradients {sorted(set(want) - set(GRADIENTS))}")
     index, code = device_index(q)
+    rows = _rows(q, v, seq_offsets)
     with launching(stream, index):
-        fields = _fields(index, code, q, k, v, a, b, A, bias, dy, direction, seq_offsets, scale, beta_scale, initial_state,
-                         None)
+        fields = _fields(index, code, rows, q, k, v, a, b, A, bias, dy, direction, seq_offsets, scale, beta_scale,
+                         initial_state, None)
         grads, out = VscanDeltaGrads(), {}
         like = {"dq": q, "dk": k, "dv": v, "da": a, "db": b, "dA": A, "dbias": A, "d_initial_state": initial_state}
         for name in GRADIENTS if want is None else want:
@@ -263,7 +271,7 @@ def delta_backward(q, k, v, a, b, A, bias=None, *, dy, route=None, direction=0, 
                 out[name] = fresh(t)
                 setattr(grads, name, out[name].data_ptr())
         if d_final_state is not None:
-            check_dense("d_final_state", d_final_state, _state_shape(q, v, seq_offsets), torch.float32, index)
+            check_dense("d_final_state", d_final_state, _state_shape(rows, q, v), torch.float32, index)
             grads.d_final_state = d_final_state.data_ptr()
         handle = _route_handle(route)
         scratch, grads.workspace, grads.workspace_bytes = _scratch(workspace, _abi.delta_backward_workspace_size, handle,
@@ -323,7 +331,7 @@ def delta_step(q, k, v, a, b, A, bias=None, *, state, state_out=None, scale=None
                     strides += (0, _row_strides(name, t.unsqueeze(1), False)[1])
         args = _pack(batch, 1, hk, hv, dk, dv, code, 0, q.data_ptr(), k.data_ptr(), v.data_ptr(), a.data_ptr(), b.data_ptr(),
                      out.data_ptr(), A.data_ptr(), 0 if bias is None else bias.data_ptr(), state.data_ptr(),
-                     state_out.data_ptr(), 0, dk ** -0.5 if scale is None else scale, beta_scale, *strides, 0, 0, 0)
+                     state_out.data_ptr(), 0, (dk and dk ** -0.5) if scale is None else scale, beta_scale, *strides, 0, 0, 0)
         check(_abi.delta_step.fn(args, torch._C._cuda_getCurrentRawStream(index)))
     if stream is not None:
         hand_over(stream, index, out, state_out)
