@@ -424,9 +424,10 @@ vscan_status vscan_status_from_device_word(int32_t word);
  * heads. Keys of length at most 1 (vscan_qknorm_forward with VSCAN_NORM_L2) and
  * beta <= 1 keep the update contractive. States are float32; the products run on
  * bf16 tensor cores with every float32 operand split into three bf16 terms, so
- * states and float32 results keep float32 accuracy. Values must be finite: a
- * non-finite value in one token can reach the other tokens of its chunk of 64 steps
- * (never an earlier chunk).
+ * states, gradients and float32 results keep float32 accuracy; a bf16 y takes two
+ * terms in its last product, whose error is a few thousandths of y's rounding.
+ * Values must be finite: a non-finite value in one token can reach the other tokens
+ * of its chunk of 64 steps (never an earlier chunk).
  */
 typedef struct vscan_delta_args {
     int32_t batch;       /* images, >= 0; with seq_offsets: packed sequences         */
@@ -475,7 +476,8 @@ typedef struct vscan_delta_args {
     uint64_t workspace_bytes;
     int32_t* status;     /* device int32 or NULL: kernels OR in 2 when an internal
                             wait gave up (outputs invalid) and never trap; decode
-                            with vscan_status_from_device_word                       */
+                            with vscan_status_from_device_word. With NULL such a
+                            call's outputs carry no sign of it                       */
 } vscan_delta_args;
 
 /*
@@ -611,7 +613,8 @@ typedef struct vscan_qknorm_args {
  */
 vscan_status vscan_qknorm_forward(const vscan_qknorm_args* args, void* stream);
 
-/* Gradients of vscan_qknorm_forward, written (not accumulated). Any output may be NULL. */
+/* Gradients of vscan_qknorm_forward, written (not accumulated). Any output may be NULL. A row
+ * of zeros with eps = 0 has no gradient: NaN, in dwq and dwk as well. */
 typedef struct vscan_qknorm_grads {
     const void* dyq;     /* device, dL/dyq at yq's strides, 16-byte aligned          */
     const void* dyk;     /* device, dL/dyk at yk's strides, 16-byte aligned          */

@@ -23,10 +23,15 @@
 // accumulation. A bf16 input is exact there; every float32 operand (the state,
 // W, T, P) is split into three bf16 terms of 8 bits each (x = x0 + x1 + x2) and
 // the products of total order up to 2 are summed, so that states and gradients
-// keep float32 accuracy: one term alone would leave 2^-9 and two 2^-17 in a carried
-// state. The one product whose result leaves in bf16 at once, W P in y, has two
-// terms of each (2^-17 before a rounding of 2^-9). The state itself is float32
-// throughout, in registers, and is only ever added to with rounding.
+// keep float32 accuracy: one cut term alone would leave up to 2^-7 and two 2^-15 in a
+// carried state. The one product whose result leaves in bf16 at once, W P in y, has two
+// terms of each, rounded: 2^-17 of each operand, and 2^-16 for the product of both second
+// terms that is left out, so at most 2^-15 of sum_j |P_ij w_j| before the rounding of y,
+// which is 2^-8 of y. By the rms it is 4.4e-6 of y, against the rounding's 1.65e-3, and y is as
+// far from float64 (to four digits) with three terms. Those cost 206 -> 214 us at 56x56 (16
+// images, 3 heads of 64 x 64), 156 -> 167 us for 24 packed sequences and 1390 -> 1480 us at
+// 64x64 + CLS (64 images, 6 heads of 128 x 128). The state itself is float32 throughout, in
+// registers, and is only ever added to with rounding.
 //
 // Measured on one B200 (one kernel at a time): 64 images of 4097 tokens, 6 heads of 128 x 128,
 // bf16: triangles 545 us, walk 768 us; 16 images of 56x56, 3 heads of 64 x 64: 52 and 150 us; one
@@ -811,7 +816,7 @@ __device__ __forceinline__ void walk_store(T* dst, long long tok, const int* row
 }
 
 // NT bf16 terms of 32 values of a row, term n in the 16 columns from addr + n * step on. Three
-// are cut (exact); one or two are rounded (2^-18 for two, cut ones would leave 2^-16), unless
+// are cut (exact); one or two are rounded (2^-17 for two, cut ones would leave 2^-15), unless
 // CUT says that more follow elsewhere.
 template <int NT, bool CUT = NT == 3>
 __device__ __forceinline__ void put_terms(uint32_t addr, int step, float (&v)[32])

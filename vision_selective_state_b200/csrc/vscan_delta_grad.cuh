@@ -267,7 +267,8 @@ __global__ void __launch_bounds__(DW_THREADS, 1) delta_rscan_kernel(const DeltaP
 // values) and waiting for them 10,000, E and M 2,400, the scaled results with their part of dg
 // 3,200. Sixteen computing warps instead of eight: 57 -> 44 us for 3 float32 images of 777 tokens
 // (dk 48, dv 80), 31 us instead of 35 for 8 bf16 ones of 197, and no change at 128 x 128, where
-// the tensor core and the loads bound the slabs.
+// the tensor core and the loads bound the slabs. 544 threads leave 96 registers each, too few for
+// all pieces fetched ahead: 4 and 84 bytes a thread spill in bf16 (DKP 64, 128), 52 and 140 in float32.
 constexpr int DG_COMPUTE = 512, DG_THREADS = 544;  // sixteen warps and one that issues the products
 
 template <typename T> struct GradRaw;  // four values of dy

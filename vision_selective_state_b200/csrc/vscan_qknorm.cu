@@ -17,10 +17,12 @@ using vscan_host::fail;
 using vscan_host::launch_after;
 using vscan_host::NvtxRange;
 
-// CTAs of q and as many of k. Forward two rounds of the four CTAs of 256 threads that an SM holds,
-// backward one round (a CTA's sums for the weights' gradients are paid once): 64 images of 4097 tokens,
-// 6 + 6 heads of 128, bf16: 306 us (one round: 318); gradients of 16 images of 3136 tokens, heads of 72:
-// 135 us (262 CTAs a side: 154; 370: 147; 740: 155).
+// CTAs of q and as many of k. Forward two rounds of the four CTAs of 256 threads that an SM holds: 64
+// images of 4097 tokens, 6 + 6 heads of 128, bf16: 308 us (one round: 318). Backward half as many, since
+// every CTA pays for its sums of the weights' gradients; the kernel's 70 to 80 registers let three CTAs
+// share an SM, so that 444 of the 592 run at once, and those of the side with fewer heads end early.
+// The best of what was measured on 16 images of 3136 tokens, 12 + 4 heads of 72: 136 us (262 CTAs a
+// side: 154; 370: 147; 740: 155).
 int most_blocks(bool back) { return 148 * (back ? 2 : 4); }
 
 vscan_status check_stride(const char* name, int64_t tok, int64_t img, int64_t width, int vec)

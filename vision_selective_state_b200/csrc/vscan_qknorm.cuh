@@ -14,11 +14,15 @@
 // exchange but the sum of squares. A CTA takes one position of q or of k and turns
 // its images and heads by one set of angles: sines and cosines are computed once a
 // position, from float64 angles (a float32 product is off by whole radians at
-// positions of 2^24). Two rows a lane are in flight, and weights wait in shared
-// memory, for more CTAs an SM. On 64 images of 4097 tokens, 6 + 6 heads of 128, bf16,
-// forward: 306 us, 5.3 TB/s, 80 % of the copy rate, the issue slots half used (329 us with
-// scalar products and a division for every row's head). Gradients of 16 images of 3136 tokens,
-// heads of 72: 135 us.
+// positions of 2^24). Two rows a lane are in flight where a row takes one unit a lane
+// (one row where the registers end: gradients at V = 8, rows of several units a lane), and
+// weights wait in shared memory, for more CTAs an SM. Registers are capped at 64 forward and
+// 80 backward; at V = 8 the forward pass spills 48 bytes a thread there, at V = 4 the passes
+// 8 to 24. On 64 images of 4097 tokens, 6 + 6 heads of 128, bf16, forward: 308 us, 5.2 TB/s, 80 %
+// of the copy rate, the issue slots half used (329 us with scalar products and a division for
+// every row's head). Gradients of 16 images of 3136 tokens, 12 + 4 heads of 72: 136 us, 2.5
+// times their bytes: 72 channels fill five of a row's eight lanes, q's CTAs have three times the
+// rows of k's, and one row a lane is in flight.
 #pragma once
 
 #include <cuda_bf16.h>

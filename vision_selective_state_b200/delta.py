@@ -219,9 +219,11 @@ def delta_forward(q, k, v, a, b, A, bias=None, *, route=None, direction=0, seq_o
     ATROUS2 Route (an ATROUS2 direction writes its own group's tokens only); without a route,
     first to last. seq_offsets: int32 [n + 1] on the device for n packed sequences in one row
     of tokens (batch 1); rows outside every sequence are left as they are. Rows that a call
-    leaves are 0 in an output made here. scale: dim_k ** -0.5 if None. final_state: True, or a
-    tensor to write the state after the last token to (initial_state itself is allowed).
-    status: as in forward().
+    leaves are 0 in an output made here; one given as `out` must not overlap the inputs. scale:
+    dim_k ** -0.5 if None. final_state: True, or a tensor to write the state after the last token
+    to (initial_state itself is allowed). status: an int32 device word, zeroed by the caller, that
+    tells of an internal wait that gave up; decode it with status_from_device_word. Without one
+    nothing tells such a call's invalid outputs from good ones.
     """
     index, code = device_index(q)
     rows = _rows(q, v, seq_offsets)
@@ -254,7 +256,7 @@ def delta_backward(q, k, v, a, b, A, bias=None, *, dy, route=None, direction=0, 
 
     Keys: dq, dk, dv, da, db (dense, in the dtype of q), dA, dbias and, with initial_state,
     d_initial_state (float32). `want` limits the keys computed. Tokens that no step visits get
-    zeros. Equal calls give equal bits.
+    zeros. Equal calls give equal bits. status: as in delta_forward.
     """
     if want is not None and not set(want) <= set(GRADIENTS):
         raise ValueError(f"want holds unknown gradients {sorted(set(want) - set(GRADIENTS))}")
@@ -289,7 +291,7 @@ def delta_step(q, k, v, a, b, A, bias=None, *, state, state_out=None, scale=None
     """One token of each of a batch of sequences (vscan_delta_step). Returns (y, new state).
 
     q, k: [batch, heads_k, dim_k]; v, y: [batch, heads_v, dim_v]; a, b: [batch, heads_v].
-    The new state goes to state_out, or in place to state.
+    The new state goes to state_out, or in place to state. `out` must not overlap the inputs.
     """
     index, code = device_index(q)
     if q.dim() != 3 or v.dim() != 3:

@@ -66,7 +66,8 @@ def _marshal(index, code, q, k, wq, wk, yq, yk, norm, eps, inv_freq, positions):
 
 def qk_norm(q, k, wq=None, wk=None, *, norm="rms", eps=1e-6, inv_freq=None, positions=None, out=None, stream=None):
     """Normalised ("l2": unit length, "rms": unit mean square), weighted and rotated (yq, yk)
-    (vscan_qknorm_forward). out: a pair of tensors to write to; (q, k) itself works in place."""
+    (vscan_qknorm_forward). out: a pair of tensors to write to, each either its own input (in
+    place) or memory that overlaps no input."""
     index, code = device_index(q)
     with launching(stream, index):
         if out is None:
